@@ -260,6 +260,62 @@ int inkling_dense_mlp_workspace_size(const inkling_dense_dims_t* dims, size_t* b
 int inkling_dense_mlp_forward(const inkling_dense_dims_t* dims, const void* x, const void* gate_up, const void* down,
                               float global_scale, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Products grouped by expert, with any number of rows each: the expert
+ * projections on their own, for callers with another activation between them,
+ * frozen or adapted experts, or rows that arrive from other GPUs.  The rows
+ * offsets[e] <= r < offsets[e + 1] belong to expert e (inkling_moe_route's
+ * expert_offsets are such offsets, and row r of its order is token
+ * sorted_slots[r] / top_k):
+ *   linear       out[r]  = weight[e] . x[row_index[r]]
+ *   input_grad   dx[r]   = weight[e]^T . dout[r]
+ *   weight_grad  dweight[e] = sum over the rows of e of dout[r] (x) x[row_index[r]]
+ * with weight [n_groups][out_features][in_features] (nn.Linear layout), x
+ * [x_rows][in_features], out and dout [rows][out_features], dx
+ * [rows][in_features].  row_index [rows] int32 or NULL (row r reads x[r]; then
+ * x_rows must equal rows).  input_grad leaves the sum over rows that share an
+ * x row to the caller.
+ * offsets [n_groups + 1] int32 on the device, non-decreasing, the last at most
+ * `rows`.  Rows before offsets[0] and from offsets[n_groups] on are neither
+ * read nor written; an expert without rows is skipped, and its dweight is
+ * zeros.  Offsets that break this are clamped to [0, rows] and raised to the
+ * largest before them, and an index outside [0, x_rows) takes the nearest row
+ * inside: wrong values, never an access out of bounds.
+ * Operands in dtype, sums in fp32 (for INKLING_F32 fp32 products too), rounded
+ * once to out_dtype (out, dx or dweight); infinities and NaN propagate.  Each
+ * sum's order is fixed, so results are bit-reproducible.
+ * Limits (INKLING_ERR_UNSUPPORTED otherwise): in_features and out_features
+ * multiples of 8 up to 2^20, 1 <= n_groups <= 512, rows and x_rows at most
+ * 2^31 - 257, fewer than 2^31 output tiles.  Tensor pointers must be 16-byte
+ * aligned, offsets and row_index 4-byte; the output must not overlap an
+ * operand.  Same conventions and errors as inkling_moe_forward otherwise;
+ * rows == 0 is a no-op for the first two and writes zeros in weight_grad.
+ */
+typedef struct {
+    int64_t rows;          /* rows of out, dout, dx and row_index */
+    int64_t x_rows;        /* rows of x (input_grad: ignored)     */
+    int32_t n_groups;
+    int32_t in_features;
+    int32_t out_features;
+    int32_t dtype;         /* inkling_dtype_t of x, dout and weight */
+    int32_t out_dtype;     /* inkling_dtype_t of the result         */
+} inkling_grouped_dims_t;
+
+/* workspace of inkling_grouped_linear and inkling_grouped_input_grad */
+int inkling_grouped_workspace_size(const inkling_grouped_dims_t* dims, size_t* bytes);
+/* workspace of inkling_grouped_weight_grad; `gathered`: called with a row_index */
+int inkling_grouped_weight_grad_workspace_size(const inkling_grouped_dims_t* dims, int gathered, size_t* bytes);
+
+int inkling_grouped_linear(const inkling_grouped_dims_t* dims, const void* x, const int32_t* row_index,
+                           const void* weight, const int32_t* offsets, void* out, void* workspace,
+                           size_t workspace_bytes, void* stream);
+int inkling_grouped_input_grad(const inkling_grouped_dims_t* dims, const void* dout, const void* weight,
+                               const int32_t* offsets, void* dx, void* workspace, size_t workspace_bytes,
+                               void* stream);
+int inkling_grouped_weight_grad(const inkling_grouped_dims_t* dims, const void* dout, const void* x,
+                                const int32_t* row_index, const int32_t* offsets, void* dweight, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
 /* Stage timing (instrumentation for benchmarks).  When `events` is non-NULL,
  * each later inkling_moe_forward on the calling thread records, on its stream,
  * events[0] before the first launch and events[i] after stage i:

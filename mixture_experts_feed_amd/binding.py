@@ -29,7 +29,9 @@ EXPORTED = ("inkling_moe_workspace_size", "inkling_moe_route", "inkling_moe_forw
             "inkling_moe_strerror", "inkling_moe_last_hip_error", "inkling_moe_set_stage_events",
             "inkling_dense_mlp_workspace_size", "inkling_dense_mlp_forward",
             "inkling_moe_backward_workspace_size", "inkling_moe_backward", "inkling_moe_saved_size",
-            "inkling_moe_forward_train", "inkling_moe_forward_noalloc")
+            "inkling_moe_forward_train", "inkling_moe_forward_noalloc",
+            "inkling_grouped_workspace_size", "inkling_grouped_weight_grad_workspace_size",
+            "inkling_grouped_linear", "inkling_grouped_input_grad", "inkling_grouped_weight_grad")
 INKLING_STAGE_EVENTS = 7
 STAGES = ("router_logits", "router_select", "permutation", "gate_up", "down", "shared_down_combine")
 
@@ -49,6 +51,12 @@ class Grads(ctypes.Structure):
     _fields_ = [("d_gate_bank", ctypes.c_void_p), ("d_routed_gate_up", ctypes.c_void_p),
                 ("d_routed_down", ctypes.c_void_p), ("d_shared_gate_up", ctypes.c_void_p),
                 ("d_shared_down", ctypes.c_void_p), ("weight_grad_dtype", ctypes.c_int32)]
+
+
+class GroupedDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("x_rows", ctypes.c_int64), ("n_groups", ctypes.c_int32),
+                ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
 
 
 class Gate(ctypes.Structure):
@@ -126,6 +134,16 @@ def load() -> ctypes.CDLL:
                                               ctypes.POINTER(Experts), ctypes.c_void_p, ctypes.c_void_p,
                                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.inkling_moe_forward_train.restype = ctypes.c_int
+    ptr, size = ctypes.c_void_p, ctypes.c_size_t
+    gdims = ctypes.POINTER(GroupedDims)
+    for name, args in (
+            ("inkling_grouped_workspace_size", [gdims, ctypes.POINTER(size)]),
+            ("inkling_grouped_weight_grad_workspace_size", [gdims, ctypes.c_int, ctypes.POINTER(size)]),
+            ("inkling_grouped_linear", [gdims, ptr, ptr, ptr, ptr, ptr, ptr, size, ptr]),
+            ("inkling_grouped_input_grad", [gdims, ptr, ptr, ptr, ptr, ptr, size, ptr]),
+            ("inkling_grouped_weight_grad", [gdims, ptr, ptr, ptr, ptr, ptr, ptr, size, ptr])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_int
     _LIB = lib
     return lib
 
@@ -427,3 +445,152 @@ def backward(x: torch.Tensor, gate_bank: torch.Tensor, bias: torch.Tensor, w_gu:
     if rc != INKLING_OK:
         raise InklingError(rc, "inkling_moe_backward")
     return grads
+
+
+# ---- products grouped by expert -------------------------------------------------
+
+
+def _check(rc: int, where: str) -> None:
+    if rc != INKLING_OK:
+        raise InklingError(rc, where)
+
+
+def _same_device(dev, **tensors) -> None:
+    for n, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{n} must be on {dev}, got {t.device}")
+
+
+def make_grouped_dims(rows, x_rows, n_groups, in_features, out_features, dtype, out_dtype=None) -> GroupedDims:
+    code = dtype if isinstance(dtype, int) else _dtype_code(dtype)
+    ocode = code if out_dtype is None else (out_dtype if isinstance(out_dtype, int) else _dtype_code(out_dtype))
+    return GroupedDims(int(rows), int(x_rows), int(n_groups), int(in_features), int(out_features), code, ocode)
+
+
+def grouped_workspace_size(dims: GroupedDims) -> int:
+    """inkling_grouped_workspace_size (grouped_linear, grouped_input_grad)."""
+    n = ctypes.c_size_t(0)
+    _check(load().inkling_grouped_workspace_size(ctypes.byref(dims), ctypes.byref(n)),
+           "inkling_grouped_workspace_size")
+    return int(n.value)
+
+
+def grouped_weight_grad_workspace_size(dims: GroupedDims, gathered: bool = False) -> int:
+    """inkling_grouped_weight_grad_workspace_size; `gathered`: called with a row_index."""
+    n = ctypes.c_size_t(0)
+    _check(load().inkling_grouped_weight_grad_workspace_size(ctypes.byref(dims), int(gathered), ctypes.byref(n)),
+           "inkling_grouped_weight_grad_workspace_size")
+    return int(n.value)
+
+
+def _grouped_checks(rows_name, src, weight, offsets, width, row_index):
+    """Checks shared by the row products; returns (rows, E, N, K)."""
+    if src.dim() != 2 or weight.dim() != 3:
+        raise ValueError(f"{rows_name} must be [rows, features] and weight [n_groups, out_features, in_features]")
+    _need(src, rows_name, weight.dtype)
+    _need(weight, "weight")
+    E, N, K = weight.shape
+    if src.shape[1] != width:
+        raise ValueError(f"{rows_name} must have {width} columns, got {src.shape[1]}")
+    _grouped_plan_checks(offsets, E, row_index)
+    _same_device(src.device, weight=weight, offsets=offsets, row_index=row_index)
+    return (src.shape[0] if row_index is None else row_index.shape[0]), E, N, K
+
+
+def _grouped_plan_checks(offsets, n_groups, row_index):
+    _need(offsets, "offsets", torch.int32)
+    if offsets.dim() != 1 or offsets.shape[0] != n_groups + 1:
+        raise ValueError("offsets must hold n_groups + 1 values")
+    if row_index is not None:
+        _need(row_index, "row_index", torch.int32)
+        if row_index.dim() != 1:
+            raise ValueError("row_index must be one-dimensional")
+
+
+def _result(t, name, shape, dtype, dev):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _same_device(dev, **{name: t})
+    return t
+
+
+def _scratch(workspace, need, dev):
+    if workspace is None:
+        return torch.empty(max(1, need), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8)
+    _same_device(dev, workspace=workspace)
+    return workspace
+
+
+def grouped_linear(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
+                   row_index: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   out_dtype: Optional[torch.dtype] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """inkling_grouped_linear: out[r] = weight[e] x[row_index[r]] for the rows
+    offsets[e] <= r < offsets[e + 1].  x [rows, K] (with row_index [rows] int32:
+    any number of rows), weight [E, N, K], offsets [E + 1] int32 on the device;
+    out [rows, N].  Rows outside the groups are left as they are (in an `out`
+    made here: unset)."""
+    R, E, N, K = _grouped_checks("x", x, weight, offsets, weight.shape[-1], row_index)
+    dev = x.device
+    out_dtype = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
+    dims = make_grouped_dims(R, x.shape[0], E, K, N, x.dtype, out_dtype)
+    out = _result(out, "out", (R, N), out_dtype, dev)
+    with torch.cuda.device(dev):
+        ws = _scratch(workspace, grouped_workspace_size(dims), dev)
+        _check(load().inkling_grouped_linear(ctypes.byref(dims), x.data_ptr(), _ptr(row_index), weight.data_ptr(),
+                                             offsets.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(),
+                                             _stream(dev)), "inkling_grouped_linear")
+    return out
+
+
+def grouped_input_grad(dout: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
+                       dx: Optional[torch.Tensor] = None, dx_dtype: Optional[torch.dtype] = None,
+                       workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """inkling_grouped_input_grad: dx[r] = weight[e]^T dout[r], [rows, K]; with a
+    row_index in the forward, the rows of one x row are for the caller to sum."""
+    R, E, N, K = _grouped_checks("dout", dout, weight, offsets, weight.shape[1], None)
+    dev = dout.device
+    dx_dtype = dx.dtype if dx is not None else dout.dtype if dx_dtype is None else dx_dtype
+    dims = make_grouped_dims(R, R, E, K, N, dout.dtype, dx_dtype)
+    dx = _result(dx, "dx", (R, K), dx_dtype, dev)
+    with torch.cuda.device(dev):
+        ws = _scratch(workspace, grouped_workspace_size(dims), dev)
+        _check(load().inkling_grouped_input_grad(ctypes.byref(dims), dout.data_ptr(), weight.data_ptr(),
+                                                 offsets.data_ptr(), dx.data_ptr(), ws.data_ptr(), ws.numel(),
+                                                 _stream(dev)), "inkling_grouped_input_grad")
+    return dx
+
+
+def grouped_weight_grad(dout: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
+                        row_index: Optional[torch.Tensor] = None, dweight: Optional[torch.Tensor] = None,
+                        weight_grad_dtype: Optional[torch.dtype] = None,
+                        workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """inkling_grouped_weight_grad: dweight[e] = sum over the rows of e of
+    dout[r] (x) x[row_index[r]], [E, N, K]: fp32 (default) or bf16
+    (`weight_grad_dtype`, or the dtype of the given `dweight`)."""
+    if dout.dim() != 2 or x.dim() != 2:
+        raise ValueError("dout and x must be [rows, features]")
+    _need(dout, "dout", x.dtype)
+    _need(x, "x")
+    E = offsets.shape[0] - 1 if offsets.dim() == 1 else 0
+    _grouped_plan_checks(offsets, E, row_index)
+    R, N = dout.shape
+    K = x.shape[1]
+    if (x if row_index is None else row_index).shape[0] != R:
+        raise ValueError("dout must have a row for each row of x, or for each entry of row_index")
+    dev = dout.device
+    _same_device(dev, x=x, offsets=offsets, row_index=row_index)
+    wdt = dweight.dtype if dweight is not None else torch.float32 if weight_grad_dtype is None else weight_grad_dtype
+    if weight_grad_dtype is not None and weight_grad_dtype != wdt:
+        raise ValueError("weight_grad_dtype differs from the dtype of the given dweight")
+    dims = make_grouped_dims(R, x.shape[0], E, K, N, x.dtype, wdt)
+    dweight = _result(dweight, "dweight", (E, N, K), wdt, dev)
+    with torch.cuda.device(dev):
+        ws = _scratch(workspace, grouped_weight_grad_workspace_size(dims, row_index is not None), dev)
+        _check(load().inkling_grouped_weight_grad(ctypes.byref(dims), dout.data_ptr(), x.data_ptr(), _ptr(row_index),
+                                                  offsets.data_ptr(), dweight.data_ptr(), ws.data_ptr(), ws.numel(),
+                                                  _stream(dev)), "inkling_grouped_weight_grad")
+    return dweight

@@ -2,6 +2,7 @@
 // layout and the launch sequence (router -> permutation -> grouped GEMMs).
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -677,6 +678,168 @@ int inkling_moe_backward(const inkling_moe_dims_t* dims, const void* x, const in
     wg.out_s = g->d_shared_gate_up;
     wg.counters = p.round_counters + 32;
     HIP_TRY(launch_wgrad(wg, s));
+    return INKLING_OK;
+}
+
+}  // extern "C"
+
+// ---- products grouped by expert -------------------------------------------------
+namespace {
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+int check_grouped_dims(const inkling_grouped_dims_t* d) {
+    if (d == nullptr) return INKLING_ERR_INVALID_ARGUMENT;
+    if (d->rows < 0 || d->x_rows < 0 || d->n_groups <= 0 || d->in_features <= 0 || d->out_features <= 0)
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (d->dtype != INKLING_F32 && d->dtype != INKLING_BF16) return INKLING_ERR_UNSUPPORTED;
+    if (d->out_dtype != INKLING_F32 && d->out_dtype != INKLING_BF16) return INKLING_ERR_UNSUPPORTED;
+    if (d->in_features % 8 != 0 || d->out_features % 8 != 0 || d->in_features > (1 << 20) ||
+        d->out_features > (1 << 20) || d->n_groups > 512)
+        return INKLING_ERR_UNSUPPORTED;
+    if (d->rows > INT32_MAX - 256 || d->x_rows > INT32_MAX - 256) return INKLING_ERR_UNSUPPORTED;
+    return INKLING_OK;
+}
+
+struct GroupedLayout {
+    size_t offs, counters, num_tiles, tiles, x_sorted, total;
+};
+
+// row_tiles: entries of the tile list; gather_bytes: rows of x in row order
+GroupedLayout make_grouped_layout(const inkling_grouped_dims_t* d, size_t row_tiles, size_t gather_bytes) {
+    GroupedLayout L = {};
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        size_t at = o;
+        o = align_up(o + bytes);
+        return at;
+    };
+    L.offs = take(((size_t)d->n_groups + 1) * 4);
+    L.counters = take(kRoundCounters * 4);
+    L.num_tiles = take(4);
+    L.tiles = take(row_tiles * sizeof(RoutedTile));
+    L.x_sorted = take(gather_bytes);
+    L.total = o;
+    return L;
+}
+
+// the larger tile list of the two row products
+size_t grouped_row_tiles(const inkling_grouped_dims_t* d) {
+    const int rows = (int)d->rows, E = d->n_groups;
+    return (size_t)std::max(group_max_row_tiles(rows, E, group_cfg(rows, E, false)),
+                            group_max_row_tiles(rows, E, group_cfg(rows, E, true)));
+}
+
+size_t grouped_gather_bytes(const inkling_grouped_dims_t* d) {
+    return (size_t)d->rows * d->in_features * (d->dtype == INKLING_BF16 ? 2 : 4);
+}
+
+GroupParams grouped_params(const inkling_grouped_dims_t* d, const GroupedLayout& L, void* ws, bool input_grad) {
+    GroupParams p = {};
+    p.dtype = d->dtype == INKLING_BF16 ? 1 : 0;
+    p.out_bf16 = d->out_dtype == INKLING_BF16 ? 1 : 0;
+    p.rows = (int)d->rows;
+    p.E = d->n_groups;
+    p.src_rows = (int)d->x_rows;
+    p.input_grad = input_grad;
+    p.k_len = input_grad ? d->out_features : d->in_features;
+    p.n_cols = input_grad ? d->in_features : d->out_features;
+    p.cfg = group_cfg(p.rows, p.E, input_grad);
+    p.offs = at<int32_t>(ws, L.offs);
+    p.counters = at<int32_t>(ws, L.counters);
+    p.num_tiles = at<int32_t>(ws, L.num_tiles);
+    p.tiles = at<RoutedTile>(ws, L.tiles);
+    return p;
+}
+
+int grouped_rows(const inkling_grouped_dims_t* d, bool input_grad, const void* src, const int32_t* row_index,
+                 const void* weight, const int32_t* offsets, void* out, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+    const int rc = check_grouped_dims(d);
+    if (rc != INKLING_OK) return rc;
+    if (d->rows == 0) return INKLING_OK;
+    if (src == nullptr || weight == nullptr || offsets == nullptr || out == nullptr || out == src || out == weight)
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (!input_grad && (row_index == nullptr ? d->x_rows != d->rows : d->x_rows == 0))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (!aligned(src, 16) || !aligned(weight, 16) || !aligned(out, 16) || !aligned(offsets, 4) ||
+        !aligned(row_index, 4))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    const GroupedLayout L = make_grouped_layout(d, grouped_row_tiles(d), 0);
+    if (workspace == nullptr || workspace_bytes < L.total) return INKLING_ERR_WORKSPACE;
+    GroupParams p = grouped_params(d, L, workspace, input_grad);
+    if (group_max_tiles(p) > INT32_MAX - 4096) return INKLING_ERR_UNSUPPORTED;
+    p.src = src;
+    p.weight = weight;
+    p.row_index = row_index;
+    p.out = out;
+    hipStream_t s = (hipStream_t)stream;
+    HIP_TRY(launch_group_plan(p, offsets, true, s));
+    HIP_TRY(launch_group_rows(p, s));
+    return INKLING_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int inkling_grouped_workspace_size(const inkling_grouped_dims_t* dims, size_t* bytes) {
+    const int rc = check_grouped_dims(dims);
+    if (rc != INKLING_OK) return rc;
+    if (bytes == nullptr) return INKLING_ERR_INVALID_ARGUMENT;
+    *bytes = make_grouped_layout(dims, grouped_row_tiles(dims), 0).total;
+    return INKLING_OK;
+}
+
+int inkling_grouped_weight_grad_workspace_size(const inkling_grouped_dims_t* dims, int gathered, size_t* bytes) {
+    const int rc = check_grouped_dims(dims);
+    if (rc != INKLING_OK) return rc;
+    if (bytes == nullptr) return INKLING_ERR_INVALID_ARGUMENT;
+    *bytes = make_grouped_layout(dims, 0, gathered ? grouped_gather_bytes(dims) : 0).total;
+    return INKLING_OK;
+}
+
+int inkling_grouped_linear(const inkling_grouped_dims_t* dims, const void* x, const int32_t* row_index,
+                           const void* weight, const int32_t* offsets, void* out, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    return grouped_rows(dims, false, x, row_index, weight, offsets, out, workspace, workspace_bytes, stream);
+}
+
+int inkling_grouped_input_grad(const inkling_grouped_dims_t* dims, const void* dout, const void* weight,
+                               const int32_t* offsets, void* dx, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+    return grouped_rows(dims, true, dout, nullptr, weight, offsets, dx, workspace, workspace_bytes, stream);
+}
+
+int inkling_grouped_weight_grad(const inkling_grouped_dims_t* dims, const void* dout, const void* x,
+                                const int32_t* row_index, const int32_t* offsets, void* dweight, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    const int rc = check_grouped_dims(dims);
+    if (rc != INKLING_OK) return rc;
+    if (offsets == nullptr || dweight == nullptr || dweight == dout || dweight == x)
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (dims->rows > 0 && (x == nullptr || dout == nullptr)) return INKLING_ERR_INVALID_ARGUMENT;
+    if (row_index == nullptr ? dims->x_rows != dims->rows : dims->rows > 0 && dims->x_rows == 0)
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (!aligned(x, 16) || !aligned(dout, 16) || !aligned(dweight, 16) || !aligned(offsets, 4) ||
+        !aligned(row_index, 4))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if ((long long)dims->n_groups * ((dims->out_features + 255) / 256) * ((dims->in_features + 127) / 128) >
+        INT32_MAX - 4096)
+        return INKLING_ERR_UNSUPPORTED;
+    const bool gather = row_index != nullptr && dims->rows > 0;
+    const GroupedLayout L = make_grouped_layout(dims, 0, gather ? grouped_gather_bytes(dims) : 0);
+    if (workspace == nullptr || workspace_bytes < L.total) return INKLING_ERR_WORKSPACE;
+    const GroupParams p = grouped_params(dims, L, workspace, false);
+    hipStream_t s = (hipStream_t)stream;
+    HIP_TRY(launch_group_plan(p, offsets, false, s));
+    if (gather) {
+        void* sorted = at<void>(workspace, L.x_sorted);
+        HIP_TRY(launch_group_gather(p.dtype, x, p.src_rows, row_index, p.offs, p.E, p.rows, dims->in_features, sorted,
+                                    s));
+        x = sorted;
+    }
+    HIP_TRY(launch_group_wgrad(p, x, dout, dims->in_features, dims->out_features, dweight, p.out_bf16, s));
     return INKLING_OK;
 }
 

@@ -54,13 +54,23 @@ namespace {
 // kModeDownOut: the shared down projection with the combine in its epilogue:
 //            out[t] = (shared sum) + sum_i y[t*k + i], in fp32 in that order,
 //            rounded once to the output type (shared tiles only)
-// A is read as [K][N] in kModeDAct, kModeDx and kModeWgrad, B in kModeWgrad.
+// The products that callers reach on their own (grouped.hip); K and N are any
+// multiples of 8 there, and a K tail reads zeros for both operands:
+// kModeGroup: out[r][n] = sum_k W_e[n][k] x[row of r][k], rounded once
+// kModeGroupDx: dx[r][n] = sum_k W_e[k][n] dout[r][k], rounded once
+// kModeGroupWgrad: dW_e[m][n] = sum_r dout[r][m] x[r][n]
+// A is read as [K][N] in kModeDAct, kModeDx, kModeWgrad, kModeGroupDx and
+// kModeGroupWgrad, B in the two weight-gradient modes.
 enum { kModeGateUp = 0, kModeDown = 1, kModeGateUpRaw = 2, kModeDAct = 3, kModeWgrad = 4, kModeDx = 5,
-       kModeDownOut = 6 };
+       kModeDownOut = 6, kModeGroup = 7, kModeGroupDx = 8, kModeGroupWgrad = 9 };
 template <int MODE>
-constexpr bool a_kn() { return MODE == kModeDAct || MODE == kModeDx || MODE == kModeWgrad; }
+constexpr bool grouped_mode() { return MODE == kModeGroup || MODE == kModeGroupDx || MODE == kModeGroupWgrad; }
 template <int MODE>
-constexpr bool b_kn() { return MODE == kModeWgrad; }
+constexpr bool wgrad_mode() { return MODE == kModeWgrad || MODE == kModeGroupWgrad; }
+template <int MODE>
+constexpr bool a_kn() { return MODE == kModeDAct || MODE == kModeDx || MODE == kModeGroupDx || wgrad_mode<MODE>(); }
+template <int MODE>
+constexpr bool b_kn() { return wgrad_mode<MODE>(); }
 // How the workgroups of an XCD walk its range of tiles after their first:
 // kSchedStride: with stride = workgroups per XCD;
 // kSchedRound: the same, meeting at the end of every round of tiles (below);
@@ -140,7 +150,19 @@ struct GemmKArgs {
     const int32_t* pos;
     void* out_final;
     int out_final_bf16;
+    // kModeGroup: T is the rows that row_token gathers from (row_token NULL:
+    // row r reads row r); kModeGroup, kModeGroupDx: out_final_bf16 is the type
+    // of out_routed
 };
+
+// what the lanes past a K tail load (16 bytes serve every lane)
+__device__ uint4 zero_chunk = {0u, 0u, 0u, 0u};
+
+typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+// four fp32 -> bf16, nearest even, NaN kept (v_cvt_pk_bf16_f32)
+__device__ __forceinline__ uint2 pack_bf16x4(const f32x4_t& v) {
+    return __builtin_bit_cast(uint2, __builtin_convertvector(v, bf16x4_t));
+}
 
 template <typename TE>
 __device__ __forceinline__ void mma16(f32x4_t& acc, const uint4& a, const uint4& b);
@@ -339,7 +361,7 @@ __device__ __forceinline__ Tile<TE> decode_tile(const GemmKArgs& a, int L, int B
     t.out = nullptr;
     t.segn = 1;
     t.segstride = 0;
-    if constexpr (MODE == kModeWgrad) {
+    if constexpr (wgrad_mode<MODE>()) {
         const int per_p = a.wg_mtiles * a.wg_ntiles;
         const int pr = L / per_p;
         int mt, nt;
@@ -351,7 +373,12 @@ __device__ __forceinline__ Tile<TE> decode_tile(const GemmKArgs& a, int L, int B
         t.N = a.wg_N;
         if (!t.is_shared) {
             const int r0 = a.offsets[pr];
-            t.K = a.poff[pr + 1] - a.poff[pr];
+            if constexpr (MODE == kModeGroupWgrad) {
+                constexpr int kStage = 64 / (int)sizeof(TE);   // whole stages of 64 bytes of K
+                t.K = (a.offsets[pr + 1] - r0 + kStage - 1) / kStage * kStage;
+            } else {
+                t.K = a.poff[pr + 1] - a.poff[pr];
+            }
             t.cnt = a.offsets[pr + 1] - r0;
             t.A = reinterpret_cast<const TE*>(a.A_routed) + (size_t)r0 * a.lda_r;
             t.B = reinterpret_cast<const TE*>(a.B_routed) + (size_t)r0 * a.ldb_r;
@@ -479,6 +506,9 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
     // operands read as [K][N]: a stage holds BK rows of K, each the tile's BN
     // (A) or BM (B) columns, filled by the same number of 1 KB wave loads
     constexpr bool AKN = a_kn<MODE>(), BKN = b_kn<MODE>();
+    constexpr bool GRP = grouped_mode<MODE>(), WG = wgrad_mode<MODE>();
+    constexpr int KUP = GRP ? BK - 1 : 0;           // a K tail is a stage of its own
+    static_assert(MODE != kModeGroupWgrad || ROWB == 64, "decode_tile pads K to stages of 64 bytes");
     // activation rows (written by gate_up, read by down): fp16 for bf16 layers,
     // so the bf16 down weights are converted to fp16 fragments (f16 MFMA)
     using TA = typename ActOf<TE>::type;
@@ -542,14 +572,14 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
     // Each XCD takes a contiguous range of blocks holding an eighth of the K
     // stages (shared and routed blocks differ in K when S*I is concatenated).
     // (weight gradients: one tile per workgroup, ranges by count)
-    const int nb_routed = MODE == kModeWgrad ? 0 : a.has_routed ? (*a.num_tiles) * a.ntn_r : 0;
-    const int nb_real = MODE == kModeWgrad ? (a.wg_E + a.S) * a.wg_mtiles * a.wg_ntiles
-                                           : a.shared_blocks + nb_routed;
+    const int nb_routed = WG ? 0 : a.has_routed ? (*a.num_tiles) * a.ntn_r : 0;
+    const int nb_real = WG ? (a.wg_E + a.S) * a.wg_mtiles * a.wg_ntiles
+                           : a.shared_blocks + nb_routed;
     const long long cost_s = (long long)a.shared_blocks * a.K_s;
     const long long cost_all = cost_s + (long long)nb_routed * a.K_r;
     auto range_start = [&](int x) -> int {
         if (x >= 8) return nb_real;
-        if constexpr (MODE == kModeWgrad) {
+        if constexpr (WG) {
             // a tile of problem p costs its K plus kWgradEpi (the fp32 tile
             // write); routed costs accumulate in poff
             const int per_p = a.wg_mtiles * a.wg_ntiles, E = a.wg_E;
@@ -648,7 +678,11 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
                 const int r = RPL * (wv + NW * q) + lr;
                 const int rr = min(r, t.rows_valid - 1);   // rows past the end re-read the last valid row
                 size_t row;
-                if (t.is_shared || MODE == kModeWgrad) row = (size_t)(t.t0 + rr);
+                if constexpr (GRP) {
+                    row = (size_t)(t.grow0 + rr);
+                    if (MODE == kModeGroup && a.row_token != nullptr)   // gathered; an index out of range reads a row in it
+                        row = (size_t)max(0, min(a.row_token[t.grow0 + rr], a.T - 1));
+                } else if (t.is_shared || MODE == kModeWgrad) row = (size_t)(t.t0 + rr);
                 else if (MODE == kModeGateUp || MODE == kModeGateUpRaw || MODE == kModeDAct)
                     row = (size_t)a.row_token[t.grow0 + rr];   // routed token rows, gathered
                 else row = (size_t)(t.grow0 + rr);
@@ -677,6 +711,21 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
     // experts along K).
     auto issue_a = [&](auto S_) __attribute__((always_inline)) {
         uint8_t* __restrict__ dst = stage_a(S_);
+        if constexpr (GRP) {
+            // the stage that holds the K tail: rows (AKN) or chunks past it load zeros
+            if (a_k + BK > cnt_ld) {
+                const size_t off = AKN ? (size_t)a_k * lda_ld : (size_t)a_k;
+#pragma unroll
+                for (int q = 0; q < A_PW; ++q) {
+                    const int r = AKN ? RPIA * (wv + NW * q) + lane / CHA : (lp ^ sw(RPL * (wv + NW * q) + lr)) * EPC;
+                    const TE* src = a_k + r < cnt_ld ? a_src[q] + off : reinterpret_cast<const TE*>(&zero_chunk);
+                    __builtin_amdgcn_global_load_lds((glb_void_t*)src, (lds_void_t*)(dst + (wv + NW * q) * 1024), 16, 0,
+                                                     0);
+                }
+                a_k += BK;
+                return;
+            }
+        }
         if constexpr (AKN) {
             const size_t off = (size_t)a_k * lda_ld;
             if (MODE == kModeWgrad && a_k + BK > cnt_ld) {
@@ -711,9 +760,24 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
     };
     auto issue_b = [&](auto S_) __attribute__((always_inline)) {
         uint8_t* __restrict__ dst = stage_b(S_);
+        if constexpr (GRP) {
+            if (b_k + BK > cnt_ld) {
+                const size_t off = BKN ? (size_t)b_k * ldb_ld : (size_t)b_k;
+#pragma unroll
+                for (int q = 0; q < B_PW; ++q) {
+                    const int qi = wv + NW * q;
+                    const int r = BKN ? RPIB * qi + lane / CHB : (lp ^ sw(RPL * qi + lr)) * EPC;
+                    const TE* src = b_k + r < cnt_ld ? b_src[q] + off : reinterpret_cast<const TE*>(&zero_chunk);
+                    if (qi < B_INS && (BKN || RPL * qi < rows_valid_ld))
+                        __builtin_amdgcn_global_load_lds((glb_void_t*)src, (lds_void_t*)(dst + qi * 1024), 16, 0, 0);
+                }
+                b_k += BK;
+                return;
+            }
+        }
         if constexpr (BKN) {
             const size_t off = (size_t)b_k * ldb_ld;
-            if (b_k + BK > cnt_ld) {
+            if (!GRP && b_k + BK > cnt_ld) {
                 // rows past the tile's count read the zero row (same columns)
 #pragma unroll
                 for (int q = 0; q < B_PW; ++q) {
@@ -759,7 +823,7 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
                                   // down_out: 1 if the row's token has routed rows
     int ep_s0 = 0;                // gate_up shared: expert of the wave's first weight row
     auto prefetch_epilogue = [&](const Tile<TE>& t) __attribute__((always_inline)) {
-        if constexpr (MODE == kModeGateUpRaw || MODE == kModeWgrad) return;
+        if constexpr (MODE == kModeGateUpRaw || WG || GRP) return;
         // columns of shared expert s: [s*2I, (s+1)*2I) in gate_up, [s*I, (s+1)*I) in dact
         const int width = MODE == kModeDAct ? a.I : 2 * a.I;
         const int s0 = min((t.n0 + wn0) / width, max(a.S - 1, 0));
@@ -1005,12 +1069,12 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
 
     Tile<TE> cur = decode_tile<TE, BM, GM, MODE>(a, L, BN);
     setup(cur);
-    issue_first(cur.K / BK);
+    issue_first((cur.K + KUP) / BK);
     prefetch_epilogue(cur);
     draw();
 
     while (true) {
-        const int nk = cur.K / BK;
+        const int nk = (cur.K + KUP) / BK;
         if constexpr (SCHED == kSchedRound) sync_round = (L - L_beg) / nloc;
         // token blocks / weight-row blocks of this wave that hold valid rows
         const int nvb_all = (cur.rows_valid + 15) >> 4;
@@ -1058,7 +1122,7 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
         if (has_next) {
             nxt = decode_tile<TE, BM, GM, MODE>(a, L, BN);
             setup(nxt);
-            issue_first(nxt.K / BK);
+            issue_first((nxt.K + KUP) / BK);
             draw();
         }
 
@@ -1145,7 +1209,8 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
                         const int c = ln + 64 * sgi, r = c >> 3, q = c & 7;
                         const f32x4_t d = *reinterpret_cast<const f32x4_t*>(ep + r * kEpRowB + q * 16);
                         float* o = rowp(r);
-                        if (o != nullptr && mb + r < cur.rows_valid && 2 * hh + (q >> 2) < nvi)
+                        if (o != nullptr && mb + r < cur.rows_valid && 2 * hh + (q >> 2) < nvi &&
+                            (!GRP || cur.n0 + wn0 + 32 * hh + 4 * q < cur.N))   // N a multiple of 8, not of 16
                             *reinterpret_cast<f32x4_t*>(o + 32 * hh + 4 * q) = d;
                     }
                 }
@@ -1190,6 +1255,30 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
                     float* hb = reinterpret_cast<float*>(cur.is_shared ? a.out_shared : a.out_routed) +
                                 (size_t)(cur.is_shared ? cur.t0 : cur.grow0) * cur.N + cur.n0 + wn0;
                     flush_f32(j, mb, [&](int r) -> float* { return hb + (size_t)(mb + r) * cur.N; });
+                } else if constexpr (GRP) {
+                    // rows of the product (weight gradients: rows of dW_e), fp32
+                    // or rounded once to bf16 (64 columns fill a 128-byte LDS row)
+                    const bool to_bf16 = WG ? a.w_out_bf16 : a.out_final_bf16;
+                    char* ob = static_cast<char*>(WG ? cur.out : a.out_routed);
+                    const size_t row0 = (size_t)(WG ? cur.t0 : cur.grow0);
+                    if (to_bf16) {
+#pragma unroll
+                        for (int i = 0; i < FN; ++i)
+                            if (i < nvi)
+                                *reinterpret_cast<uint2*>(ep + rw * kEpRowB + (16 * i + 4 * g4) * 2) =
+                                    pack_bf16x4(acc[i][j]);
+                        bf16_t* hb = reinterpret_cast<bf16_t*>(ob) + row0 * cur.N + cur.n0 + wn0;
+#pragma unroll
+                        for (int sgi = 0; sgi < 2; ++sgi) {
+                            const int c = ln + 64 * sgi, r = c >> 3, q = c & 7;
+                            const uint4 d = *reinterpret_cast<const uint4*>(ep + r * kEpRowB + q * 16);
+                            if (mb + r < cur.rows_valid && cur.n0 + wn0 + 8 * q < cur.N)
+                                *reinterpret_cast<uint4*>(hb + (size_t)(mb + r) * cur.N + 8 * q) = d;
+                        }
+                    } else {
+                        float* hb = reinterpret_cast<float*>(ob) + row0 * cur.N + cur.n0 + wn0;
+                        flush_f32(j, mb, [&](int r) -> float* { return hb + (size_t)(mb + r) * cur.N; });
+                    }
                 } else if constexpr (MODE == kModeWgrad) {
                     if (a.w_out_bf16) {
                         // bf16 gradients: the fp32 sums rounded once; 64 columns
@@ -1278,7 +1367,16 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
                     const int n = cur.n0 + wn0 + 16 * i + 4 * (lane >> 4);
                     if (i < nvi) {
                         const f32x4_t v = acc[i][j];
-                        if (MODE == kModeGateUpRaw) {   // h kept in fp32 (not an MFMA operand)
+                        if constexpr (GRP) {
+                            const size_t at = (size_t)((WG ? cur.t0 : cur.grow0) + m) * cur.N + n;
+                            void* ob = WG ? cur.out : a.out_routed;
+                            if (n < cur.N) {
+                                if (WG ? a.w_out_bf16 : a.out_final_bf16)
+                                    *reinterpret_cast<uint2*>(static_cast<bf16_t*>(ob) + at) = pack_bf16x4(v);
+                                else
+                                    *reinterpret_cast<f32x4_t*>(static_cast<float*>(ob) + at) = v;
+                            }
+                        } else if (MODE == kModeGateUpRaw) {   // h kept in fp32 (not an MFMA operand)
                             float* o = reinterpret_cast<float*>(cur.is_shared ? a.out_shared : a.out_routed) +
                                        (size_t)(cur.is_shared ? cur.t0 + m : cur.grow0 + m) * cur.N + n;
                             float w[4] = {v[0], v[1], v[2], v[3]};

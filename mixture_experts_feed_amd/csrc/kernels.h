@@ -164,6 +164,39 @@ hipError_t launch_dbank(int dtype, const float* dz, const void* x, int T, int H,
                         hipStream_t stream);
 int dbank_partial_floats(int H, int NE);
 
+// ---- products grouped by expert (grouped.hip) --------------------------------
+struct GroupParams {
+    int dtype;             // 0 f32, 1 bf16: rows and weights
+    int cfg;               // group_cfg()
+    int rows, E;
+    const void* src;       // rows of k_len values
+    const void* weight;    // [E][n_out][n_in]
+    const int32_t* row_index;   // row r reads src[row_index[r]] (NULL: src[r]); forward only
+    int src_rows;
+    void* out;             // [rows][n_cols]
+    int out_bf16;
+    int k_len, n_cols;     // forward: n_in, n_out; input gradient: n_out, n_in
+    bool input_grad;
+    // plan, in the caller's workspace
+    int32_t* offs;         // [E + 1]
+    RoutedTile* tiles;
+    int32_t* num_tiles;
+    int32_t* counters;     // kRoundCounters
+};
+int group_cfg(int rows, int E, bool input_grad);
+long long group_max_row_tiles(int rows, int E, int cfg);
+long long group_max_tiles(const GroupParams& p);   // row tiles x column tiles
+// the plan from the caller's offsets (clamped to the rows, non-decreasing);
+// `tiles`: the row tiles too
+hipError_t launch_group_plan(const GroupParams& p, const int32_t* offsets, bool tiles, hipStream_t stream);
+hipError_t launch_group_rows(const GroupParams& p, hipStream_t stream);
+// out[r] = src[row_index[r]] for the rows of the plan
+hipError_t launch_group_gather(int dtype, const void* src, int src_rows, const int32_t* row_index,
+                               const int32_t* offs, int E, int rows, int D, void* out, hipStream_t stream);
+// dw[e] = dout^T x over the rows of e (x and dout in row order)
+hipError_t launch_group_wgrad(const GroupParams& p, const void* x, const void* dout, int n_in, int n_out, void* dw,
+                              int dw_bf16, hipStream_t stream);
+
 // gamma[t] = value for t < T; the GEMM round counters zeroed (the dense MLP's
 // stand-in for the router and the permutation)
 hipError_t launch_dense_prep(float* gamma, int T, float value, int32_t* round_counters, hipStream_t stream);

@@ -1,0 +1,96 @@
+"""Host-side argument checks of the expert-block operators' C ABI (no GPU):
+every refusal returns before anything is launched."""
+import ctypes
+import os
+
+import pytest
+
+from mixture_experts_feed_amd import binding as B
+
+P = ctypes.c_void_p
+FAKE, FAKE2, FAKE3, ODD = 0x10000, 0x20000, 0x30000, 0x10008
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(B.LIB_PATH):
+        from mixture_experts_feed_amd import build
+        build.build(verbose=False)
+    return B.load()
+
+
+def _grouped(**kw):
+    d = dict(rows=100, x_rows=100, n_groups=4, in_features=64, out_features=40, dtype=B.INKLING_BF16,
+             out_dtype=B.INKLING_BF16)
+    d.update(kw)
+    return B.GroupedDims(d["rows"], d["x_rows"], d["n_groups"], d["in_features"], d["out_features"], d["dtype"],
+                         d["out_dtype"])
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), B.INKLING_ERR_INVALID_ARGUMENT),
+    (dict(x_rows=-1), B.INKLING_ERR_INVALID_ARGUMENT),
+    (dict(n_groups=0), B.INKLING_ERR_INVALID_ARGUMENT),
+    (dict(in_features=0), B.INKLING_ERR_INVALID_ARGUMENT),
+    (dict(out_features=-8), B.INKLING_ERR_INVALID_ARGUMENT),
+    (dict(n_groups=513), B.INKLING_ERR_UNSUPPORTED),
+    (dict(in_features=60), B.INKLING_ERR_UNSUPPORTED),
+    (dict(out_features=36), B.INKLING_ERR_UNSUPPORTED),
+    (dict(in_features=(1 << 20) + 8), B.INKLING_ERR_UNSUPPORTED),
+    (dict(dtype=2), B.INKLING_ERR_UNSUPPORTED),
+    (dict(out_dtype=-1), B.INKLING_ERR_UNSUPPORTED),
+    (dict(rows=2 ** 31, x_rows=2 ** 31), B.INKLING_ERR_UNSUPPORTED),
+    (dict(x_rows=2 ** 31), B.INKLING_ERR_UNSUPPORTED),
+])
+def test_grouped_dims(lib, kw, code):
+    d, n = _grouped(**kw), ctypes.c_size_t(0)
+    assert lib.inkling_grouped_workspace_size(ctypes.byref(d), ctypes.byref(n)) == code
+    assert lib.inkling_grouped_weight_grad_workspace_size(ctypes.byref(d), 1, ctypes.byref(n)) == code
+    assert lib.inkling_grouped_linear(ctypes.byref(d), FAKE, FAKE, FAKE, FAKE, FAKE2, FAKE, BIG, None) == code
+    assert lib.inkling_grouped_input_grad(ctypes.byref(d), FAKE, FAKE, FAKE, FAKE2, FAKE, BIG, None) == code
+    assert lib.inkling_grouped_weight_grad(ctypes.byref(d), FAKE, FAKE, FAKE, FAKE, FAKE2, FAKE, BIG, None) == code
+
+
+def test_grouped_pointers(lib):
+    d = _grouped()
+    bad = B.INKLING_ERR_INVALID_ARGUMENT
+    fwd = lambda x=FAKE, i=None, w=FAKE2, o=FAKE, out=FAKE3, ws=FAKE, n=BIG, dd=d: lib.inkling_grouped_linear(  # noqa: E731
+        ctypes.byref(dd), x, i, w, o, out, ws, n, None)
+    for kw in (dict(x=None), dict(w=None), dict(o=None), dict(out=None), dict(out=FAKE), dict(out=FAKE2),
+               dict(x=ODD), dict(w=ODD), dict(out=ODD), dict(o=FAKE + 2), dict(i=FAKE + 1)):
+        assert fwd(**kw) == bad, kw
+    assert fwd(ws=None) == B.INKLING_ERR_WORKSPACE
+    assert fwd(n=64) == B.INKLING_ERR_WORKSPACE
+    assert fwd(dd=_grouped(x_rows=99)) == bad                       # no row index: x has a row for each row
+    assert fwd(dd=_grouped(x_rows=0), i=FAKE) == bad                # an index into nothing
+    assert lib.inkling_grouped_linear(None, FAKE, None, FAKE, FAKE, FAKE2, FAKE, BIG, None) == bad
+    dx = lambda d_=FAKE, w=FAKE2, o=FAKE, out=FAKE3: lib.inkling_grouped_input_grad(  # noqa: E731
+        ctypes.byref(d), d_, w, o, out, FAKE, BIG, None)
+    for kw in (dict(d_=None), dict(w=None), dict(o=None), dict(out=None), dict(out=FAKE2), dict(d_=ODD)):
+        assert dx(**kw) == bad, kw
+    dw = lambda d_=FAKE, x=FAKE2, i=None, o=FAKE, out=FAKE3, n=BIG: lib.inkling_grouped_weight_grad(  # noqa: E731
+        ctypes.byref(d), d_, x, i, o, out, FAKE, n, None)
+    for kw in (dict(d_=None), dict(x=None), dict(o=None), dict(out=None), dict(out=FAKE2), dict(x=ODD),
+               dict(out=ODD)):
+        assert dw(**kw) == bad, kw
+    n = ctypes.c_size_t(0)
+    assert lib.inkling_grouped_weight_grad_workspace_size(ctypes.byref(d), 0, ctypes.byref(n)) == 0
+    plain = n.value
+    assert lib.inkling_grouped_weight_grad_workspace_size(ctypes.byref(d), 1, ctypes.byref(n)) == 0
+    assert n.value >= plain + 100 * 64 * 2
+    assert dw(i=FAKE, n=plain) == B.INKLING_ERR_WORKSPACE
+    assert lib.inkling_grouped_workspace_size(ctypes.byref(d), None) == bad
+
+
+def test_grouped_tile_count_limit(lib):
+    """2^31 - 257 rows against 2^20 columns are more output tiles than the kernels count."""
+    d = _grouped(rows=2 ** 31 - 257, x_rows=2 ** 31 - 257, out_features=1 << 20)
+    assert lib.inkling_grouped_linear(ctypes.byref(d), FAKE, None, FAKE2, FAKE, FAKE3, FAKE, 1 << 50,
+                                      None) == B.INKLING_ERR_UNSUPPORTED
+
+
+def test_grouped_no_rows_is_a_noop(lib):
+    d = _grouped(rows=0, x_rows=0)
+    assert lib.inkling_grouped_linear(ctypes.byref(d), None, None, None, None, None, None, 0, None) == B.INKLING_OK
+    assert lib.inkling_grouped_input_grad(ctypes.byref(d), None, None, None, None, None, 0, None) == B.INKLING_OK

@@ -316,6 +316,86 @@ int inkling_grouped_weight_grad(const inkling_grouped_dims_t* dims, const void* 
                                 const int32_t* row_index, const int32_t* offsets, void* dweight, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/*
+ * SwiGLU between an expert's two projections (inkling_swiglu with routing
+ * weights), with an 8-bit checkpoint of its input for the backward pass:
+ *   forward   act = gamma * silu(g) * u,  h [rows][2*I] = [g0, u0, g1, u1, ...]
+ *   backward  dh, dgamma and act again, from dact and the checkpoint alone.
+ * The checkpoint holds each value as an int8 and one power of two for every 32
+ * columns of a row: the smallest 2^e, e >= -126, with max|h| <= 127 * 2^e; the
+ * int8 is h / 2^e to nearest, ties to even.  A value comes back off by at most
+ * 2^(e-1), so by at most max|h| / 127 of its 32 columns; a block that holds an
+ * infinity or a NaN comes back as NaN.  Layout: [rows][2*I] int8, then
+ * [rows][2*I/32] bytes e + 127 (255: NaN block); 2.0625 * I bytes a row, against
+ * 8 * I of inkling_moe_forward_train's fp32 projections.
+ * The backward is the derivative of act at the values that come back: with
+ * s = sigmoid(g), p = g * s * u: act = gamma * p, dgamma = sum dact * p,
+ * dg = gamma * dact * u * s * (1 + g * (1 - s)), du = gamma * dact * g * s.
+ *   gamma     [rows] fp32, or NULL for 1
+ *   row_count one int32 on the device, or NULL for all rows: rows from
+ *             *row_count on are neither read nor written (offsets + n_groups of
+ *             grouped rows); clamped to [0, rows]
+ * h, act, dact and dh in dims->dtype; arithmetic in fp32, rounded once.
+ * Limits: intermediate a multiple of 16 up to 2^20, rows <= 2^31 - 257.
+ * Tensor pointers 16-byte aligned (gamma, dgamma and row_count 4-byte); outputs
+ * must not overlap operands.  No workspace; rows == 0 is a no-op.
+ */
+typedef struct {
+    int64_t rows;
+    int32_t intermediate; /* I */
+    int32_t dtype;        /* inkling_dtype_t of h, act, dact, dh */
+} inkling_swiglu_dims_t;
+
+/* bytes of the checkpoint */
+int inkling_swiglu_checkpoint_size(const inkling_swiglu_dims_t* dims, size_t* bytes);
+
+/* checkpoint: written, or NULL to keep nothing (serving) */
+int inkling_swiglu_forward(const inkling_swiglu_dims_t* dims, const void* h, const float* gamma,
+                           const int32_t* row_count, void* act, void* checkpoint, size_t checkpoint_bytes,
+                           void* stream);
+
+/* act and dgamma may be NULL (not computed) */
+int inkling_swiglu_backward(const inkling_swiglu_dims_t* dims, const void* dact, const void* checkpoint,
+                            size_t checkpoint_bytes, const float* gamma, const int32_t* row_count, void* dh,
+                            void* act, float* dgamma, void* stream);
+
+/*
+ * Layer norm and RMS norm over the rows of x [rows][hidden] (the norm in front
+ * of the block):
+ *   INKLING_NORM_LAYER  out = (x - mean) * rstd * weight + bias,
+ *                       rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ *   INKLING_NORM_RMS    the same with mean = 0 and no bias (bias and dbias must
+ *                       be NULL)
+ * weight, bias, dweight and dbias are [hidden] fp32; x, out, dout and dx in
+ * dims->dtype; statistics and sums in fp32, the variance about the mean (no
+ * difference of large squares), each result rounded once.
+ *   stats  [rows][2] fp32: mean (0 for RMS) and rstd; forward: may be NULL
+ * The backward returns gradients of sum(dout * out); dweight and dbias are
+ * overwritten and summed over the rows in a fixed order (bit-reproducible).
+ * bias NULL: no bias; dbias NULL: not wanted.  rows == 0 is a no-op for the
+ * forward and gives zero dweight and dbias in the backward.
+ * Limits: hidden <= 16384 (any width; multiples of 8 bf16 or 4 fp32 values are
+ * the fast path), rows <= 2^31 - 65537, 0 <= eps finite (eps 0 and a constant
+ * row: infinite rstd).  Tensor pointers 16-byte aligned; outputs must not
+ * overlap operands.
+ */
+typedef enum { INKLING_NORM_LAYER = 0, INKLING_NORM_RMS = 1 } inkling_norm_kind_t;
+
+typedef struct {
+    int64_t rows;
+    int32_t hidden;
+    int32_t kind;   /* inkling_norm_kind_t */
+    int32_t dtype;  /* inkling_dtype_t of x, out, dout, dx */
+    float eps;
+} inkling_norm_dims_t;
+
+int inkling_norm_forward(const inkling_norm_dims_t* dims, const void* x, const float* weight, const float* bias,
+                         void* out, float* stats, void* stream);
+int inkling_norm_backward_workspace_size(const inkling_norm_dims_t* dims, size_t* bytes);
+int inkling_norm_backward(const inkling_norm_dims_t* dims, const void* dout, const void* x, const float* weight,
+                          const float* stats, void* dx, float* dweight, float* dbias, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
 /* Stage timing (instrumentation for benchmarks).  When `events` is non-NULL,
  * each later inkling_moe_forward on the calling thread records, on its stream,
  * events[0] before the first launch and events[i] after stage i:

@@ -31,7 +31,12 @@ EXPORTED = ("inkling_moe_workspace_size", "inkling_moe_route", "inkling_moe_forw
             "inkling_moe_backward_workspace_size", "inkling_moe_backward", "inkling_moe_saved_size",
             "inkling_moe_forward_train", "inkling_moe_forward_noalloc",
             "inkling_grouped_workspace_size", "inkling_grouped_weight_grad_workspace_size",
-            "inkling_grouped_linear", "inkling_grouped_input_grad", "inkling_grouped_weight_grad")
+            "inkling_grouped_linear", "inkling_grouped_input_grad", "inkling_grouped_weight_grad",
+            "inkling_swiglu_checkpoint_size", "inkling_swiglu_forward", "inkling_swiglu_backward",
+            "inkling_norm_forward", "inkling_norm_backward_workspace_size", "inkling_norm_backward")
+INKLING_NORM_LAYER = 0
+INKLING_NORM_RMS = 1
+NORM_KINDS = {"layer": INKLING_NORM_LAYER, "rms": INKLING_NORM_RMS}
 INKLING_STAGE_EVENTS = 7
 STAGES = ("router_logits", "router_select", "permutation", "gate_up", "down", "shared_down_combine")
 
@@ -57,6 +62,15 @@ class GroupedDims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("x_rows", ctypes.c_int64), ("n_groups", ctypes.c_int32),
                 ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32)]
+
+
+class SwigluDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("intermediate", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class Gate(ctypes.Structure):
@@ -135,13 +149,19 @@ def load() -> ctypes.CDLL:
                                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.inkling_moe_forward_train.restype = ctypes.c_int
     ptr, size = ctypes.c_void_p, ctypes.c_size_t
-    gdims = ctypes.POINTER(GroupedDims)
+    gdims, sdims, ndims = (ctypes.POINTER(c) for c in (GroupedDims, SwigluDims, NormDims))
     for name, args in (
             ("inkling_grouped_workspace_size", [gdims, ctypes.POINTER(size)]),
             ("inkling_grouped_weight_grad_workspace_size", [gdims, ctypes.c_int, ctypes.POINTER(size)]),
             ("inkling_grouped_linear", [gdims, ptr, ptr, ptr, ptr, ptr, ptr, size, ptr]),
             ("inkling_grouped_input_grad", [gdims, ptr, ptr, ptr, ptr, ptr, size, ptr]),
-            ("inkling_grouped_weight_grad", [gdims, ptr, ptr, ptr, ptr, ptr, ptr, size, ptr])):
+            ("inkling_grouped_weight_grad", [gdims, ptr, ptr, ptr, ptr, ptr, ptr, size, ptr]),
+            ("inkling_swiglu_checkpoint_size", [sdims, ctypes.POINTER(size)]),
+            ("inkling_swiglu_forward", [sdims, ptr, ptr, ptr, ptr, ptr, size, ptr]),
+            ("inkling_swiglu_backward", [sdims, ptr, ptr, size, ptr, ptr, ptr, ptr, ptr, ptr]),
+            ("inkling_norm_forward", [ndims, ptr, ptr, ptr, ptr, ptr, ptr]),
+            ("inkling_norm_backward_workspace_size", [ndims, ctypes.POINTER(size)]),
+            ("inkling_norm_backward", [ndims, ptr, ptr, ptr, ptr, ptr, ptr, ptr, ptr, size, ptr])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = ctypes.c_int
     _LIB = lib
@@ -594,3 +614,168 @@ def grouped_weight_grad(dout: torch.Tensor, x: torch.Tensor, offsets: torch.Tens
                                                   offsets.data_ptr(), dweight.data_ptr(), ws.data_ptr(), ws.numel(),
                                                   _stream(dev)), "inkling_grouped_weight_grad")
     return dweight
+
+
+# ---- SwiGLU with an 8-bit checkpoint ------------------------------------------------
+
+
+def make_swiglu_dims(rows, intermediate, dtype) -> SwigluDims:
+    return SwigluDims(int(rows), int(intermediate), dtype if isinstance(dtype, int) else _dtype_code(dtype))
+
+
+def swiglu_checkpoint_size(dims: SwigluDims) -> int:
+    """inkling_swiglu_checkpoint_size: bytes of the 8-bit checkpoint."""
+    n = ctypes.c_size_t(0)
+    _check(load().inkling_swiglu_checkpoint_size(ctypes.byref(dims), ctypes.byref(n)),
+           "inkling_swiglu_checkpoint_size")
+    return int(n.value)
+
+
+def _row_checks(dev, rows, gamma, row_count):
+    if gamma is not None:
+        _need(gamma, "gamma", torch.float32)
+        if gamma.numel() != rows:
+            raise ValueError(f"gamma must hold {rows} values")
+    if row_count is not None:
+        _need(row_count, "row_count", torch.int32)
+        if row_count.numel() != 1:
+            raise ValueError("row_count must hold one value")
+    _same_device(dev, gamma=gamma, row_count=row_count)
+
+
+def swiglu_forward(h: torch.Tensor, gamma: Optional[torch.Tensor] = None, row_count: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None, checkpoint: Optional[torch.Tensor] = None,
+                   save: bool = True):
+    """inkling_swiglu_forward: (act [rows, I], checkpoint) of h [rows, 2I]
+    (interleaved [gate, up] columns), act = gamma silu(gate) up.  The checkpoint
+    is a uint8 tensor of swiglu_checkpoint_size bytes (made here unless given);
+    save=False keeps none and returns None in its place.  Rows from
+    row_count[0] on are left as they are."""
+    if h.dim() != 2 or h.shape[1] % 2:
+        raise ValueError("h must be [rows, 2 * intermediate]")
+    _need(h, "h")
+    R, I = h.shape[0], h.shape[1] // 2
+    dev = h.device
+    _row_checks(dev, R, gamma, row_count)
+    dims = make_swiglu_dims(R, I, h.dtype)
+    need = swiglu_checkpoint_size(dims)
+    out = _result(out, "out", (R, I), h.dtype, dev)
+    if not save and checkpoint is not None:
+        raise ValueError("save=False keeps no checkpoint: give none")
+    if save:
+        checkpoint = _scratch(checkpoint, need, dev)
+    with torch.cuda.device(dev):
+        _check(load().inkling_swiglu_forward(ctypes.byref(dims), h.data_ptr(), _ptr(gamma), _ptr(row_count),
+                                             out.data_ptr(), _ptr(checkpoint),
+                                             0 if checkpoint is None else checkpoint.numel(), _stream(dev)),
+               "inkling_swiglu_forward")
+    return out, checkpoint
+
+
+def swiglu_backward(dact: torch.Tensor, checkpoint: torch.Tensor, gamma: Optional[torch.Tensor] = None,
+                    row_count: Optional[torch.Tensor] = None, dh: Optional[torch.Tensor] = None,
+                    act: Optional[torch.Tensor] = None, dgamma: Optional[torch.Tensor] = None,
+                    want_act: bool = True, want_dgamma: bool = True) -> dict:
+    """inkling_swiglu_backward: dict(dh [rows, 2I], act [rows, I], dgamma
+    [rows] fp32) from dact and the checkpoint that swiglu_forward filled with
+    the same gamma and row_count; act (for the down projection's weight
+    gradient) and dgamma are None where they are not wanted."""
+    if dact.dim() != 2:
+        raise ValueError("dact must be [rows, intermediate]")
+    _need(dact, "dact")
+    _need(checkpoint, "checkpoint", torch.uint8)
+    R, I = dact.shape
+    dev = dact.device
+    _row_checks(dev, R, gamma, row_count)
+    _same_device(dev, checkpoint=checkpoint)
+    if (act is not None and not want_act) or (dgamma is not None and not want_dgamma):
+        raise ValueError("a result is both given and not wanted")
+    dims = make_swiglu_dims(R, I, dact.dtype)
+    swiglu_checkpoint_size(dims)   # the limits, before anything is allocated
+    dh = _result(dh, "dh", (R, 2 * I), dact.dtype, dev)
+    act = _result(act, "act", (R, I), dact.dtype, dev) if want_act else None
+    dgamma = _result(dgamma, "dgamma", (R,), torch.float32, dev) if want_dgamma else None
+    with torch.cuda.device(dev):
+        _check(load().inkling_swiglu_backward(ctypes.byref(dims), dact.data_ptr(), checkpoint.data_ptr(),
+                                              checkpoint.numel(), _ptr(gamma), _ptr(row_count), dh.data_ptr(),
+                                              _ptr(act), _ptr(dgamma), _stream(dev)), "inkling_swiglu_backward")
+    return {"dh": dh, "act": act, "dgamma": dgamma}
+
+
+# ---- layer norm and RMS norm --------------------------------------------------------
+
+
+def make_norm_dims(rows, hidden, kind, dtype, eps) -> NormDims:
+    if isinstance(kind, str):
+        if kind not in NORM_KINDS:
+            raise ValueError(f"kind must be one of {sorted(NORM_KINDS)}")
+        kind = NORM_KINDS[kind]
+    return NormDims(int(rows), int(hidden), kind, dtype if isinstance(dtype, int) else _dtype_code(dtype), float(eps))
+
+
+def norm_backward_workspace_size(dims: NormDims) -> int:
+    """inkling_norm_backward_workspace_size."""
+    n = ctypes.c_size_t(0)
+    _check(load().inkling_norm_backward_workspace_size(ctypes.byref(dims), ctypes.byref(n)),
+           "inkling_norm_backward_workspace_size")
+    return int(n.value)
+
+
+def _norm_checks(x, weight, bias):
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, hidden]")
+    _need(x, "x")
+    for t, n in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _need(t, n, torch.float32)
+            if t.shape != (x.shape[1],):
+                raise ValueError(f"{n} must have shape ({x.shape[1]},)")
+    _same_device(x.device, weight=weight, bias=bias)
+
+
+def norm_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 kind: str = "layer", out: Optional[torch.Tensor] = None, stats: Optional[torch.Tensor] = None,
+                 save: bool = True):
+    """inkling_norm_forward: (out, stats) of x [rows, hidden]; kind "layer" or
+    "rms" (no mean, no bias).  stats [rows, 2] fp32 (mean, 1 / sqrt(variance +
+    eps)) is what norm_backward takes; save=False keeps none (None)."""
+    _norm_checks(x, weight, bias)
+    R, H = x.shape
+    dev = x.device
+    dims = make_norm_dims(R, H, kind, x.dtype, eps)
+    norm_backward_workspace_size(dims)   # the limits, before anything is allocated
+    out = _result(out, "out", (R, H), x.dtype, dev)
+    if not save and stats is not None:
+        raise ValueError("save=False keeps no stats: give none")
+    stats = _result(stats, "stats", (R, 2), torch.float32, dev) if save else None
+    with torch.cuda.device(dev):
+        _check(load().inkling_norm_forward(ctypes.byref(dims), x.data_ptr(), weight.data_ptr(), _ptr(bias),
+                                           out.data_ptr(), _ptr(stats), _stream(dev)), "inkling_norm_forward")
+    return out, stats
+
+
+def norm_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, stats: torch.Tensor,
+                  kind: str = "layer", bias: bool = False, dx: Optional[torch.Tensor] = None,
+                  dweight: Optional[torch.Tensor] = None, dbias: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None) -> dict:
+    """inkling_norm_backward: dict(dx, dweight, dbias) from dout, the forward's
+    x and weight and its stats; dbias is None unless `bias` (or a `dbias`) is
+    given."""
+    _norm_checks(x, weight, None)
+    R, H = x.shape
+    dev = x.device
+    _need(dout, "dout", x.dtype)
+    _need(stats, "stats", torch.float32)
+    if dout.shape != x.shape or stats.shape != (R, 2):
+        raise ValueError("dout must have x's shape and stats be [rows, 2]")
+    _same_device(dev, dout=dout, stats=stats)
+    dims = make_norm_dims(R, H, kind, x.dtype, 0.0)
+    ws = _scratch(workspace, norm_backward_workspace_size(dims), dev)
+    dx = _result(dx, "dx", (R, H), x.dtype, dev)
+    dweight = _result(dweight, "dweight", (H,), torch.float32, dev)
+    dbias = _result(dbias, "dbias", (H,), torch.float32, dev) if bias or dbias is not None else None
+    with torch.cuda.device(dev):
+        _check(load().inkling_norm_backward(ctypes.byref(dims), dout.data_ptr(), x.data_ptr(), weight.data_ptr(),
+                                            stats.data_ptr(), dx.data_ptr(), dweight.data_ptr(), _ptr(dbias),
+                                            ws.data_ptr(), ws.numel(), _stream(dev)), "inkling_norm_backward")
+    return {"dx": dx, "dweight": dweight, "dbias": dbias}

@@ -843,6 +843,171 @@ int inkling_grouped_weight_grad(const inkling_grouped_dims_t* dims, const void* 
     return INKLING_OK;
 }
 
+}  // extern "C"
+
+// ---- SwiGLU with an 8-bit checkpoint; norms ---------------------------------------
+namespace {
+
+int check_swiglu_dims(const inkling_swiglu_dims_t* d) {
+    if (d == nullptr || d->rows < 0 || d->intermediate <= 0) return INKLING_ERR_INVALID_ARGUMENT;
+    if (d->dtype != INKLING_F32 && d->dtype != INKLING_BF16) return INKLING_ERR_UNSUPPORTED;
+    if (d->intermediate % 16 != 0 || d->intermediate > (1 << 20) || d->rows > INT32_MAX - 256)
+        return INKLING_ERR_UNSUPPORTED;
+    return INKLING_OK;
+}
+
+size_t swiglu_kept_bytes(const inkling_swiglu_dims_t* d) { return (size_t)d->rows * 2 * d->intermediate; }
+size_t swiglu_checkpoint_bytes(const inkling_swiglu_dims_t* d) {
+    return swiglu_kept_bytes(d) + (size_t)d->rows * (d->intermediate / 16);
+}
+
+SwigluParams swiglu_params(const inkling_swiglu_dims_t* d, const float* gamma, const int32_t* row_count,
+                           void* checkpoint) {
+    SwigluParams p = {};
+    p.dtype = d->dtype == INKLING_BF16 ? 1 : 0;
+    p.rows = (int)d->rows;
+    p.I = d->intermediate;
+    p.gamma = gamma;
+    p.row_count = row_count;
+    if (checkpoint != nullptr) {
+        p.kept = static_cast<int8_t*>(checkpoint);
+        p.exps = static_cast<uint8_t*>(checkpoint) + swiglu_kept_bytes(d);
+    }
+    return p;
+}
+
+int check_norm_dims(const inkling_norm_dims_t* d) {
+    if (d == nullptr || d->rows < 0 || d->hidden <= 0) return INKLING_ERR_INVALID_ARGUMENT;
+    if (!(d->eps >= 0.0f && d->eps <= 3.4028234e38f)) return INKLING_ERR_INVALID_ARGUMENT;   // also NaN
+    if (d->kind != INKLING_NORM_LAYER && d->kind != INKLING_NORM_RMS) return INKLING_ERR_UNSUPPORTED;
+    if (d->dtype != INKLING_F32 && d->dtype != INKLING_BF16) return INKLING_ERR_UNSUPPORTED;
+    if (d->hidden > 16384 || d->rows > INT32_MAX - 65536) return INKLING_ERR_UNSUPPORTED;
+    return INKLING_OK;
+}
+
+// partial rows of dweight and dbias
+size_t norm_part_bytes(const inkling_norm_dims_t* d) {
+    return align_up((size_t)norm_parts((int)d->rows, d->hidden) * 2 * d->hidden * sizeof(float));
+}
+
+NormParams norm_params(const inkling_norm_dims_t* d) {
+    NormParams p = {};
+    p.dtype = d->dtype == INKLING_BF16 ? 1 : 0;
+    p.rms = d->kind == INKLING_NORM_RMS;
+    p.rows = (int)d->rows;
+    p.H = d->hidden;
+    p.eps = d->eps;
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int inkling_swiglu_checkpoint_size(const inkling_swiglu_dims_t* dims, size_t* bytes) {
+    const int rc = check_swiglu_dims(dims);
+    if (rc != INKLING_OK) return rc;
+    if (bytes == nullptr) return INKLING_ERR_INVALID_ARGUMENT;
+    *bytes = swiglu_checkpoint_bytes(dims);
+    return INKLING_OK;
+}
+
+int inkling_swiglu_forward(const inkling_swiglu_dims_t* dims, const void* h, const float* gamma,
+                           const int32_t* row_count, void* act, void* checkpoint, size_t checkpoint_bytes,
+                           void* stream) {
+    const int rc = check_swiglu_dims(dims);
+    if (rc != INKLING_OK) return rc;
+    if (dims->rows == 0) return INKLING_OK;
+    if (h == nullptr || act == nullptr || act == h || checkpoint == h || checkpoint == act)
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (!aligned(h, 16) || !aligned(act, 16) || !aligned(checkpoint, 16) || !aligned(gamma, 4) ||
+        !aligned(row_count, 4))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (checkpoint != nullptr && checkpoint_bytes < swiglu_checkpoint_bytes(dims)) return INKLING_ERR_WORKSPACE;
+    SwigluParams p = swiglu_params(dims, gamma, row_count, checkpoint);
+    p.h = h;
+    p.act = act;
+    HIP_TRY(launch_swiglu_forward(p, (hipStream_t)stream));
+    return INKLING_OK;
+}
+
+int inkling_swiglu_backward(const inkling_swiglu_dims_t* dims, const void* dact, const void* checkpoint,
+                            size_t checkpoint_bytes, const float* gamma, const int32_t* row_count, void* dh,
+                            void* act, float* dgamma, void* stream) {
+    const int rc = check_swiglu_dims(dims);
+    if (rc != INKLING_OK) return rc;
+    if (dims->rows == 0) return INKLING_OK;
+    if (dact == nullptr || checkpoint == nullptr || dh == nullptr || dh == dact || dh == checkpoint || act == dact ||
+        act == dh || act == checkpoint || (dgamma != nullptr && (dgamma == gamma || dgamma == dh || dgamma == act)))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (!aligned(dact, 16) || !aligned(checkpoint, 16) || !aligned(dh, 16) || !aligned(act, 16) ||
+        !aligned(gamma, 4) || !aligned(dgamma, 4) || !aligned(row_count, 4))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (checkpoint_bytes < swiglu_checkpoint_bytes(dims)) return INKLING_ERR_WORKSPACE;
+    SwigluParams p = swiglu_params(dims, gamma, row_count, const_cast<void*>(checkpoint));
+    p.dact = dact;
+    p.dh = dh;
+    p.act = act;
+    p.dgamma = dgamma;
+    HIP_TRY(launch_swiglu_backward(p, (hipStream_t)stream));
+    return INKLING_OK;
+}
+
+int inkling_norm_forward(const inkling_norm_dims_t* dims, const void* x, const float* weight, const float* bias,
+                         void* out, float* stats, void* stream) {
+    const int rc = check_norm_dims(dims);
+    if (rc != INKLING_OK) return rc;
+    if (dims->rows == 0) return INKLING_OK;
+    if (x == nullptr || weight == nullptr || out == nullptr || out == x) return INKLING_ERR_INVALID_ARGUMENT;
+    if (dims->kind == INKLING_NORM_RMS && bias != nullptr) return INKLING_ERR_INVALID_ARGUMENT;
+    if (!aligned(x, 16) || !aligned(out, 16) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(stats, 16))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    NormParams p = norm_params(dims);
+    p.x = x;
+    p.weight = weight;
+    p.bias = bias;
+    p.out = out;
+    p.stats_out = stats;
+    HIP_TRY(launch_norm_forward(p, (hipStream_t)stream));
+    return INKLING_OK;
+}
+
+int inkling_norm_backward_workspace_size(const inkling_norm_dims_t* dims, size_t* bytes) {
+    const int rc = check_norm_dims(dims);
+    if (rc != INKLING_OK) return rc;
+    if (bytes == nullptr) return INKLING_ERR_INVALID_ARGUMENT;
+    *bytes = norm_part_bytes(dims);
+    return INKLING_OK;
+}
+
+int inkling_norm_backward(const inkling_norm_dims_t* dims, const void* dout, const void* x, const float* weight,
+                          const float* stats, void* dx, float* dweight, float* dbias, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    const int rc = check_norm_dims(dims);
+    if (rc != INKLING_OK) return rc;
+    if (weight == nullptr || dweight == nullptr || dweight == dbias || dweight == weight)
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (dims->rows > 0 &&
+        (dout == nullptr || x == nullptr || stats == nullptr || dx == nullptr || dx == dout || dx == x))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (dims->kind == INKLING_NORM_RMS && dbias != nullptr) return INKLING_ERR_INVALID_ARGUMENT;
+    if (!aligned(dout, 16) || !aligned(x, 16) || !aligned(weight, 16) || !aligned(stats, 16) || !aligned(dx, 16) ||
+        !aligned(dweight, 16) || !aligned(dbias, 16))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (workspace == nullptr || workspace_bytes < norm_part_bytes(dims)) return INKLING_ERR_WORKSPACE;
+    NormParams p = norm_params(dims);
+    p.dout = dout;
+    p.x = x;
+    p.weight = weight;
+    p.stats = stats;
+    p.dx = dx;
+    p.dweight = dweight;
+    p.dbias = dbias;
+    p.part = static_cast<float*>(workspace);
+    HIP_TRY(launch_norm_backward(p, (hipStream_t)stream));
+    return INKLING_OK;
+}
+
 const char* inkling_moe_strerror(int code) {
     switch (code) {
         case INKLING_OK: return "success";

@@ -197,6 +197,45 @@ hipError_t launch_group_gather(int dtype, const void* src, int src_rows, const i
 hipError_t launch_group_wgrad(const GroupParams& p, const void* x, const void* dout, int n_in, int n_out, void* dw,
                               int dw_bf16, hipStream_t stream);
 
+// ---- SwiGLU with its input kept in 8 bits (swiglu.hip) ------------------------
+struct SwigluParams {
+    int dtype;                  // 0 f32, 1 bf16: h, act, dact, dh
+    int rows, I;                // I a multiple of 16
+    const int32_t* row_count;   // rows in use, on the device (NULL: all)
+    const float* gamma;         // [rows] (NULL: 1)
+    const void* h;              // forward: [rows][2I]
+    const void* dact;           // backward: [rows][I]
+    int8_t* kept;               // [rows][2I] (forward: NULL keeps nothing)
+    uint8_t* exps;              // [rows][I / 16]
+    void* act;                  // [rows][I] (backward: NULL skips it)
+    void* dh;                   // [rows][2I]
+    float* dgamma;              // [rows] (NULL skips it)
+};
+hipError_t launch_swiglu_forward(const SwigluParams& p, hipStream_t stream);
+hipError_t launch_swiglu_backward(const SwigluParams& p, hipStream_t stream);
+
+// ---- layer norm and RMS norm (norm.hip) ---------------------------------------
+struct NormParams {
+    int dtype;             // 0 f32, 1 bf16: x, out, dout, dx
+    bool rms;
+    int rows, H;           // H at most 16384
+    float eps;
+    const void* x;
+    const float* weight;   // [H]
+    const float* bias;     // [H] or NULL
+    void* out;
+    float* stats_out;      // [rows][2] mean, 1 / sqrt(variance + eps), or NULL
+    const void* dout;
+    const float* stats;
+    void* dx;
+    float* dweight;        // [H]
+    float* dbias;          // [H] or NULL
+    float* part;           // [norm_parts()][dbias ? 2 : 1][H]
+};
+int norm_parts(int rows, int H);
+hipError_t launch_norm_forward(const NormParams& p, hipStream_t stream);
+hipError_t launch_norm_backward(const NormParams& p, hipStream_t stream);
+
 // gamma[t] = value for t < T; the GEMM round counters zeroed (the dense MLP's
 // stand-in for the router and the permutation)
 hipError_t launch_dense_prep(float* gamma, int T, float value, int32_t* round_counters, hipStream_t stream);

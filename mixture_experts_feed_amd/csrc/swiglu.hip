@@ -1,0 +1,203 @@
+// SwiGLU between an expert's two projections with its input kept in 8 bits.
+//
+// h [R][2I] holds [g0, u0, g1, u1, ...]; act = gamma g sigmoid(g) u.  For the
+// backward pass h is kept as one byte a value: 32 consecutive columns share a
+// power of two 2^e, the smallest (e >= -126) with max|h| <= 127 2^e, and each
+// value is the int8 nearest to h / 2^e (ties to even), off by at most 2^(e-1),
+// that is max|h| / 127 of its block.  A power of two makes h / 2^e and q 2^e
+// exact, so that the kept values do not depend on how a quotient is rounded.
+// The exponent is a byte, e + 127; 255 marks a block with an infinity or a NaN,
+// whose values come back as NaN.
+// The backward pass takes g and u from the bytes:
+//   s = sigmoid(g), p = g s u:  a = gamma p,  dgamma = sum over I of dact p,
+//   dg = gamma dact u s (1 + g (1 - s)),  du = gamma dact g s.
+//
+// Both passes are one read of their inputs and one write of their outputs, so
+// HBM bounds them: per row of I columns bf16 moves 8 I bytes forward (4 I in,
+// 2 I + 2 I out) and 10 I backward (2 I + 2 I in, 4 I + 2 I out).  A lane holds
+// 16 columns (8 pairs): 16-byte accesses to the bytes and to bf16 act.
+#include <algorithm>
+
+#include "common.h"
+#include "kernels.h"
+#include "vec.h"
+
+namespace inkling {
+
+namespace {
+
+constexpr int kCols = 16;   // columns of h a lane holds; two lanes share an exponent
+
+// bf16 rows take the hardware exponential and reciprocal (a relative error of a
+// few 2^-22 for |v| < 40, far below bf16's half step 2^-8); fp32 rows the
+// library exponential and a division.
+template <typename TE>
+__device__ __forceinline__ float sigmoid_of(float v) {
+    if constexpr (sizeof(TE) == 2) return __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+    else return 1.0f / (1.0f + expf(-v));
+}
+
+template <typename TE, int N>
+__device__ __forceinline__ void load_cols(const TE* p, float* v) {
+    constexpr int V = 16 / sizeof(TE);
+#pragma unroll
+    for (int i = 0; i < N; i += V) widen(load_raw<TE, V>(p + i), v + i);
+}
+
+// Kept byte of the exponent for a block whose largest |h| has these bits.
+// Adding 0x1FFFF carries into the exponent exactly when the significand passes
+// 127/64 = 1.1111110b, the largest that 127 steps of 2^(exponent - 6) hold.
+__device__ __forceinline__ int exponent_byte(uint32_t top) {
+    if (top >= 0x7F800000u) return 255;
+    return max((int)((top + 0x1FFFFu) >> 23) - 6, 1);
+}
+
+template <typename TE>
+__global__ __launch_bounds__(256) void swiglu_forward_kernel(const TE* __restrict__ h, const float* __restrict__ gamma,
+                                                             const int32_t* __restrict__ row_count, int row0, int rows,
+                                                             int I, TE* __restrict__ act, int8_t* __restrict__ kept,
+                                                             uint8_t* __restrict__ exps) {
+    const int end = row_count != nullptr ? max(0, min(rows, *row_count - row0)) : rows;
+    const uint32_t per_row = (uint32_t)I / 8;                 // lanes a row takes
+    const uint32_t total = (uint32_t)end * per_row;           // < 2^31 (launcher)
+    for (uint32_t c = blockIdx.x * 256 + threadIdx.x; c < total; c += gridDim.x * 256) {
+        const size_t row = row0 + c / per_row;
+        const int col = (int)(c % per_row);                   // 16 columns of h, 8 of act
+        const size_t at = row * 2 * I + (size_t)col * kCols;
+        float v[kCols];
+        load_cols<TE, kCols>(h + at, v);
+        const float gm = gamma != nullptr ? gamma[row] : 1.0f;
+        float a[kCols / 2];
+#pragma unroll
+        for (int i = 0; i < kCols / 2; ++i) a[i] = gm * (v[2 * i] * sigmoid_of<TE>(v[2 * i]) * v[2 * i + 1]);
+        store_vec<TE, kCols / 2>(act + row * I + (size_t)col * (kCols / 2), a);
+        if (kept != nullptr) {
+            uint32_t top = 0;   // integer order of |h|: NaN above infinity
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+            top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+            const int e = exponent_byte(top);
+            const float inv = e == 255 ? 0.0f : __uint_as_float((uint32_t)(254 - e) << 23);
+            // h / 2^e + 1.5 2^23 rounds to an integer, nearest even, whose low
+            // byte is the int8
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(__builtin_fmaf(v[4 * j + i], inv, 12582912.0f));
+                w[j] = (b[0] & 0xFFu) | (b[1] & 0xFFu) << 8 | (b[2] & 0xFFu) << 16 | b[3] << 24;
+            }
+            *reinterpret_cast<uint4*>(kept + at) = make_uint4(w[0], w[1], w[2], w[3]);
+            if ((col & 1) == 0) exps[row * (size_t)(I / 16) + (col >> 1)] = (uint8_t)e;
+        }
+    }
+}
+
+// G lanes a row (a row's lanes are neighbours in a wave): dgamma is the sum of
+// a fixed order over a lane's columns, then over the lanes.
+template <typename TE, int G>
+__global__ __launch_bounds__(256) void swiglu_backward_kernel(
+    const TE* __restrict__ dact, const int8_t* __restrict__ kept, const uint8_t* __restrict__ exps,
+    const float* __restrict__ gamma, const int32_t* __restrict__ row_count, int rows, int I, TE* __restrict__ dh,
+    TE* __restrict__ act, float* __restrict__ dgamma) {
+    const int end = row_count != nullptr ? max(0, min(rows, *row_count)) : rows;
+    const int sub = threadIdx.x % G, per_row = I / 8;
+    constexpr int kRows = 256 / G;
+    for (long long r = (long long)blockIdx.x * kRows + threadIdx.x / G; r < end; r += (long long)gridDim.x * kRows) {
+        const size_t row = (size_t)r;
+        const float gm = gamma != nullptr ? gamma[row] : 1.0f;
+        float part = 0.0f;
+        for (int col = sub; col < per_row; col += G) {
+            const size_t at = row * 2 * I + (size_t)col * kCols;
+            const uint4 q = *reinterpret_cast<const uint4*>(kept + at);
+            const int e = exps[row * (size_t)(I / 16) + (col >> 1)];
+            const float scale = __uint_as_float(e == 255 ? 0x7FC00000u : (uint32_t)e << 23);
+            float da[kCols / 2];
+            load_cols<TE, kCols / 2>(dact + row * I + (size_t)col * (kCols / 2), da);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            float dv[kCols], av[kCols / 2];
+#pragma unroll
+            for (int i = 0; i < kCols / 2; ++i) {
+                const uint32_t pair = w[i >> 1] >> (16 * (i & 1));
+                const float g = (float)(int8_t)(pair & 0xFFu) * scale;
+                const float u = (float)(int8_t)((pair >> 8) & 0xFFu) * scale;
+                const float s = sigmoid_of<TE>(g);
+                const float si = g * s, p = si * u;
+                const float dp = gm * da[i];
+                part += da[i] * p;
+                av[i] = gm * p;
+                dv[2 * i] = dp * u * s * (1.0f + g * (1.0f - s));
+                dv[2 * i + 1] = dp * si;
+            }
+            store_vec<TE, kCols>(dh + at, dv);
+            if (act != nullptr) store_vec<TE, kCols / 2>(act + row * I + (size_t)col * (kCols / 2), av);
+        }
+        if (dgamma != nullptr) {
+#pragma unroll
+            for (int d = 1; d < G; d <<= 1) part += __shfl_xor(part, d);
+            if (sub == 0) dgamma[row] = part;
+        }
+    }
+}
+
+// Lanes a row: the width that leaves the fewest lanes without columns, the
+// larger of equals (fewer steps a row).
+int lanes_per_row(int per_row) {
+    int best = 8;
+    double most = 0.0;
+    for (int g = 8; g <= 64; g *= 2) {
+        const double used = (double)per_row / ((per_row + g - 1) / g * g);
+        if (used >= most) {
+            most = used;
+            best = g;
+        }
+    }
+    return best;
+}
+
+template <typename TE>
+hipError_t backward_typed(const SwigluParams& p, hipStream_t stream) {
+    const int G = lanes_per_row(p.I / 8);
+    const long long blocks = ((long long)p.rows * G + 255) / 256;
+    const dim3 grid((unsigned)std::min<long long>(blocks, (long long)device_cu_count() * 32));
+    auto go = [&](auto g) {
+        constexpr int kG = decltype(g)::value;
+        hipLaunchKernelGGL((swiglu_backward_kernel<TE, kG>), grid, dim3(256), 0, stream,
+                           static_cast<const TE*>(p.dact), p.kept, p.exps, p.gamma, p.row_count, p.rows, p.I,
+                           static_cast<TE*>(p.dh), static_cast<TE*>(p.act), p.dgamma);
+    };
+    if (G == 64) go(std::integral_constant<int, 64>{});
+    else if (G == 32) go(std::integral_constant<int, 32>{});
+    else if (G == 16) go(std::integral_constant<int, 16>{});
+    else go(std::integral_constant<int, 8>{});
+    return hipGetLastError();
+}
+
+template <typename TE>
+hipError_t forward_typed(const SwigluParams& p, hipStream_t stream) {
+    // bands of rows whose lanes a 32-bit index counts (with room for the stride)
+    const int band = std::max(1, (int)((1u << 30) / (unsigned)(p.I / 8)));
+    for (int row0 = 0; row0 < p.rows; row0 += std::min(band, p.rows - row0)) {
+        const int n = std::min(band, p.rows - row0);
+        const long long blocks = ((long long)n * (p.I / 8) + 255) / 256;
+        const dim3 grid((unsigned)std::min<long long>(blocks, (long long)device_cu_count() * 32));
+        hipLaunchKernelGGL(swiglu_forward_kernel<TE>, grid, dim3(256), 0, stream, static_cast<const TE*>(p.h), p.gamma,
+                           p.row_count, row0, n, p.I, static_cast<TE*>(p.act), p.kept, p.exps);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_swiglu_forward(const SwigluParams& p, hipStream_t stream) {
+    return p.dtype == 1 ? forward_typed<bf16_t>(p, stream) : forward_typed<float>(p, stream);
+}
+
+hipError_t launch_swiglu_backward(const SwigluParams& p, hipStream_t stream) {
+    return p.dtype == 1 ? backward_typed<bf16_t>(p, stream) : backward_typed<float>(p, stream);
+}
+
+}  // namespace inkling

@@ -94,3 +94,92 @@ def test_grouped_no_rows_is_a_noop(lib):
     d = _grouped(rows=0, x_rows=0)
     assert lib.inkling_grouped_linear(ctypes.byref(d), None, None, None, None, None, None, 0, None) == B.INKLING_OK
     assert lib.inkling_grouped_input_grad(ctypes.byref(d), None, None, None, None, None, 0, None) == B.INKLING_OK
+
+
+def _swiglu(**kw):
+    d = dict(rows=100, intermediate=64, dtype=B.INKLING_BF16) | kw
+    return B.SwigluDims(d["rows"], d["intermediate"], d["dtype"])
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), B.INKLING_ERR_INVALID_ARGUMENT),
+    (dict(intermediate=0), B.INKLING_ERR_INVALID_ARGUMENT),
+    (dict(intermediate=24), B.INKLING_ERR_UNSUPPORTED),
+    (dict(intermediate=(1 << 20) + 16), B.INKLING_ERR_UNSUPPORTED),
+    (dict(dtype=2), B.INKLING_ERR_UNSUPPORTED),
+    (dict(rows=2 ** 31), B.INKLING_ERR_UNSUPPORTED),
+])
+def test_swiglu_dims(lib, kw, code):
+    d, n = _swiglu(**kw), ctypes.c_size_t(0)
+    assert lib.inkling_swiglu_checkpoint_size(ctypes.byref(d), ctypes.byref(n)) == code
+    assert lib.inkling_swiglu_forward(ctypes.byref(d), FAKE, None, None, FAKE2, FAKE3, BIG, None) == code
+    assert lib.inkling_swiglu_backward(ctypes.byref(d), FAKE, FAKE2, BIG, None, None, FAKE3, None, None, None) == code
+
+
+def test_swiglu_pointers(lib):
+    d, n = _swiglu(), ctypes.c_size_t(0)
+    bad = B.INKLING_ERR_INVALID_ARGUMENT
+    assert lib.inkling_swiglu_checkpoint_size(ctypes.byref(d), None) == bad
+    assert lib.inkling_swiglu_checkpoint_size(ctypes.byref(d), ctypes.byref(n)) == 0
+    assert n.value == 100 * 128 + 100 * 4
+    fwd = lambda h=FAKE, g=None, c=None, act=FAKE2, ck=FAKE3, size=n.value: lib.inkling_swiglu_forward(  # noqa: E731
+        ctypes.byref(d), h, g, c, act, ck, size, None)
+    for kw in (dict(h=None), dict(act=None), dict(act=FAKE), dict(ck=FAKE), dict(ck=FAKE2), dict(h=ODD),
+               dict(act=ODD), dict(ck=ODD), dict(g=FAKE + 2), dict(c=FAKE + 1)):
+        assert fwd(**kw) == bad, kw
+    assert fwd(size=n.value - 1) == B.INKLING_ERR_WORKSPACE
+    bwd = lambda da=FAKE, ck=FAKE2, size=n.value, g=None, dh=FAKE3, act=None, dg=None: (  # noqa: E731
+        lib.inkling_swiglu_backward(ctypes.byref(d), da, ck, size, g, None, dh, act, dg, None))
+    for kw in (dict(da=None), dict(ck=None), dict(dh=None), dict(dh=FAKE), dict(dh=FAKE2), dict(act=FAKE),
+               dict(act=FAKE2), dict(act=FAKE3), dict(da=ODD), dict(ck=ODD), dict(dh=ODD), dict(act=ODD),
+               dict(dg=FAKE3), dict(g=0x50000, dg=0x50000), dict(dg=0x50002)):
+        assert bwd(**kw) == bad, kw
+    assert bwd(size=n.value - 1) == B.INKLING_ERR_WORKSPACE
+    e = _swiglu(rows=0)
+    assert lib.inkling_swiglu_forward(ctypes.byref(e), None, None, None, None, None, 0, None) == B.INKLING_OK
+    assert lib.inkling_swiglu_backward(ctypes.byref(e), None, None, 0, None, None, None, None, None,
+                                       None) == B.INKLING_OK
+
+
+def _norm(**kw):
+    d = dict(rows=100, hidden=64, kind=B.INKLING_NORM_LAYER, dtype=B.INKLING_BF16, eps=1e-6) | kw
+    return B.NormDims(d["rows"], d["hidden"], d["kind"], d["dtype"], d["eps"])
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), B.INKLING_ERR_INVALID_ARGUMENT),
+    (dict(hidden=0), B.INKLING_ERR_INVALID_ARGUMENT),
+    (dict(eps=-1e-6), B.INKLING_ERR_INVALID_ARGUMENT),
+    (dict(eps=float("nan")), B.INKLING_ERR_INVALID_ARGUMENT),
+    (dict(eps=float("inf")), B.INKLING_ERR_INVALID_ARGUMENT),
+    (dict(kind=2), B.INKLING_ERR_UNSUPPORTED),
+    (dict(dtype=2), B.INKLING_ERR_UNSUPPORTED),
+    (dict(hidden=16385), B.INKLING_ERR_UNSUPPORTED),
+    (dict(rows=2 ** 31 - 65536), B.INKLING_ERR_UNSUPPORTED),
+])
+def test_norm_dims(lib, kw, code):
+    d, n = _norm(**kw), ctypes.c_size_t(0)
+    assert lib.inkling_norm_backward_workspace_size(ctypes.byref(d), ctypes.byref(n)) == code
+    assert lib.inkling_norm_forward(ctypes.byref(d), FAKE, FAKE, None, FAKE2, None, None) == code
+    assert lib.inkling_norm_backward(ctypes.byref(d), FAKE, FAKE, FAKE, FAKE, FAKE2, FAKE3, None, FAKE, BIG,
+                                     None) == code
+
+
+def test_norm_pointers(lib):
+    d, r, n = _norm(), _norm(kind=B.INKLING_NORM_RMS), ctypes.c_size_t(0)
+    bad = B.INKLING_ERR_INVALID_ARGUMENT
+    fwd = lambda x=FAKE, w=FAKE3, b=None, out=FAKE2, st=None, dd=d: lib.inkling_norm_forward(  # noqa: E731
+        ctypes.byref(dd), x, w, b, out, st, None)
+    for kw in (dict(x=None), dict(w=None), dict(out=None), dict(out=FAKE), dict(x=ODD), dict(w=ODD), dict(b=ODD),
+               dict(out=ODD), dict(st=ODD), dict(dd=r, b=FAKE)):
+        assert fwd(**kw) == bad, kw
+    assert lib.inkling_norm_backward_workspace_size(ctypes.byref(d), ctypes.byref(n)) == 0
+    bwd = lambda dy=FAKE, x=FAKE2, w=FAKE3, st=FAKE, dx=0x40000, dw=0x50000, db=None, ws=FAKE, size=n.value, dd=d: (  # noqa: E731
+        lib.inkling_norm_backward(ctypes.byref(dd), dy, x, w, st, dx, dw, db, ws, size, None))
+    for kw in (dict(dy=None), dict(x=None), dict(w=None), dict(st=None), dict(dx=None), dict(dw=None), dict(dx=FAKE),
+               dict(dx=FAKE2), dict(db=0x50000), dict(dw=FAKE3), dict(dy=ODD), dict(x=ODD), dict(dx=ODD),
+               dict(dw=0x50008), dict(db=0x60008), dict(dd=r, db=0x60000)):
+        assert bwd(**kw) == bad, kw
+    assert bwd(ws=None) == B.INKLING_ERR_WORKSPACE
+    assert bwd(size=n.value - 1) == B.INKLING_ERR_WORKSPACE
+    assert lib.inkling_norm_forward(ctypes.byref(_norm(rows=0)), None, None, None, None, None, None) == B.INKLING_OK

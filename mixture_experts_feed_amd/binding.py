@@ -194,7 +194,13 @@ def workspace_size(dims: Dims) -> int:
     return int(n.value)
 
 
+# the stream's handle without a Stream object around it, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -481,6 +487,18 @@ def _same_device(dev, **tensors) -> None:
             raise ValueError(f"{n} must be on {dev}, got {t.device}")
 
 
+def _call(dev, name: str, *args) -> None:
+    """The entry point `name` on dev's current stream, with dev the current device."""
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(dev))
+    if rc != INKLING_OK:
+        raise InklingError(rc, name)
+
+
 def make_grouped_dims(rows, x_rows, n_groups, in_features, out_features, dtype, out_dtype=None) -> GroupedDims:
     code = dtype if isinstance(dtype, int) else _dtype_code(dtype)
     ocode = code if out_dtype is None else (out_dtype if isinstance(out_dtype, int) else _dtype_code(out_dtype))
@@ -558,11 +576,9 @@ def grouped_linear(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
     out_dtype = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
     dims = make_grouped_dims(R, x.shape[0], E, K, N, x.dtype, out_dtype)
     out = _result(out, "out", (R, N), out_dtype, dev)
-    with torch.cuda.device(dev):
-        ws = _scratch(workspace, grouped_workspace_size(dims), dev)
-        _check(load().inkling_grouped_linear(ctypes.byref(dims), x.data_ptr(), _ptr(row_index), weight.data_ptr(),
-                                             offsets.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(),
-                                             _stream(dev)), "inkling_grouped_linear")
+    ws = _scratch(workspace, grouped_workspace_size(dims), dev)
+    _call(dev, "inkling_grouped_linear", ctypes.byref(dims), x.data_ptr(), _ptr(row_index), weight.data_ptr(),
+          offsets.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
@@ -576,11 +592,9 @@ def grouped_input_grad(dout: torch.Tensor, weight: torch.Tensor, offsets: torch.
     dx_dtype = dx.dtype if dx is not None else dout.dtype if dx_dtype is None else dx_dtype
     dims = make_grouped_dims(R, R, E, K, N, dout.dtype, dx_dtype)
     dx = _result(dx, "dx", (R, K), dx_dtype, dev)
-    with torch.cuda.device(dev):
-        ws = _scratch(workspace, grouped_workspace_size(dims), dev)
-        _check(load().inkling_grouped_input_grad(ctypes.byref(dims), dout.data_ptr(), weight.data_ptr(),
-                                                 offsets.data_ptr(), dx.data_ptr(), ws.data_ptr(), ws.numel(),
-                                                 _stream(dev)), "inkling_grouped_input_grad")
+    ws = _scratch(workspace, grouped_workspace_size(dims), dev)
+    _call(dev, "inkling_grouped_input_grad", ctypes.byref(dims), dout.data_ptr(), weight.data_ptr(),
+          offsets.data_ptr(), dx.data_ptr(), ws.data_ptr(), ws.numel())
     return dx
 
 
@@ -608,11 +622,9 @@ def grouped_weight_grad(dout: torch.Tensor, x: torch.Tensor, offsets: torch.Tens
         raise ValueError("weight_grad_dtype differs from the dtype of the given dweight")
     dims = make_grouped_dims(R, x.shape[0], E, K, N, x.dtype, wdt)
     dweight = _result(dweight, "dweight", (E, N, K), wdt, dev)
-    with torch.cuda.device(dev):
-        ws = _scratch(workspace, grouped_weight_grad_workspace_size(dims, row_index is not None), dev)
-        _check(load().inkling_grouped_weight_grad(ctypes.byref(dims), dout.data_ptr(), x.data_ptr(), _ptr(row_index),
-                                                  offsets.data_ptr(), dweight.data_ptr(), ws.data_ptr(), ws.numel(),
-                                                  _stream(dev)), "inkling_grouped_weight_grad")
+    ws = _scratch(workspace, grouped_weight_grad_workspace_size(dims, row_index is not None), dev)
+    _call(dev, "inkling_grouped_weight_grad", ctypes.byref(dims), dout.data_ptr(), x.data_ptr(), _ptr(row_index),
+          offsets.data_ptr(), dweight.data_ptr(), ws.data_ptr(), ws.numel())
     return dweight
 
 
@@ -664,11 +676,8 @@ def swiglu_forward(h: torch.Tensor, gamma: Optional[torch.Tensor] = None, row_co
         raise ValueError("save=False keeps no checkpoint: give none")
     if save:
         checkpoint = _scratch(checkpoint, need, dev)
-    with torch.cuda.device(dev):
-        _check(load().inkling_swiglu_forward(ctypes.byref(dims), h.data_ptr(), _ptr(gamma), _ptr(row_count),
-                                             out.data_ptr(), _ptr(checkpoint),
-                                             0 if checkpoint is None else checkpoint.numel(), _stream(dev)),
-               "inkling_swiglu_forward")
+    _call(dev, "inkling_swiglu_forward", ctypes.byref(dims), h.data_ptr(), _ptr(gamma), _ptr(row_count),
+          out.data_ptr(), _ptr(checkpoint), 0 if checkpoint is None else checkpoint.numel())
     return out, checkpoint
 
 
@@ -691,14 +700,11 @@ def swiglu_backward(dact: torch.Tensor, checkpoint: torch.Tensor, gamma: Optiona
     if (act is not None and not want_act) or (dgamma is not None and not want_dgamma):
         raise ValueError("a result is both given and not wanted")
     dims = make_swiglu_dims(R, I, dact.dtype)
-    swiglu_checkpoint_size(dims)   # the limits, before anything is allocated
     dh = _result(dh, "dh", (R, 2 * I), dact.dtype, dev)
     act = _result(act, "act", (R, I), dact.dtype, dev) if want_act else None
     dgamma = _result(dgamma, "dgamma", (R,), torch.float32, dev) if want_dgamma else None
-    with torch.cuda.device(dev):
-        _check(load().inkling_swiglu_backward(ctypes.byref(dims), dact.data_ptr(), checkpoint.data_ptr(),
-                                              checkpoint.numel(), _ptr(gamma), _ptr(row_count), dh.data_ptr(),
-                                              _ptr(act), _ptr(dgamma), _stream(dev)), "inkling_swiglu_backward")
+    _call(dev, "inkling_swiglu_backward", ctypes.byref(dims), dact.data_ptr(), checkpoint.data_ptr(),
+          checkpoint.numel(), _ptr(gamma), _ptr(row_count), dh.data_ptr(), _ptr(act), _ptr(dgamma))
     return {"dh": dh, "act": act, "dgamma": dgamma}
 
 
@@ -728,7 +734,7 @@ def _norm_checks(x, weight, bias):
     for t, n in ((weight, "weight"), (bias, "bias")):
         if t is not None:
             _need(t, n, torch.float32)
-            if t.shape != (x.shape[1],):
+            if t.dim() != 1 or t.shape[0] != x.shape[1]:
                 raise ValueError(f"{n} must have shape ({x.shape[1]},)")
     _same_device(x.device, weight=weight, bias=bias)
 
@@ -743,14 +749,12 @@ def norm_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Ten
     R, H = x.shape
     dev = x.device
     dims = make_norm_dims(R, H, kind, x.dtype, eps)
-    norm_backward_workspace_size(dims)   # the limits, before anything is allocated
     out = _result(out, "out", (R, H), x.dtype, dev)
     if not save and stats is not None:
         raise ValueError("save=False keeps no stats: give none")
     stats = _result(stats, "stats", (R, 2), torch.float32, dev) if save else None
-    with torch.cuda.device(dev):
-        _check(load().inkling_norm_forward(ctypes.byref(dims), x.data_ptr(), weight.data_ptr(), _ptr(bias),
-                                           out.data_ptr(), _ptr(stats), _stream(dev)), "inkling_norm_forward")
+    _call(dev, "inkling_norm_forward", ctypes.byref(dims), x.data_ptr(), weight.data_ptr(), _ptr(bias),
+          out.data_ptr(), _ptr(stats))
     return out, stats
 
 
@@ -774,8 +778,6 @@ def norm_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, sta
     dx = _result(dx, "dx", (R, H), x.dtype, dev)
     dweight = _result(dweight, "dweight", (H,), torch.float32, dev)
     dbias = _result(dbias, "dbias", (H,), torch.float32, dev) if bias or dbias is not None else None
-    with torch.cuda.device(dev):
-        _check(load().inkling_norm_backward(ctypes.byref(dims), dout.data_ptr(), x.data_ptr(), weight.data_ptr(),
-                                            stats.data_ptr(), dx.data_ptr(), dweight.data_ptr(), _ptr(dbias),
-                                            ws.data_ptr(), ws.numel(), _stream(dev)), "inkling_norm_backward")
+    _call(dev, "inkling_norm_backward", ctypes.byref(dims), dout.data_ptr(), x.data_ptr(), weight.data_ptr(),
+          stats.data_ptr(), dx.data_ptr(), dweight.data_ptr(), _ptr(dbias), ws.data_ptr(), ws.numel())
     return {"dx": dx, "dweight": dweight, "dbias": dbias}

@@ -887,7 +887,7 @@ int check_norm_dims(const inkling_norm_dims_t* d) {
 
 // partial rows of dweight and dbias
 size_t norm_part_bytes(const inkling_norm_dims_t* d) {
-    return align_up((size_t)norm_parts((int)d->rows, d->hidden) * 2 * d->hidden * sizeof(float));
+    return align_up((size_t)norm_parts(d->dtype == INKLING_BF16 ? 1 : 0, (int)d->rows, d->hidden) * 2 * d->hidden * sizeof(float));
 }
 
 NormParams norm_params(const inkling_norm_dims_t* d) {

@@ -232,7 +232,7 @@ struct NormParams {
     float* dbias;          // [H] or NULL
     float* part;           // [norm_parts()][dbias ? 2 : 1][H]
 };
-int norm_parts(int rows, int H);
+int norm_parts(int dtype, int rows, int H);
 hipError_t launch_norm_forward(const NormParams& p, hipStream_t stream);
 hipError_t launch_norm_backward(const NormParams& p, hipStream_t stream);
 

@@ -7,11 +7,20 @@
 //
 // HBM bounds both passes: x is read once and kept in registers for the second
 // moment about the mean (two passes over registers, so a large mean costs no
-// digits), the result is written once.  A workgroup walks rows with its columns
-// of w and b in registers, and loads the next row before the sums of the
-// current one.  The backward pass keeps its columns' sums of dw and db in
-// registers over all its rows and writes one partial row for each workgroup;
-// a second kernel adds the partial rows in order, so results repeat bit for bit.
+// digits), the result is written once.
+//
+// A row is held in 16-byte vectors, one a lane where the width allows: rows of
+// up to 64 vectors by 8 to 64 neighbouring lanes of a wave (no LDS), wider ones
+// by a workgroup with as many waves as they need (up to 1024 lanes, then up to
+// 512 with 4 or 8 vectors each).  One vector a lane keeps the registers few, so that several
+// workgroups a CU hide each other's sums.  Rows that are not whole vectors are
+// read with the same accesses at their own alignment, the last partial vector
+// value by value.  Lanes walk rows with their columns of w and b in registers
+// and load the next row before the sums of the current one.
+// The backward pass keeps its columns' sums of dw and db in registers over all
+// its rows and writes one partial row for each workgroup (narrow rows: each
+// wave); a second kernel adds the partial rows in order, so results repeat bit
+// for bit.
 #include <algorithm>
 
 #include "common.h"
@@ -22,174 +31,275 @@ namespace inkling {
 
 namespace {
 
-// Sums over a workgroup of TPR threads (one wave: no LDS).  `buf` alternates
-// from call to call, so one barrier a sum is enough.
-template <int TPR, int N>
-__device__ __forceinline__ void block_sums(float (&v)[N], float (*buf)[N]) {
+constexpr int kMaxWaves = 16;
+// one vector a lane up to 1024 lanes; several a lane need the registers of 512
+template <int NV, int G>
+constexpr int max_threads() { return G != 0 ? 256 : NV == 1 ? 1024 : 512; }
+
+// Sums over the lanes that hold a row: G lanes of a wave (G < 64 or one wave),
+// or G == 0: the workgroup.  `buf` alternates from call to call, so that one
+// barrier a sum is enough; the waves' sums are added in order.
+template <int G, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*buf)[N]) {
+    constexpr int L = G == 0 ? kWave : G;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-    if constexpr (TPR > kWave) {
-        const int wv = threadIdx.x >> 6;
+    for (int i = 0; i < N; ++i) v[i] = lanes_sum<L>(v[i]);
+    if constexpr (G == 0) {
         if (lane_id() == 0)
 #pragma unroll
-            for (int i = 0; i < N; ++i) buf[wv][i] = v[i];
+            for (int i = 0; i < N; ++i) buf[threadIdx.x >> 6][i] = v[i];
         __syncthreads();
+        const int waves = blockDim.x >> 6;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            v[i] = buf[0][i];
+        for (int i = 0; i < N; ++i) v[i] = buf[0][i];
+        for (int w = 1; w < waves; ++w)
 #pragma unroll
-            for (int w = 1; w < TPR / kWave; ++w) v[i] += buf[w][i];
-        }
+            for (int i = 0; i < N; ++i) v[i] += buf[w][i];
     }
 }
 
-// V values a vector, NV vectors a thread: vector j of a thread is columns
-// (j TPR + thread) V.
-template <typename TE, int V, int NV, int TPR, bool RMS>
-__global__ __launch_bounds__(TPR) void norm_forward_kernel(const TE* __restrict__ x, const float* __restrict__ w,
-                                                           const float* __restrict__ b, int rows, int H, float eps,
-                                                           TE* __restrict__ out, float* __restrict__ stats) {
-    __shared__ float sums[2][2][TPR / kWave][1];
-    const int nv = H / V, t = threadIdx.x;
-    const float inv_h = 1.0f / (float)H;
-    float wr[NV][V], br[NV][V];
+template <typename TE>
+struct LooseOf;
+template <>
+struct LooseOf<bf16_t> { typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2))); };
+template <>
+struct LooseOf<float> { typedef uint32_t type __attribute__((ext_vector_type(4), aligned(4))); };
+
+// A lane's vectors of a row: vector j is columns (j * lanes + t) V ..
+// TAIL: H is not a multiple of V (nor are rows 16-byte aligned); `last` values
+// of the last vector exist.
+template <typename TE, int NV, bool TAIL>
+struct Row {
+    static constexpr int V = 16 / sizeof(TE);
+    typedef Raw<TE, V> Vec;
+    typedef typename LooseOf<TE>::type Loose;   // the same 16 bytes at the alignment of a value
+    static __device__ __forceinline__ void load(Vec* r, const TE* p, int t, int lanes, int full, int last) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            const int k = j * lanes + t;
+            if constexpr (TAIL) {
+                if (k < full) {
+                    const Loose q = *reinterpret_cast<const Loose*>(p + (size_t)k * V);
+                    __builtin_memcpy(&r[j], &q, sizeof(Vec));
+                } else {
+                    TE e[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const bool in = j * TPR + t < nv;
-            const int col = (j * TPR + t) * V + i;
-            wr[j][i] = in ? w[col] : 0.0f;
-            br[j][i] = in && b != nullptr ? b[col] : 0.0f;
+                    for (int i = 0; i < V; ++i) {
+                        e[i] = TE(0);
+                        if (k == full && i < last) e[i] = p[(size_t)k * V + i];
+                    }
+                    __builtin_memcpy(&r[j], e, sizeof(Vec));
+                }
+            } else {
+                // lanes past the row hold zeros
+                r[j] = Vec{};
+                if (k < full) r[j] = load_raw<TE, V>(p + (size_t)k * V);
+            }
         }
-    Raw<TE, V> cur[NV], nxt[NV];
-    auto load = [&](Raw<TE, V>* r, size_t row) __attribute__((always_inline)) {
+    }
+    static __device__ __forceinline__ void store(TE* p, int j, int t, int lanes, int full, int last, const float* v) {
+        const int k = j * lanes + t;
+        if (k < full) {
+            if constexpr (TAIL) {
+                TE e[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) store_vec<TE, 1>(e + i, v + i);
+                Loose q;
+                __builtin_memcpy(&q, e, sizeof(Vec));
+                *reinterpret_cast<Loose*>(p + (size_t)k * V) = q;
+            } else {
+                store_vec<TE, V>(p + (size_t)k * V, v);
+            }
+        } else if (TAIL && k == full) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < last) store_vec<TE, 1>(p + (size_t)k * V + i, v + i);
+        }
+    }
+    // fp32 columns of w, b or of a partial row
+    static __device__ __forceinline__ void columns(float (*c)[V], const float* p, int t, int lanes, int H) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (j * TPR + t < nv) r[j] = load_raw<TE, V>(x + row * H + (size_t)(j * TPR + t) * V);
-    };
-    int row = blockIdx.x, turn = 0;
-    load(cur, row);
-    for (; row < rows; row += gridDim.x, turn ^= 1) {
-        if (row + (int)gridDim.x < rows) load(nxt, (size_t)row + gridDim.x);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int col = (j * lanes + t) * V + i;
+                c[j][i] = p != nullptr && (TAIL ? col < H : (j * lanes + t) * V < H) ? p[col] : 0.0f;
+            }
+    }
+};
+
+// The row a lane starts with, how far the next one is, and its place in it.
+template <int G>
+struct Place {
+    int t, lanes, row, step;
+    __device__ __forceinline__ Place() {
+        if constexpr (G == 0) {
+            t = threadIdx.x;
+            lanes = blockDim.x;
+            row = blockIdx.x;
+            step = gridDim.x;
+        } else {
+            t = threadIdx.x % G;
+            lanes = G;
+            row = blockIdx.x * (256 / G) + threadIdx.x / G;
+            step = gridDim.x * (256 / G);
+        }
+    }
+};
+
+template <typename TE, int NV, int G, bool TAIL, bool RMS>
+__global__ __launch_bounds__((max_threads<NV, G>())) void norm_forward_kernel(
+    const TE* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, int rows, int H, float eps,
+    TE* __restrict__ out, float* __restrict__ stats) {
+    using R = Row<TE, NV, TAIL>;
+    constexpr int V = R::V;
+    __shared__ float sums[2][2][kMaxWaves][1];
+    const Place<G> at;
+    const int full = H / V, last = H - full * V, t = at.t, lanes = at.lanes;
+    const float n = (float)H;
+    typename R::Vec cur[NV], nxt[NV];
+    int row = at.row;
+    if (row < rows) R::load(cur, x + (size_t)row * H, t, lanes, full, last);
+    float wr[NV][V], br[NV][V];
+    R::columns(wr, w, t, lanes, H);
+    if constexpr (!RMS) R::columns(br, b, t, lanes, H);
+    // (G != 0: the lanes of a row leave together, and no barrier follows)
+    for (int turn = 0; row < rows; row += at.step, turn ^= 1) {
+        if (rows - row > at.step) R::load(nxt, x + ((size_t)row + at.step) * H, t, lanes, full, last);
         float v[NV][V];
         float s[1] = {0.0f};
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (j * TPR + t < nv) {
-                widen(cur[j], v[j]);
-                if constexpr (!RMS)
+        for (int j = 0; j < NV; ++j) {
+            widen(cur[j], v[j]);
+            if constexpr (!RMS)
 #pragma unroll
-                    for (int i = 0; i < V; ++i) s[0] += v[j][i];
-            }
+                for (int i = 0; i < V; ++i) s[0] += v[j][i];
+        }
         float m = 0.0f;
         if constexpr (!RMS) {
-            block_sums<TPR, 1>(s, sums[turn][0]);
-            m = s[0] * inv_h;
+            row_sums<G, 1>(s, sums[turn][0]);
+            m = s[0] / n;   // a quotient, not contracted into x - m
         }
         s[0] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (j * TPR + t < nv)
+        for (int j = 0; j < NV; ++j) {
+            const int left = H - (j * lanes + t) * V;   // columns of this vector that exist
 #pragma unroll
-                for (int i = 0; i < V; ++i) s[0] += (v[j][i] - m) * (v[j][i] - m);
-        block_sums<TPR, 1>(s, sums[turn][1]);
-        const float r = 1.0f / sqrtf(s[0] * inv_h + eps);
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (j * TPR + t < nv) {
-                float y[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) y[i] = (v[j][i] - m) * r * wr[j][i] + br[j][i];
-                store_vec<TE, V>(out + (size_t)row * H + (size_t)(j * TPR + t) * V, y);
+            for (int i = 0; i < V; ++i) {
+                const float d = v[j][i] - m;
+                s[0] += (RMS || (TAIL ? i < left : left > 0)) ? d * d : 0.0f;   // RMS: absent columns are 0
             }
+        }
+        row_sums<G, 1>(s, sums[turn][1]);
+        const float r = 1.0f / sqrtf(s[0] / n + eps);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float y[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                y[i] = (v[j][i] - m) * r * wr[j][i];
+                if constexpr (!RMS) y[i] += br[j][i];
+            }
+            R::store(out + (size_t)row * H, j, t, lanes, full, last, y);
+        }
         if (stats != nullptr && t == 0) *reinterpret_cast<float2*>(stats + 2 * (size_t)row) = make_float2(m, r);
 #pragma unroll
         for (int j = 0; j < NV; ++j) cur[j] = nxt[j];
     }
 }
 
-// part [gridDim.x][2][H] (RMS norm or no bias wanted: [gridDim.x][1][H])
-template <typename TE, int V, int NV, int TPR, bool RMS>
-__global__ __launch_bounds__(TPR) void norm_backward_kernel(const TE* __restrict__ dout, const TE* __restrict__ x,
-                                                            const float* __restrict__ stats,
-                                                            const float* __restrict__ w, int rows, int H, int parts,
-                                                            TE* __restrict__ dx, float* __restrict__ part) {
-    __shared__ float sums[2][TPR / kWave][2];
-    const int nv = H / V, t = threadIdx.x;
-    const float inv_h = 1.0f / (float)H;
+// part [partial rows][parts][H]: dw, and db where parts is 2
+template <typename TE, int NV, int G, bool TAIL, bool RMS>
+__global__ __launch_bounds__((max_threads<NV, G>())) void norm_backward_kernel(
+    const TE* __restrict__ dout, const TE* __restrict__ x, const float* __restrict__ stats,
+    const float* __restrict__ w, int rows, int H, int parts, TE* __restrict__ dx, float* __restrict__ part) {
+    using R = Row<TE, NV, TAIL>;
+    constexpr int V = R::V;
+    __shared__ float sums[2][kMaxWaves][2];
+    const Place<G> at;
+    const int full = H / V, last = H - full * V, t = at.t, lanes = at.lanes;
+    const float n = (float)H;
+    typename R::Vec cx[NV], cd[NV], nx[NV], nd[NV];
+    float2 st = make_float2(0.0f, 0.0f), nst = st;
+    int row = at.row;
+    if (row < rows) {
+        st = *reinterpret_cast<const float2*>(stats + 2 * (size_t)row);
+        R::load(cx, x + (size_t)row * H, t, lanes, full, last);
+        R::load(cd, dout + (size_t)row * H, t, lanes, full, last);
+    }
     float wr[NV][V], dw[NV][V], db[NV][V];
+    R::columns(wr, w, t, lanes, H);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) dw[j][i] = db[j][i] = 0.0f;
+    for (int turn = 0; row < rows; row += at.step, turn ^= 1) {
+        if (rows - row > at.step) {
+            const size_t next = (size_t)row + at.step;
+            nst = *reinterpret_cast<const float2*>(stats + 2 * next);
+            R::load(nx, x + next * H, t, lanes, full, last);
+            R::load(nd, dout + next * H, t, lanes, full, last);
+        }
+        const float m = RMS ? 0.0f : st.x, r = st.y;
+        // columns that do not exist have dout 0 and w 0: they add nothing
+        float xh[NV][V], c[NV][V];
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float d[V];
+            widen(cx[j], xh[j]);
+            widen(cd[j], d);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                xh[j][i] = (xh[j][i] - m) * r;
+                c[j][i] = d[i] * wr[j][i];
+                dw[j][i] += d[i] * xh[j][i];
+                if constexpr (!RMS) {
+                    db[j][i] += d[i];
+                    s[1] += c[j][i];
+                }
+                s[0] += c[j][i] * xh[j][i];
+            }
+        }
+        row_sums<G, 2>(s, sums[turn]);
+        const float cx_mean = s[0] / n, c_mean = RMS ? 0.0f : s[1] / n;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float o[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = r * (c[j][i] - c_mean - xh[j][i] * cx_mean);
+            R::store(dx + (size_t)row * H, j, t, lanes, full, last, o);
+            cx[j] = nx[j];
+            cd[j] = nd[j];
+        }
+        st = nst;
+    }
+    size_t at_part = blockIdx.x;
+    if constexpr (G != 0) {
+        // the rows of a wave's groups: one partial row a wave
+#pragma unroll
+        for (int d = G; d < kWave; d <<= 1)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    dw[j][i] += __shfl_xor(dw[j][i], d);
+                    db[j][i] += __shfl_xor(db[j][i], d);
+                }
+        at_part = (size_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+        if (lane_id() >= G) return;
+    }
+    float* pw = part + at_part * parts * H;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            wr[j][i] = j * TPR + t < nv ? w[(j * TPR + t) * V + i] : 0.0f;
-            dw[j][i] = 0.0f;
-            db[j][i] = 0.0f;
-        }
-    Raw<TE, V> cx[NV], cd[NV], nx[NV], nd[NV];
-    auto load = [&](Raw<TE, V>* r, const TE* p, size_t row) __attribute__((always_inline)) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (j * TPR + t < nv) r[j] = load_raw<TE, V>(p + row * H + (size_t)(j * TPR + t) * V);
-    };
-    int row = blockIdx.x, turn = 0;
-    if (row < rows) {
-        load(cx, x, row);
-        load(cd, dout, row);
-    }
-    for (; row < rows; row += gridDim.x, turn ^= 1) {
-        const float2 st = *reinterpret_cast<const float2*>(stats + 2 * (size_t)row);
-        const float m = RMS ? 0.0f : st.x, r = st.y;
-        if (row + (int)gridDim.x < rows) {
-            load(nx, x, (size_t)row + gridDim.x);
-            load(nd, dout, (size_t)row + gridDim.x);
-        }
-        float xh[NV][V], c[NV][V];
-        float s[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (j * TPR + t < nv) {
-                float d[V];
-                widen(cx[j], xh[j]);
-                widen(cd[j], d);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    xh[j][i] = (xh[j][i] - m) * r;
-                    c[j][i] = d[i] * wr[j][i];
-                    dw[j][i] += d[i] * xh[j][i];
-                    if constexpr (!RMS) {
-                        db[j][i] += d[i];
-                        s[1] += c[j][i];
-                    }
-                    s[0] += c[j][i] * xh[j][i];
-                }
+            const int col = (j * lanes + t) * V + i;
+            if (col < H) {
+                pw[col] = dw[j][i];
+                if (!RMS && parts == 2) pw[H + col] = db[j][i];
             }
-        block_sums<TPR, 2>(s, sums[turn]);
-        const float cx_mean = s[0] * inv_h, c_mean = RMS ? 0.0f : s[1] * inv_h;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (j * TPR + t < nv) {
-                float o[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) o[i] = r * (c[j][i] - c_mean - xh[j][i] * cx_mean);
-                store_vec<TE, V>(dx + (size_t)row * H + (size_t)(j * TPR + t) * V, o);
-            }
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            cx[j] = nx[j];
-            cd[j] = nd[j];
         }
-    }
-    float* pw = part + (size_t)blockIdx.x * parts * H;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-        if (j * TPR + t < nv)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                pw[(j * TPR + t) * V + i] = dw[j][i];
-                if (!RMS && parts == 2) pw[H + (j * TPR + t) * V + i] = db[j][i];
-            }
 }
 
 // out[c] = sum over p < n of part[p][c] for the W = parts x H columns: a
@@ -202,8 +312,17 @@ __global__ __launch_bounds__(64 * kSumWaves) void norm_sum_kernel(const float* _
     const int lane = lane_id(), wv = threadIdx.x >> 6;
     const int c = blockIdx.x * 64 + lane;
     float v = 0.0f;
-    if (c < W)
-        for (int p = wv; p < n; p += kSumWaves) v += part[(size_t)p * W + c];
+    if (c < W) {
+        int p = wv;
+        for (; p + 7 * kSumWaves < n; p += 8 * kSumWaves) {   // eight loads in flight
+            float u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = part[(size_t)(p + i * kSumWaves) * W + c];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v += u[i];
+        }
+        for (; p < n; p += kSumWaves) v += part[(size_t)p * W + c];
+    }
     s[wv][lane] = v;
     __syncthreads();
     if (wv == 0 && c < W) {
@@ -213,103 +332,103 @@ __global__ __launch_bounds__(64 * kSumWaves) void norm_sum_kernel(const float* _
     }
 }
 
-// Threads a row and vectors a thread for H columns in vectors of V: one wave up
-// to 2 vectors a lane, then 256 threads up to 4, 512 and 1024 (unaligned rows:
-// 256 or 1024 threads, up to 16 single values).
+// How H columns are held: lanes of a wave (g), or a workgroup of `threads` with
+// nv vectors a lane.
 struct Shape {
-    int tpr, nv;
+    int g, nv, threads;
 };
 Shape shape_of(int H, int V) {
-    const int n = H / V;
-    if (V == 1) {
-        if (n <= 256 * 4) return {256, 4};
-        if (n <= 256 * 16) return {256, 16};
-        return {1024, 16};
-    }
-    if (n <= 128) return {64, 2};
-    if (n <= 1024) return {256, (n + 255) / 256};
-    if (n <= 2048) return {512, 4};
-    return {1024, 4};
+    const int n = (H + V - 1) / V;
+    if (n <= 64) return {n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64, 1, 256};
+    const int nv = n <= 1024 ? 1 : n <= 2048 ? 4 : 8;
+    return {0, nv, ((n + nv - 1) / nv + 63) / 64 * 64};
+}
+int values_of(int dtype) { return dtype == 1 ? 8 : 4; }
+
+// f(nv, g) for the shape's template arguments
+template <int V, typename F>
+void with_shape(const Shape& s, F&& f) {
+    using std::integral_constant;
+    const integral_constant<int, 1> one = {};
+    if (s.g == 8) f(one, integral_constant<int, 8>{});
+    else if (s.g == 16) f(one, integral_constant<int, 16>{});
+    else if (s.g == 32) f(one, integral_constant<int, 32>{});
+    else if (s.g == 64) f(one, integral_constant<int, 64>{});
+    else if (s.nv == 1) f(one, integral_constant<int, 0>{});
+    else if (s.nv == 4) f(integral_constant<int, 4>{}, integral_constant<int, 0>{});
+    else if constexpr (V == 4) f(integral_constant<int, 8>{}, integral_constant<int, 0>{});   // fp32 past 8192 columns
 }
 
-template <typename TE, int V, bool RMS, typename F>
-void with_shape(int H, F&& f) {
-    const Shape s = shape_of(H, V);
-    auto go = [&](auto nv, auto tpr) { f(nv, tpr); };
-#define NORM_SHAPE(NV_, TPR_) \
-    if (s.nv == NV_ && s.tpr == TPR_) return go(std::integral_constant<int, NV_>{}, std::integral_constant<int, TPR_>{})
-    if constexpr (V == 1) {
-        NORM_SHAPE(4, 256);
-        NORM_SHAPE(16, 256);
-        NORM_SHAPE(16, 1024);
-    } else {
-        NORM_SHAPE(2, 64);
-        NORM_SHAPE(1, 256);
-        NORM_SHAPE(2, 256);
-        NORM_SHAPE(3, 256);
-        NORM_SHAPE(4, 256);
-        NORM_SHAPE(4, 512);
-        if constexpr (V == 4) NORM_SHAPE(4, 1024);   // past 8192 columns
-    }
-#undef NORM_SHAPE
+// workgroups that hold `rows` rows, at most `most`
+int workgroups(const Shape& s, int rows, int most) {
+    const int per = s.g == 0 ? 1 : 256 / s.g;
+    return std::max(1, std::min((rows + per - 1) / per, most));
 }
 
-template <typename TE, int V, bool RMS>
+template <typename TE, bool TAIL, bool RMS>
 hipError_t forward_typed(const NormParams& p, hipStream_t stream) {
-    with_shape<TE, V, RMS>(p.H, [&](auto nv, auto tpr) {
-        constexpr int NV = decltype(nv)::value, TPR = decltype(tpr)::value;
-        const int grid = std::min(p.rows, device_cu_count() * (2048 / TPR));
-        hipLaunchKernelGGL((norm_forward_kernel<TE, V, NV, TPR, RMS>), dim3(grid), dim3(TPR), 0, stream,
-                           static_cast<const TE*>(p.x), p.weight, p.bias, p.rows, p.H, p.eps, static_cast<TE*>(p.out),
-                           p.stats_out);
+    const Shape s = shape_of(p.H, values_of(p.dtype));
+    const int grid = workgroups(s, p.rows, device_cu_count() * (2048 / s.threads));
+    with_shape<16 / sizeof(TE)>(s, [&](auto nv, auto g) {
+        hipLaunchKernelGGL((norm_forward_kernel<TE, decltype(nv)::value, decltype(g)::value, TAIL, RMS>), dim3(grid),
+                           dim3(s.threads), 0, stream, static_cast<const TE*>(p.x), p.weight, p.bias, p.rows, p.H,
+                           p.eps, static_cast<TE*>(p.out), p.stats_out);
     });
     return hipGetLastError();
 }
 
-template <typename TE, int V, bool RMS>
+// Workgroups of the backward pass.  Each ends with one partial row (narrow rows:
+// four) that is written and read back, so each takes 4 rows a lane or more, and
+// 16 or more where 512 workgroups are enough; at most what the card holds.
+int backward_grid(const Shape& s, int rows) {
+    const int per = s.g == 0 ? 1 : 256 / s.g;
+    const int steps = (rows + per - 1) / per;
+    const int most = std::min(std::max(512, steps / 16), 256 * std::max(1, 2048 / s.threads));
+    return std::max(1, std::min((steps + 3) / 4, most));
+}
+
+template <typename TE, bool TAIL, bool RMS>
 hipError_t backward_typed(const NormParams& p, hipStream_t stream) {
-    const int grid = norm_parts(p.rows, p.H);
+    const Shape s = shape_of(p.H, values_of(p.dtype));
+    const int grid = backward_grid(s, p.rows);
     const int parts = p.dbias != nullptr ? 2 : 1;
-    with_shape<TE, V, RMS>(p.H, [&](auto nv, auto tpr) {
-        constexpr int NV = decltype(nv)::value, TPR = decltype(tpr)::value;
-        hipLaunchKernelGGL((norm_backward_kernel<TE, V, NV, TPR, RMS>), dim3(grid), dim3(TPR), 0, stream,
-                           static_cast<const TE*>(p.dout), static_cast<const TE*>(p.x), p.stats, p.weight, p.rows, p.H,
-                           parts, static_cast<TE*>(p.dx), p.part);
+    with_shape<16 / sizeof(TE)>(s, [&](auto nv, auto g) {
+        hipLaunchKernelGGL((norm_backward_kernel<TE, decltype(nv)::value, decltype(g)::value, TAIL, RMS>), dim3(grid),
+                           dim3(s.threads), 0, stream, static_cast<const TE*>(p.dout), static_cast<const TE*>(p.x),
+                           p.stats, p.weight, p.rows, p.H, parts, static_cast<TE*>(p.dx), p.part);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int W = parts * p.H;
-    hipLaunchKernelGGL(norm_sum_kernel, dim3((W + 63) / 64), dim3(64 * kSumWaves), 0, stream, p.part, grid, p.H, W,
-                       p.dweight, p.dbias);
+    hipLaunchKernelGGL(norm_sum_kernel, dim3((W + 63) / 64), dim3(64 * kSumWaves), 0, stream, p.part,
+                       norm_parts(p.dtype, p.rows, p.H), p.H, W, p.dweight, p.dbias);
     return hipGetLastError();
 }
 
-// 16-byte vectors where rows are whole vectors (the entry points ask for
-// 16-byte aligned tensors), else single values
 template <typename F>
 hipError_t by_type(const NormParams& p, F&& f) {
-    auto kind = [&](auto te, auto v) { return p.rms ? f(te, v, std::true_type{}) : f(te, v, std::false_type{}); };
-    using One = std::integral_constant<int, 1>;
-    if (p.dtype == 1)
-        return p.H % 8 == 0 ? kind(bf16_t{}, std::integral_constant<int, 8>{}) : kind(bf16_t{}, One{});
-    return p.H % 4 == 0 ? kind(float{}, std::integral_constant<int, 4>{}) : kind(float{}, One{});
+    const bool tail = p.H % values_of(p.dtype) != 0;
+    auto kind = [&](auto te, auto tl) { return p.rms ? f(te, tl, std::true_type{}) : f(te, tl, std::false_type{}); };
+    auto ends = [&](auto te) { return tail ? kind(te, std::true_type{}) : kind(te, std::false_type{}); };
+    return p.dtype == 1 ? ends(bf16_t{}) : ends(float{});
 }
 
 }  // namespace
 
-// Workgroups of the backward pass, one partial row each: 16 rows or more for
-// each, so that the partial rows stay a small part of the traffic, two a CU.
-int norm_parts(int rows, int H) { return std::max(1, std::min((rows + 15) / 16, 512)); }
+int norm_parts(int dtype, int rows, int H) {
+    const Shape s = shape_of(H, values_of(dtype));
+    return backward_grid(s, rows) * (s.g == 0 ? 1 : 4);
+}
 
 hipError_t launch_norm_forward(const NormParams& p, hipStream_t stream) {
-    return by_type(p, [&](auto te, auto v, auto rms) {
-        return forward_typed<decltype(te), decltype(v)::value, decltype(rms)::value>(p, stream);
+    return by_type(p, [&](auto te, auto tail, auto rms) {
+        return forward_typed<decltype(te), decltype(tail)::value, decltype(rms)::value>(p, stream);
     });
 }
 
 hipError_t launch_norm_backward(const NormParams& p, hipStream_t stream) {
-    return by_type(p, [&](auto te, auto v, auto rms) {
-        return backward_typed<decltype(te), decltype(v)::value, decltype(rms)::value>(p, stream);
+    return by_type(p, [&](auto te, auto tail, auto rms) {
+        return backward_typed<decltype(te), decltype(tail)::value, decltype(rms)::value>(p, stream);
     });
 }
 

@@ -134,8 +134,7 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(
             if (act != nullptr) store_vec<TE, kCols / 2>(act + row * I + (size_t)col * (kCols / 2), av);
         }
         if (dgamma != nullptr) {
-#pragma unroll
-            for (int d = 1; d < G; d <<= 1) part += __shfl_xor(part, d);
+            part = lanes_sum<G>(part);
             if (sub == 0) dgamma[row] = part;
         }
     }

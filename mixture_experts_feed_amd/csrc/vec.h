@@ -79,10 +79,25 @@ __device__ __forceinline__ void store_vec(TE* p, const float* v) {
     }
 }
 
-// sum over the lanes of a wave, in a fixed order; every lane gets it
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d);
+// v from the lane that a DPP control names (all of them stay inside 16 lanes)
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+
+// sum over G neighbouring lanes (8, 16, 32 or 64), in a fixed order; every lane
+// gets it.  Up to 16 lanes through DPP: neighbours, pairs, then mirrored halves
+// (each step adds two values that are equal over the lanes of a half, so the
+// mirror is as good as an xor); beyond through LDS lane permutes.
+template <int G>
+__device__ __forceinline__ float lanes_sum(float v) {
+    static_assert(G == 8 || G == 16 || G == 32 || G == 64, "lanes of a group");
+    v += dpp<0xB1>(v);               // quad_perm [1, 0, 3, 2]
+    v += dpp<0x4E>(v);               // quad_perm [2, 3, 0, 1]
+    v += dpp<0x141>(v);              // row_half_mirror
+    if constexpr (G >= 16) v += dpp<0x140>(v);   // row_mirror
+    if constexpr (G >= 32) v += __shfl_xor(v, 16);
+    if constexpr (G >= 64) v += __shfl_xor(v, 32);
     return v;
 }
 

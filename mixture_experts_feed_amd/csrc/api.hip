@@ -731,7 +731,9 @@ size_t grouped_row_tiles(const inkling_grouped_dims_t* d) {
 }
 
 size_t grouped_gather_bytes(const inkling_grouped_dims_t* d) {
-    return (size_t)d->rows * d->in_features * (d->dtype == INKLING_BF16 ? 2 : 4);
+    if (group_small_wgrad(d->dtype == INKLING_BF16 ? 1 : 0, d->n_groups, d->in_features, d->out_features))
+        return 0;   // gathered as they are loaded
+    return (size_t)d->rows * d->in_features * 2;
 }
 
 GroupParams grouped_params(const inkling_grouped_dims_t* d, const GroupedLayout& L, void* ws, bool input_grad) {
@@ -768,12 +770,18 @@ int grouped_rows(const inkling_grouped_dims_t* d, bool input_grad, const void* s
     const GroupedLayout L = make_grouped_layout(d, grouped_row_tiles(d), 0);
     if (workspace == nullptr || workspace_bytes < L.total) return INKLING_ERR_WORKSPACE;
     GroupParams p = grouped_params(d, L, workspace, input_grad);
-    if (group_max_tiles(p) > INT32_MAX - 4096) return INKLING_ERR_UNSUPPORTED;
+    const bool small = group_small(p.dtype, p.rows, p.E, p.n_cols);
+    if ((small ? group_small_tiles(p.rows, p.E, p.n_cols) : group_max_tiles(p)) > INT32_MAX - 4096)
+        return INKLING_ERR_UNSUPPORTED;
     p.src = src;
     p.weight = weight;
     p.row_index = row_index;
     p.out = out;
     hipStream_t s = (hipStream_t)stream;
+    if (small) {
+        HIP_TRY(launch_group_small(p, offsets, s));
+        return INKLING_OK;
+    }
     HIP_TRY(launch_group_plan(p, offsets, true, s));
     HIP_TRY(launch_group_rows(p, s));
     return INKLING_OK;
@@ -824,19 +832,26 @@ int inkling_grouped_weight_grad(const inkling_grouped_dims_t* dims, const void* 
     if (!aligned(x, 16) || !aligned(dout, 16) || !aligned(dweight, 16) || !aligned(offsets, 4) ||
         !aligned(row_index, 4))
         return INKLING_ERR_INVALID_ARGUMENT;
-    if ((long long)dims->n_groups * ((dims->out_features + 255) / 256) * ((dims->in_features + 127) / 128) >
+    const bool small = group_small_wgrad(dims->dtype == INKLING_BF16 ? 1 : 0, dims->n_groups, dims->in_features,
+                                         dims->out_features);
+    const long long side = small ? 64 : 128;   // at least this wide a tile each way
+    if (dims->n_groups * ((dims->out_features + side - 1) / side) * ((dims->in_features + side - 1) / side) >
         INT32_MAX - 4096)
         return INKLING_ERR_UNSUPPORTED;
     const bool gather = row_index != nullptr && dims->rows > 0;
     const GroupedLayout L = make_grouped_layout(dims, 0, gather ? grouped_gather_bytes(dims) : 0);
     if (workspace == nullptr || workspace_bytes < L.total) return INKLING_ERR_WORKSPACE;
-    const GroupParams p = grouped_params(dims, L, workspace, false);
+    GroupParams p = grouped_params(dims, L, workspace, false);
     hipStream_t s = (hipStream_t)stream;
+    if (small) {
+        p.row_index = row_index;
+        HIP_TRY(launch_group_small_wgrad(p, offsets, x, dout, dims->in_features, dims->out_features, dweight, s));
+        return INKLING_OK;
+    }
     HIP_TRY(launch_group_plan(p, offsets, false, s));
     if (gather) {
         void* sorted = at<void>(workspace, L.x_sorted);
-        HIP_TRY(launch_group_gather(p.dtype, x, p.src_rows, row_index, p.offs, p.E, p.rows, dims->in_features, sorted,
-                                    s));
+        HIP_TRY(launch_group_gather(x, p.src_rows, row_index, p.offs, p.E, p.rows, dims->in_features, sorted, s));
         x = sorted;
     }
     HIP_TRY(launch_group_wgrad(p, x, dout, dims->in_features, dims->out_features, dweight, p.out_bf16, s));

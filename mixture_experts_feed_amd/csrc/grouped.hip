@@ -1,12 +1,19 @@
 // Products grouped by expert with ragged row counts, reached on their own:
 //   out[r] = W_e x[row_index[r]]   dx[r] = W_e^T dout[r]   dW_e = sum_r dout[r] (x) x[row_index[r]]
-// for the rows offsets[e] <= r < offsets[e + 1] of expert e.  The matrix work is
-// moe_gemm_kernel (gemm_kernel.h) in its three grouped modes; here are the plan
-// that turns the caller's offsets into row tiles, and the launches.
+// for the rows offsets[e] <= r < offsets[e + 1] of expert e.  Three kernels:
+//   small_product_kernel (grouped_small.h)  64 x 64 tiles, one launch without a
+//     plan: fp32, and bf16 products with too few large tiles for the card;
+//   moe_gemm_kernel (gemm_kernel.h)  the layer's tiles: the bf16 forward, with few
+//     rows an expert (weights streamed) and many, and weight gradients of few rows;
+//   product_kernel (grouped_gemm.h)  256 x 256 tiles of four waves: bf16 input
+//     gradients, and weight gradients of many rows.
+// The latter two follow a plan: the caller's offsets made safe, and row tiles.
 #include <algorithm>
 
 #include "common.h"
 #include "gemm_kernel.h"
+#include "grouped_gemm.h"
+#include "grouped_small.h"
 #include "kernels.h"
 
 namespace inkling {
@@ -77,13 +84,11 @@ __global__ __launch_bounds__(kMaxGroups) void group_plan_kernel(const int32_t* _
 
 // out[r] = src[row_index[r]] for offs[0] <= r < offs[E] (an index out of range
 // takes the nearest row in it): rows of D elements, D a multiple of 8.
-template <typename TE>
-__global__ __launch_bounds__(256) void group_gather_kernel(const TE* __restrict__ src, int src_rows,
+__global__ __launch_bounds__(256) void group_gather_kernel(const bf16_t* __restrict__ src, int src_rows,
                                                            const int32_t* __restrict__ row_index,
                                                            const int32_t* __restrict__ offs, int E, int D,
-                                                           TE* __restrict__ out) {
-    constexpr int V = 16 / sizeof(TE);
-    const int nv = D / V;
+                                                           bf16_t* __restrict__ out) {
+    const int nv = D / 8;
     for (int r = offs[0] + blockIdx.x; r < offs[E]; r += gridDim.x) {
         const size_t row = (size_t)max(0, min(row_index[r], src_rows - 1));
         const uint4* s = reinterpret_cast<const uint4*>(src + row * D);
@@ -102,19 +107,32 @@ int grid_of(long long tiles, int per_cu) {
     return (grid + 7) / 8 * 8;
 }
 
-template <typename TE, int MODE>
-hipError_t launch_rows(int cfg, const GemmKArgs& a, long long max_tiles, hipStream_t stream) {
+hipError_t launch_forward(int cfg, const GemmKArgs& a, long long max_tiles, hipStream_t stream) {
+    const dim3 grid(grid_of(max_tiles, 1));
     if (cfg == 0)
-        hipLaunchKernelGGL((moe_gemm_kernel<TE, 256, 256, 4, 2, 2, 2, 128, 8, kSchedGroup, MODE>),
-                           dim3(grid_of(max_tiles, 1)), dim3(512), 0, stream, a);
-    else if constexpr (MODE == kModeGroup)
-        hipLaunchKernelGGL((moe_gemm_kernel<TE, 128, 16, 8, 1, 4, 4, 128, 1, kSchedStride, MODE>),
-                           dim3(grid_of(max_tiles, 1)), dim3(512), 0, stream, a);
+        hipLaunchKernelGGL((moe_gemm_kernel<bf16_t, 256, 256, 4, 2, 2, 2, 128, 8, kSchedGroup, kModeGroup>), grid,
+                           dim3(512), 0, stream, a);
+    else
+        hipLaunchKernelGGL((moe_gemm_kernel<bf16_t, 128, 16, 8, 1, 4, 4, 128, 1, kSchedStride, kModeGroup>), grid,
+                           dim3(512), 0, stream, a);
     return hipGetLastError();
 }
 
+// Weight gradients of bf16 operands: product_kernel from this many rows an
+// expert on, below it the layer's 128 x 256 tiles, two workgroups a CU, whose
+// change from tile to tile overlaps.  Measured, us, 128 x 256 tiles against
+// product_kernel: fp32 gradients 920 / 1117 at 128 rows (4096 x 2048 weights),
+// 355 / 340 at 256 (2048 x 2048), 343 / 300 at 384 (1536 x 2048), 670 / 610 at
+// 1024; bf16 gradients (half the bytes to write) 262 / 297 at 256, 271 / 282 at
+// 384, 295 / 294 at 512, 602 / 560 at 1024, 499 / 470 at 2048.
+int wgrad_min_rows(int dw_bf16) { return dw_bf16 ? 768 : 256; }
+
 }  // namespace
 
+// Up to 48 rows an expert on average, the forward streams the weights past tiles
+// of 16 rows (the layer's decode tiles): 805 us at 2 rows an expert, 6144 x 4096,
+// 6.9 TB/s.  Input gradients always take 256 x 256 tiles (whose few-row form
+// skips the row blocks without rows): 408 us at 64 rows, 4096 x 2048, 5.4 TB/s.
 int group_cfg(int rows, int E, bool input_grad) {
     return !input_grad && (double)rows / E <= 48.0 ? 1 : 0;
 }
@@ -134,7 +152,91 @@ hipError_t launch_group_plan(const GroupParams& p, const int32_t* offsets, bool 
     return hipGetLastError();
 }
 
+// 64 x 64 tiles below one 256 x 256 tile a CU.  Measured, us, forward, 64 x 64
+// against 256 x 256: 13 / 19 at 12 experts of 30 rows (512 x 512), 28 / 40 at 16
+// of 256 rows (1024 x 1024, 128 large tiles), 46 / 45 at 16 of 512 (192), 50 / 46 at
+// 8 of 512 (2048 x 1024, 192).  fp32 takes them at every size: 13 / 34 us at 8
+// experts of 83 rows (136 x 200), 50 / 84 at 32 of 64 (1024 x 1024), and up to 22%
+// slower on large products (727 / 594 at 16 of 512, 2048 x 2048), which bf16 is for.
+bool group_small(int dtype, int rows, int E, int n_cols) {
+    if (dtype == 0) return true;
+    return group_max_row_tiles(rows, E, 0) * ((n_cols + 255) / 256) < 256;
+}
+
+bool group_small_wgrad(int dtype, int E, int n_in, int n_out) {
+    if (dtype == 0) return true;
+    return (long long)E * ((n_out + 255) / 256) * ((n_in + 127) / 128) < 256;
+}
+
+long long group_small_tiles(int rows, int E, int n_cols) {
+    return (((long long)rows + 63) / 64 + E) * ((n_cols + 63) / 64);
+}
+
+hipError_t launch_group_small(const GroupParams& p, const int32_t* offsets, hipStream_t stream) {
+    SmallArgs a = {};
+    a.A = p.weight;
+    a.B = p.src;
+    a.offsets = offsets;
+    a.row_index = p.row_index;
+    a.src_rows = p.src_rows;
+    a.rows = p.rows;
+    a.E = p.E;
+    a.K = p.k_len;
+    a.N = p.n_cols;
+    a.ntn = (p.n_cols + 63) / 64;
+    a.out = p.out;
+    a.out_bf16 = p.out_bf16;
+    const dim3 grid((unsigned)group_small_tiles(p.rows, p.E, p.n_cols)), block(256);
+    if (p.dtype == 1) {
+        if (p.input_grad) hipLaunchKernelGGL((small_product_kernel<bf16_t, kProdDx>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((small_product_kernel<bf16_t, kProdRows>), grid, block, 0, stream, a);
+    } else {
+        if (p.input_grad) hipLaunchKernelGGL((small_product_kernel<float, kProdDx>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((small_product_kernel<float, kProdRows>), grid, block, 0, stream, a);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_group_small_wgrad(const GroupParams& p, const int32_t* offsets, const void* x, const void* dout,
+                                    int n_in, int n_out, void* dw, hipStream_t stream) {
+    SmallArgs a = {};
+    a.A = x;
+    a.B = dout;
+    a.offsets = offsets;
+    a.row_index = p.row_index;
+    a.src_rows = p.src_rows;
+    a.rows = p.rows;
+    a.E = p.E;
+    a.N = n_in;
+    a.M = n_out;
+    a.ntn = (n_in + 63) / 64;
+    a.ntm = (n_out + 63) / 64;
+    a.out = dw;
+    a.out_bf16 = p.out_bf16;
+    const dim3 grid((unsigned)((long long)p.E * a.ntm * a.ntn)), block(256);
+    if (p.dtype == 1) hipLaunchKernelGGL((small_product_kernel<bf16_t, kProdWgrad>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((small_product_kernel<float, kProdWgrad>), grid, block, 0, stream, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_group_rows(const GroupParams& p, hipStream_t stream) {
+    if (p.dtype == 1 && p.input_grad) {
+        ProductArgs a = {};
+        a.A = static_cast<const bf16_t*>(p.weight);
+        a.B = static_cast<const bf16_t*>(p.src);
+        a.offs = p.offs;
+        a.tiles = p.tiles;
+        a.num_tiles = p.num_tiles;
+        a.E = p.E;
+        a.K = p.k_len;
+        a.N = p.n_cols;
+        a.ntn = (p.n_cols + 255) / 256;
+        a.out = p.out;
+        a.out_bf16 = p.out_bf16;
+        a.counters = p.counters;
+        hipLaunchKernelGGL(product_kernel<kProdDx>, dim3(grid_of(group_max_tiles(p), 1)), dim3(256), 0, stream, a);
+        return hipGetLastError();
+    }
     GemmKArgs a = {};
     a.round_counter = p.counters;
     a.tiles = p.tiles;
@@ -148,31 +250,38 @@ hipError_t launch_group_rows(const GroupParams& p, hipStream_t stream) {
     a.out_final_bf16 = p.out_bf16;
     a.K_r = p.k_len;
     a.N_r = p.n_cols;
-    a.lda_r = p.n_cols;   // input gradient: the weights as K rows of n_cols
     a.ntn_r = (p.n_cols + tile_cols(p.cfg) - 1) / tile_cols(p.cfg);
     a.has_routed = 1;
-    const long long tiles = group_max_tiles(p);
-    if (p.input_grad)
-        return p.dtype == 1 ? launch_rows<bf16_t, kModeGroupDx>(p.cfg, a, tiles, stream)
-                            : launch_rows<float, kModeGroupDx>(p.cfg, a, tiles, stream);
-    return p.dtype == 1 ? launch_rows<bf16_t, kModeGroup>(p.cfg, a, tiles, stream)
-                        : launch_rows<float, kModeGroup>(p.cfg, a, tiles, stream);
+    return launch_forward(p.cfg, a, group_max_tiles(p), stream);
 }
 
-hipError_t launch_group_gather(int dtype, const void* src, int src_rows, const int32_t* row_index,
+hipError_t launch_group_gather(const void* src, int src_rows, const int32_t* row_index,
                                const int32_t* offs, int E, int rows, int D, void* out, hipStream_t stream) {
     const int blocks = std::min(rows, 4096);
-    if (dtype == 1)
-        hipLaunchKernelGGL(group_gather_kernel<bf16_t>, dim3(blocks), dim3(256), 0, stream,
-                           static_cast<const bf16_t*>(src), src_rows, row_index, offs, E, D, static_cast<bf16_t*>(out));
-    else
-        hipLaunchKernelGGL(group_gather_kernel<float>, dim3(blocks), dim3(256), 0, stream,
-                           static_cast<const float*>(src), src_rows, row_index, offs, E, D, static_cast<float*>(out));
+    hipLaunchKernelGGL(group_gather_kernel, dim3(blocks), dim3(256), 0, stream, static_cast<const bf16_t*>(src),
+                       src_rows, row_index, offs, E, D, static_cast<bf16_t*>(out));
     return hipGetLastError();
 }
 
 hipError_t launch_group_wgrad(const GroupParams& p, const void* x, const void* dout, int n_in, int n_out, void* dw,
                               int dw_bf16, hipStream_t stream) {
+    if (p.rows >= (long long)p.E * wgrad_min_rows(dw_bf16)) {
+        ProductArgs a = {};
+        a.A = static_cast<const bf16_t*>(x);
+        a.B = static_cast<const bf16_t*>(dout);
+        a.offs = p.offs;
+        a.E = p.E;
+        a.N = n_in;
+        a.M = n_out;
+        a.ntn = (n_in + 255) / 256;
+        a.ntm = (n_out + 255) / 256;
+        a.out = dw;
+        a.out_bf16 = dw_bf16;
+        a.counters = p.counters;
+        const dim3 grid(grid_of((long long)p.E * a.ntm * a.ntn, 1));
+        hipLaunchKernelGGL(product_kernel<kProdWgrad>, grid, dim3(256), 0, stream, a);
+        return hipGetLastError();
+    }
     GemmKArgs a = {};
     a.round_counter = p.counters;
     a.offsets = p.offs;
@@ -190,12 +299,8 @@ hipError_t launch_group_wgrad(const GroupParams& p, const void* x, const void* d
     a.w_out_routed = dw;
     a.w_out_bf16 = dw_bf16;
     const int grid = grid_of((long long)p.E * a.wg_mtiles * a.wg_ntiles, 2);
-    if (p.dtype == 1)
-        hipLaunchKernelGGL((moe_gemm_kernel<bf16_t, 128, 256, 2, 2, 2, 2, 64, 4, kSchedQueue, kModeGroupWgrad>),
-                           dim3(grid), dim3(256), 0, stream, a);
-    else
-        hipLaunchKernelGGL((moe_gemm_kernel<float, 128, 256, 2, 2, 2, 2, 64, 4, kSchedQueue, kModeGroupWgrad>),
-                           dim3(grid), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((moe_gemm_kernel<bf16_t, 128, 256, 2, 2, 2, 2, 64, 4, kSchedQueue, kModeGroupWgrad>),
+                       dim3(grid), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

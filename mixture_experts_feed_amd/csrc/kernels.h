@@ -186,12 +186,20 @@ struct GroupParams {
 int group_cfg(int rows, int E, bool input_grad);
 long long group_max_row_tiles(int rows, int E, int cfg);
 long long group_max_tiles(const GroupParams& p);   // row tiles x column tiles
+// whether the products run on 64 x 64 tiles, from the caller's offsets: without
+// a plan (offs, tiles, num_tiles and counters unused)
+bool group_small(int dtype, int rows, int E, int n_cols);
+bool group_small_wgrad(int dtype, int E, int n_in, int n_out);
+long long group_small_tiles(int rows, int E, int n_cols);
+hipError_t launch_group_small(const GroupParams& p, const int32_t* offsets, hipStream_t stream);
+hipError_t launch_group_small_wgrad(const GroupParams& p, const int32_t* offsets, const void* x, const void* dout,
+                                    int n_in, int n_out, void* dw, hipStream_t stream);
 // the plan from the caller's offsets (clamped to the rows, non-decreasing);
 // `tiles`: the row tiles too
 hipError_t launch_group_plan(const GroupParams& p, const int32_t* offsets, bool tiles, hipStream_t stream);
 hipError_t launch_group_rows(const GroupParams& p, hipStream_t stream);
 // out[r] = src[row_index[r]] for the rows of the plan
-hipError_t launch_group_gather(int dtype, const void* src, int src_rows, const int32_t* row_index,
+hipError_t launch_group_gather(const void* src, int src_rows, const int32_t* row_index,
                                const int32_t* offs, int E, int rows, int D, void* out, hipStream_t stream);
 // dw[e] = dout^T x over the rows of e (x and dout in row order)
 hipError_t launch_group_wgrad(const GroupParams& p, const void* x, const void* dout, int n_in, int n_out, void* dw,

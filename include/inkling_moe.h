@@ -301,7 +301,8 @@ typedef struct {
     int32_t out_dtype;     /* inkling_dtype_t of the result         */
 } inkling_grouped_dims_t;
 
-/* workspace of inkling_grouped_linear and inkling_grouped_input_grad */
+/* workspace of inkling_grouped_linear and inkling_grouped_input_grad (0 for
+ * small products: then it may be NULL) */
 int inkling_grouped_workspace_size(const inkling_grouped_dims_t* dims, size_t* bytes);
 /* workspace of inkling_grouped_weight_grad; `gathered`: called with a row_index */
 int inkling_grouped_weight_grad_workspace_size(const inkling_grouped_dims_t* dims, int gathered, size_t* bytes);

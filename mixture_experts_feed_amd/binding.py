@@ -557,7 +557,7 @@ def _result(t, name, shape, dtype, dev):
 
 def _scratch(workspace, need, dev):
     if workspace is None:
-        return torch.empty(max(1, need), dtype=torch.uint8, device=dev)
+        return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _need(workspace, "workspace", torch.uint8)
     _same_device(dev, workspace=workspace)
     return workspace
@@ -578,7 +578,7 @@ def grouped_linear(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
     out = _result(out, "out", (R, N), out_dtype, dev)
     ws = _scratch(workspace, grouped_workspace_size(dims), dev)
     _call(dev, "inkling_grouped_linear", ctypes.byref(dims), x.data_ptr(), _ptr(row_index), weight.data_ptr(),
-          offsets.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel())
+          offsets.data_ptr(), out.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
     return out
 
 
@@ -594,7 +594,7 @@ def grouped_input_grad(dout: torch.Tensor, weight: torch.Tensor, offsets: torch.
     dx = _result(dx, "dx", (R, K), dx_dtype, dev)
     ws = _scratch(workspace, grouped_workspace_size(dims), dev)
     _call(dev, "inkling_grouped_input_grad", ctypes.byref(dims), dout.data_ptr(), weight.data_ptr(),
-          offsets.data_ptr(), dx.data_ptr(), ws.data_ptr(), ws.numel())
+          offsets.data_ptr(), dx.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
     return dx
 
 
@@ -624,7 +624,7 @@ def grouped_weight_grad(dout: torch.Tensor, x: torch.Tensor, offsets: torch.Tens
     dweight = _result(dweight, "dweight", (E, N, K), wdt, dev)
     ws = _scratch(workspace, grouped_weight_grad_workspace_size(dims, row_index is not None), dev)
     _call(dev, "inkling_grouped_weight_grad", ctypes.byref(dims), dout.data_ptr(), x.data_ptr(), _ptr(row_index),
-          offsets.data_ptr(), dweight.data_ptr(), ws.data_ptr(), ws.numel())
+          offsets.data_ptr(), dweight.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
     return dweight
 
 
@@ -779,5 +779,5 @@ def norm_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, sta
     dweight = _result(dweight, "dweight", (H,), torch.float32, dev)
     dbias = _result(dbias, "dbias", (H,), torch.float32, dev) if bias or dbias is not None else None
     _call(dev, "inkling_norm_backward", ctypes.byref(dims), dout.data_ptr(), x.data_ptr(), weight.data_ptr(),
-          stats.data_ptr(), dx.data_ptr(), dweight.data_ptr(), _ptr(dbias), ws.data_ptr(), ws.numel())
+          stats.data_ptr(), dx.data_ptr(), dweight.data_ptr(), _ptr(dbias), _ptr(ws), 0 if ws is None else ws.numel())
     return {"dx": dx, "dweight": dweight, "dbias": dbias}

@@ -705,6 +705,15 @@ struct GroupedLayout {
     size_t offs, counters, num_tiles, tiles, x_sorted, total;
 };
 
+bool grouped_small(const inkling_grouped_dims_t* d, bool input_grad) {
+    return group_small(d->dtype == INKLING_BF16 ? 1 : 0, (int)d->rows, d->n_groups,
+                       input_grad ? d->in_features : d->out_features);
+}
+
+bool grouped_small_wgrad(const inkling_grouped_dims_t* d) {
+    return group_small_wgrad(d->dtype == INKLING_BF16 ? 1 : 0, d->n_groups, d->in_features, d->out_features);
+}
+
 // row_tiles: entries of the tile list; gather_bytes: rows of x in row order
 GroupedLayout make_grouped_layout(const inkling_grouped_dims_t* d, size_t row_tiles, size_t gather_bytes) {
     GroupedLayout L = {};
@@ -731,9 +740,7 @@ size_t grouped_row_tiles(const inkling_grouped_dims_t* d) {
 }
 
 size_t grouped_gather_bytes(const inkling_grouped_dims_t* d) {
-    if (group_small_wgrad(d->dtype == INKLING_BF16 ? 1 : 0, d->n_groups, d->in_features, d->out_features))
-        return 0;   // gathered as they are loaded
-    return (size_t)d->rows * d->in_features * 2;
+    return (size_t)d->rows * d->in_features * 2;   // bf16 (fp32 takes the small tiles)
 }
 
 GroupParams grouped_params(const inkling_grouped_dims_t* d, const GroupedLayout& L, void* ws, bool input_grad) {
@@ -767,10 +774,10 @@ int grouped_rows(const inkling_grouped_dims_t* d, bool input_grad, const void* s
     if (!aligned(src, 16) || !aligned(weight, 16) || !aligned(out, 16) || !aligned(offsets, 4) ||
         !aligned(row_index, 4))
         return INKLING_ERR_INVALID_ARGUMENT;
+    const bool small = grouped_small(d, input_grad);   // takes no workspace
     const GroupedLayout L = make_grouped_layout(d, grouped_row_tiles(d), 0);
-    if (workspace == nullptr || workspace_bytes < L.total) return INKLING_ERR_WORKSPACE;
+    if (!small && (workspace == nullptr || workspace_bytes < L.total)) return INKLING_ERR_WORKSPACE;
     GroupParams p = grouped_params(d, L, workspace, input_grad);
-    const bool small = group_small(p.dtype, p.rows, p.E, p.n_cols);
     if ((small ? group_small_tiles(p.rows, p.E, p.n_cols) : group_max_tiles(p)) > INT32_MAX - 4096)
         return INKLING_ERR_UNSUPPORTED;
     p.src = src;
@@ -795,7 +802,8 @@ int inkling_grouped_workspace_size(const inkling_grouped_dims_t* dims, size_t* b
     const int rc = check_grouped_dims(dims);
     if (rc != INKLING_OK) return rc;
     if (bytes == nullptr) return INKLING_ERR_INVALID_ARGUMENT;
-    *bytes = make_grouped_layout(dims, grouped_row_tiles(dims), 0).total;
+    const bool small = grouped_small(dims, false) && grouped_small(dims, true);
+    *bytes = small ? 0 : make_grouped_layout(dims, grouped_row_tiles(dims), 0).total;
     return INKLING_OK;
 }
 
@@ -803,7 +811,9 @@ int inkling_grouped_weight_grad_workspace_size(const inkling_grouped_dims_t* dim
     const int rc = check_grouped_dims(dims);
     if (rc != INKLING_OK) return rc;
     if (bytes == nullptr) return INKLING_ERR_INVALID_ARGUMENT;
-    *bytes = make_grouped_layout(dims, 0, gathered ? grouped_gather_bytes(dims) : 0).total;
+    *bytes = grouped_small_wgrad(dims)
+                 ? 0
+                 : make_grouped_layout(dims, 0, gathered ? grouped_gather_bytes(dims) : 0).total;
     return INKLING_OK;
 }
 
@@ -832,15 +842,14 @@ int inkling_grouped_weight_grad(const inkling_grouped_dims_t* dims, const void* 
     if (!aligned(x, 16) || !aligned(dout, 16) || !aligned(dweight, 16) || !aligned(offsets, 4) ||
         !aligned(row_index, 4))
         return INKLING_ERR_INVALID_ARGUMENT;
-    const bool small = group_small_wgrad(dims->dtype == INKLING_BF16 ? 1 : 0, dims->n_groups, dims->in_features,
-                                         dims->out_features);
+    const bool small = grouped_small_wgrad(dims);   // takes no workspace
     const long long side = small ? 64 : 128;   // at least this wide a tile each way
     if (dims->n_groups * ((dims->out_features + side - 1) / side) * ((dims->in_features + side - 1) / side) >
         INT32_MAX - 4096)
         return INKLING_ERR_UNSUPPORTED;
     const bool gather = row_index != nullptr && dims->rows > 0;
     const GroupedLayout L = make_grouped_layout(dims, 0, gather ? grouped_gather_bytes(dims) : 0);
-    if (workspace == nullptr || workspace_bytes < L.total) return INKLING_ERR_WORKSPACE;
+    if (!small && (workspace == nullptr || workspace_bytes < L.total)) return INKLING_ERR_WORKSPACE;
     GroupParams p = grouped_params(dims, L, workspace, false);
     hipStream_t s = (hipStream_t)stream;
     if (small) {

@@ -153,6 +153,98 @@ def test_weight_bound_long_k():
     _check_all(Case([130, 60], 2040, 520, BF16), BF16)
 
 
+LARGE = {
+    # (counts, K, N): past one 256 x 256 tile a CU, so that the tiles of the
+    # larger products run, with few rows an expert, many, and both sides of the
+    # weight gradients' row counts
+    "streamed_ragged": ([3, 0, 17, 48, 1, 33, 16, 20] * 8, 264, 1032),
+    "around_256": ([255, 256, 257, 1, 0, 511, 513, 70] * 4, 520, 2056),
+    "many_rows": ([1100, 900, 0, 1300, 1000, 1, 1500, 2000], 1032, 1544),
+    "narrow_output": ([300, 270] * 100, 72, 264),
+    "one_has_all": ([0] * 30 + [5000] + [0] * 33, 264, 1288),
+}
+
+
+@pytest.mark.parametrize("case", list(LARGE))
+def test_large_tiles(case):
+    counts, K, N = LARGE[case]
+    c = Case(counts, K, N, BF16, first=1, room=2, tokens=777, seed=4)
+    _say(f"[grouped] large {case}")
+    dims = B.make_grouped_dims(c.R, 777, len(counts), K, N, BF16)
+    assert B.grouped_workspace_size(dims) > 0 and B.grouped_weight_grad_workspace_size(dims) > 0
+    _check_all(c, BF16)
+    dw = B.grouped_weight_grad(c.dout, c.x, c.offsets, row_index=c.index)
+    dx = B.grouped_input_grad(c.dout, c.w, c.offsets, dx=_marked((c.R, K), F32))
+    torch.cuda.synchronize()
+    _close("dweight fp32", dw, *c.weight_grad(), max(counts), F32)
+    _close("dx fp32", dx, *c.input_grad(), N, F32)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_non_finite_values_on_large_tiles(value):
+    """As above, on the tiles of the larger products: a row's and a K tail's neighbours stay finite."""
+    counts = [255, 256, 257, 1, 0, 511, 513, 70] * 4
+    c = Case(counts, 520, 2056, BF16, room=2)
+    base = (*_all(c, F32)[:2], B.grouped_weight_grad(c.dout, c.x, c.offsets))
+    r = 255 + 256 + 256          # the last row of the third group
+    x, d = c.x.clone(), c.dout.clone()
+    x[r, 519] = value
+    d[r, 2055] = value
+    out = B.grouped_linear(x, c.w, c.offsets, out=_marked((c.R, c.N), F32))
+    dx = B.grouped_input_grad(d, c.w, c.offsets, dx=_marked((c.R, c.K), F32))
+    dw = B.grouped_weight_grad(c.dout, x, c.offsets)
+    torch.cuda.synchronize()
+    keep = torch.ones(c.R, dtype=torch.bool, device=DEV)
+    keep[r] = False
+    for got, ref in ((out, base[0]), (dx, base[1])):
+        assert not torch.isfinite(got[r]).any() and torch.equal(got[keep], ref[keep])
+    assert not torch.isfinite(dw[2, :, 519]).any()
+    dw[2, :, 519] = base[2][2, :, 519]
+    assert torch.equal(dw, base[2])
+
+
+def test_large_tiles_in_graphs_that_share_a_workspace():
+    """The plan and the tile counters live in the workspace: two captured graphs
+    and eager calls take turns with one."""
+    a = Case([300, 270] * 40, 264, 1032, BF16, tokens=400, seed=6)
+    b = Case([3, 0, 17, 48] * 16, 520, 1288, BF16, seed=7)
+    need = 0
+    for c in (a, b):
+        dims = B.make_grouped_dims(c.R, c.x.shape[0], len(c.counts), c.K, c.N, BF16)
+        need = max(need, B.grouped_workspace_size(dims), B.grouped_weight_grad_workspace_size(dims, True))
+    ws = torch.full((need,), 0x7F, dtype=torch.uint8, device=DEV)
+    sets = []
+    for c in (a, b):
+        bufs = (_marked((c.R, c.N), BF16), _marked((c.R, c.K), BF16), _marked((len(c.counts), c.N, c.K), BF16))
+
+        def step(c=c, bufs=bufs):
+            B.grouped_linear(c.x, c.w, c.offsets, row_index=c.index, out=bufs[0], workspace=ws)
+            B.grouped_input_grad(c.dout, c.w, c.offsets, dx=bufs[1], workspace=ws)
+            B.grouped_weight_grad(c.dout, c.x, c.offsets, row_index=c.index, dweight=bufs[2], workspace=ws)
+
+        ref = (B.grouped_linear(c.x, c.w, c.offsets, row_index=c.index),
+               B.grouped_input_grad(c.dout, c.w, c.offsets),
+               B.grouped_weight_grad(c.dout, c.x, c.offsets, row_index=c.index, weight_grad_dtype=BF16))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        side.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        sets.append((g, bufs, ref, step))
+    for turn in range(3):
+        for g, bufs, ref, step in sets:
+            for eager in (False, True):
+                for t in bufs:
+                    t.fill_(MARK)
+                step() if eager else g.replay()
+                torch.cuda.synchronize()
+                for got, want in zip(bufs, ref):
+                    assert torch.equal(got, want), f"turn {turn}"
+
+
 def test_same_x_row_many_times():
     c = Case([30, 200, 7], 128, 72, BF16, tokens=9)
     c.index.zero_()
@@ -347,7 +439,8 @@ def test_refusals():
         with pytest.raises(ValueError):
             B.grouped_linear(**kw)
     with pytest.raises(B.InklingError) as e:
-        B.grouped_linear(x, w, off, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+        B.grouped_linear(_rand((64, 64), BF16, 3), _rand((64, 1024, 64), BF16, 4), torch.arange(65, dtype=torch.int32, device=DEV),
+                         workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     assert e.value.code == B.INKLING_ERR_WORKSPACE
     with pytest.raises(B.InklingError) as e:
         B.grouped_linear(x[:, :60].contiguous(), w[:, :, :60].contiguous(), off)   # 60 columns: not a multiple of 8

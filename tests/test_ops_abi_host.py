@@ -60,8 +60,9 @@ def test_grouped_pointers(lib):
     for kw in (dict(x=None), dict(w=None), dict(o=None), dict(out=None), dict(out=FAKE), dict(out=FAKE2),
                dict(x=ODD), dict(w=ODD), dict(out=ODD), dict(o=FAKE + 2), dict(i=FAKE + 1)):
         assert fwd(**kw) == bad, kw
-    assert fwd(ws=None) == B.INKLING_ERR_WORKSPACE
-    assert fwd(n=64) == B.INKLING_ERR_WORKSPACE
+    large = _grouped(rows=9000, x_rows=9000, n_groups=64, in_features=2048, out_features=2048)
+    assert fwd(dd=large, ws=None) == B.INKLING_ERR_WORKSPACE
+    assert fwd(dd=large, n=64) == B.INKLING_ERR_WORKSPACE
     assert fwd(dd=_grouped(x_rows=99)) == bad                       # no row index: x has a row for each row
     assert fwd(dd=_grouped(x_rows=0), i=FAKE) == bad                # an index into nothing
     assert lib.inkling_grouped_linear(None, FAKE, None, FAKE, FAKE, FAKE2, FAKE, BIG, None) == bad

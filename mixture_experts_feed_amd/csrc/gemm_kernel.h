@@ -57,17 +57,18 @@ namespace {
 // The products that callers reach on their own (grouped.hip); K and N are any
 // multiples of 8 there, and a K tail reads zeros for both operands:
 // kModeGroup: out[r][n] = sum_k W_e[n][k] x[row of r][k], rounded once
+// kModeGroupDx: dx[r][n] = sum_k W_e[k][n] dout[r][k], rounded once
 // kModeGroupWgrad: dW_e[m][n] = sum_r dout[r][m] x[r][n]
-// A is read as [K][N] in kModeDAct, kModeDx and the two weight-gradient modes,
-// B in the latter.
+// A is read as [K][N] in kModeDAct, kModeDx, kModeGroupDx and the two
+// weight-gradient modes, B in the latter.
 enum { kModeGateUp = 0, kModeDown = 1, kModeGateUpRaw = 2, kModeDAct = 3, kModeWgrad = 4, kModeDx = 5,
-       kModeDownOut = 6, kModeGroup = 7, kModeGroupWgrad = 8 };
+       kModeDownOut = 6, kModeGroup = 7, kModeGroupDx = 8, kModeGroupWgrad = 9 };
 template <int MODE>
-constexpr bool grouped_mode() { return MODE == kModeGroup || MODE == kModeGroupWgrad; }
+constexpr bool grouped_mode() { return MODE == kModeGroup || MODE == kModeGroupDx || MODE == kModeGroupWgrad; }
 template <int MODE>
 constexpr bool wgrad_mode() { return MODE == kModeWgrad || MODE == kModeGroupWgrad; }
 template <int MODE>
-constexpr bool a_kn() { return MODE == kModeDAct || MODE == kModeDx || wgrad_mode<MODE>(); }
+constexpr bool a_kn() { return MODE == kModeDAct || MODE == kModeDx || MODE == kModeGroupDx || wgrad_mode<MODE>(); }
 template <int MODE>
 constexpr bool b_kn() { return wgrad_mode<MODE>(); }
 // How the workgroups of an XCD walk its range of tiles after their first:
@@ -150,7 +151,8 @@ struct GemmKArgs {
     void* out_final;
     int out_final_bf16;
     // kModeGroup: T is the rows that row_token gathers from (row_token NULL:
-    // row r reads row r), out_final_bf16 the type of out_routed
+    // row r reads row r); kModeGroup, kModeGroupDx: out_final_bf16 is the type
+    // of out_routed
 };
 
 // what the lanes past a K tail load (16 bytes serve every lane)

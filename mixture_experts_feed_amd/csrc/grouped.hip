@@ -1,18 +1,14 @@
 // Products grouped by expert with ragged row counts, reached on their own:
 //   out[r] = W_e x[row_index[r]]   dx[r] = W_e^T dout[r]   dW_e = sum_r dout[r] (x) x[row_index[r]]
-// for the rows offsets[e] <= r < offsets[e + 1] of expert e.  Three kernels:
+// for the rows offsets[e] <= r < offsets[e + 1] of expert e.  Two kernels:
 //   small_product_kernel (grouped_small.h)  64 x 64 tiles, one launch without a
 //     plan: fp32, and bf16 products with too few large tiles for the card;
-//   moe_gemm_kernel (gemm_kernel.h)  the layer's tiles: the bf16 forward, with few
-//     rows an expert (weights streamed) and many, and weight gradients of few rows;
-//   product_kernel (grouped_gemm.h)  256 x 256 tiles of four waves: bf16 input
-//     gradients, and weight gradients of many rows.
-// The latter two follow a plan: the caller's offsets made safe, and row tiles.
+//   moe_gemm_kernel (gemm_kernel.h)  the layer's tiles, in its grouped modes:
+//     everything else, after a plan (the caller's offsets made safe, row tiles).
 #include <algorithm>
 
 #include "common.h"
 #include "gemm_kernel.h"
-#include "grouped_gemm.h"
 #include "grouped_small.h"
 #include "kernels.h"
 
@@ -107,25 +103,12 @@ int grid_of(long long tiles, int per_cu) {
     return (grid + 7) / 8 * 8;
 }
 
-hipError_t launch_forward(int cfg, const GemmKArgs& a, long long max_tiles, hipStream_t stream) {
-    const dim3 grid(grid_of(max_tiles, 1));
-    if (cfg == 0)
-        hipLaunchKernelGGL((moe_gemm_kernel<bf16_t, 256, 256, 4, 2, 2, 2, 128, 8, kSchedGroup, kModeGroup>), grid,
-                           dim3(512), 0, stream, a);
-    else
-        hipLaunchKernelGGL((moe_gemm_kernel<bf16_t, 128, 16, 8, 1, 4, 4, 128, 1, kSchedStride, kModeGroup>), grid,
-                           dim3(512), 0, stream, a);
-    return hipGetLastError();
+// sched: see prefill_sched in gemm.hip
+template <int SCHED, int MODE>
+void launch_256(const GemmKArgs& a, long long max_tiles, hipStream_t stream) {
+    hipLaunchKernelGGL((moe_gemm_kernel<bf16_t, 256, 256, 4, 2, 2, 2, 128, 8, SCHED, MODE>),
+                       dim3(grid_of(max_tiles, 1)), dim3(512), 0, stream, a);
 }
-
-// Weight gradients of bf16 operands: product_kernel from this many rows an
-// expert on, below it the layer's 128 x 256 tiles, two workgroups a CU, whose
-// change from tile to tile overlaps.  Measured, us, 128 x 256 tiles against
-// product_kernel: fp32 gradients 920 / 1117 at 128 rows (4096 x 2048 weights),
-// 355 / 340 at 256 (2048 x 2048), 343 / 300 at 384 (1536 x 2048), 670 / 610 at
-// 1024; bf16 gradients (half the bytes to write) 262 / 297 at 256, 271 / 282 at
-// 384, 295 / 294 at 512, 602 / 560 at 1024, 499 / 470 at 2048.
-int wgrad_min_rows(int dw_bf16) { return dw_bf16 ? 768 : 256; }
 
 }  // namespace
 
@@ -220,23 +203,6 @@ hipError_t launch_group_small_wgrad(const GroupParams& p, const int32_t* offsets
 }
 
 hipError_t launch_group_rows(const GroupParams& p, hipStream_t stream) {
-    if (p.dtype == 1 && p.input_grad) {
-        ProductArgs a = {};
-        a.A = static_cast<const bf16_t*>(p.weight);
-        a.B = static_cast<const bf16_t*>(p.src);
-        a.offs = p.offs;
-        a.tiles = p.tiles;
-        a.num_tiles = p.num_tiles;
-        a.E = p.E;
-        a.K = p.k_len;
-        a.N = p.n_cols;
-        a.ntn = (p.n_cols + 255) / 256;
-        a.out = p.out;
-        a.out_bf16 = p.out_bf16;
-        a.counters = p.counters;
-        hipLaunchKernelGGL(product_kernel<kProdDx>, dim3(grid_of(group_max_tiles(p), 1)), dim3(256), 0, stream, a);
-        return hipGetLastError();
-    }
     GemmKArgs a = {};
     a.round_counter = p.counters;
     a.tiles = p.tiles;
@@ -252,7 +218,14 @@ hipError_t launch_group_rows(const GroupParams& p, hipStream_t stream) {
     a.N_r = p.n_cols;
     a.ntn_r = (p.n_cols + tile_cols(p.cfg) - 1) / tile_cols(p.cfg);
     a.has_routed = 1;
-    return launch_forward(p.cfg, a, group_max_tiles(p), stream);
+    a.lda_r = p.n_cols;   // input gradient: the weights as K rows of n_cols
+    const long long tiles = group_max_tiles(p);
+    if (p.cfg != 0)
+        hipLaunchKernelGGL((moe_gemm_kernel<bf16_t, 128, 16, 8, 1, 4, 4, 128, 1, kSchedStride, kModeGroup>),
+                           dim3(grid_of(tiles, 1)), dim3(512), 0, stream, a);
+    else if (p.input_grad) launch_256<kSchedGroup, kModeGroupDx>(a, tiles, stream);
+    else launch_256<kSchedGroup, kModeGroup>(a, tiles, stream);
+    return hipGetLastError();
 }
 
 hipError_t launch_group_gather(const void* src, int src_rows, const int32_t* row_index,
@@ -265,23 +238,6 @@ hipError_t launch_group_gather(const void* src, int src_rows, const int32_t* row
 
 hipError_t launch_group_wgrad(const GroupParams& p, const void* x, const void* dout, int n_in, int n_out, void* dw,
                               int dw_bf16, hipStream_t stream) {
-    if (p.rows >= (long long)p.E * wgrad_min_rows(dw_bf16)) {
-        ProductArgs a = {};
-        a.A = static_cast<const bf16_t*>(x);
-        a.B = static_cast<const bf16_t*>(dout);
-        a.offs = p.offs;
-        a.E = p.E;
-        a.N = n_in;
-        a.M = n_out;
-        a.ntn = (n_in + 255) / 256;
-        a.ntm = (n_out + 255) / 256;
-        a.out = dw;
-        a.out_bf16 = dw_bf16;
-        a.counters = p.counters;
-        const dim3 grid(grid_of((long long)p.E * a.ntm * a.ntn, 1));
-        hipLaunchKernelGGL(product_kernel<kProdWgrad>, grid, dim3(256), 0, stream, a);
-        return hipGetLastError();
-    }
     GemmKArgs a = {};
     a.round_counter = p.counters;
     a.offsets = p.offs;

@@ -7,6 +7,7 @@ If the library is missing this module raises: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -481,16 +482,21 @@ def _check(rc: int, where: str) -> None:
         raise InklingError(rc, where)
 
 
-def _same_device(dev, **tensors) -> None:
-    for n, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{n} must be on {dev}, got {t.device}")
+def _operand(t: Optional[torch.Tensor], name: str, dtype, dev) -> None:
+    """A contiguous tensor of this dtype on dev, a GPU, or None."""
+    if t is None or (t.dtype is dtype and t.get_device() == dev.index and t.is_contiguous()):
+        return   # (the CPU's get_device() is -1 and its index None)
+    _need(t, name, dtype)
+    raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+_device_count = functools.lru_cache(maxsize=None)(torch.cuda.device_count)
 
 
 def _call(dev, name: str, *args) -> None:
     """The entry point `name` on dev's current stream, with dev the current device."""
-    fn = getattr(load(), name)
-    if torch.cuda.current_device() == dev.index:
+    fn = getattr(_LIB or load(), name)
+    if _device_count() == 1 or torch.cuda.current_device() == dev.index:
         rc = fn(*args, _stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -521,45 +527,59 @@ def grouped_weight_grad_workspace_size(dims: GroupedDims, gathered: bool = False
     return int(n.value)
 
 
+# C structs and sizes by the sizes of a call: (pointer to the dims, bytes)
+@functools.lru_cache(maxsize=1024)
+def _grouped_plan(*sizes):
+    dims = make_grouped_dims(*sizes)
+    return ctypes.byref(dims), grouped_workspace_size(dims)
+
+
+@functools.lru_cache(maxsize=1024)
+def _grouped_weight_grad_plan(gathered, *sizes):
+    dims = make_grouped_dims(*sizes)
+    return ctypes.byref(dims), grouped_weight_grad_workspace_size(dims, gathered)
+
+
 def _grouped_checks(rows_name, src, weight, offsets, width, row_index):
     """Checks shared by the row products; returns (rows, E, N, K)."""
     if src.dim() != 2 or weight.dim() != 3:
         raise ValueError(f"{rows_name} must be [rows, features] and weight [n_groups, out_features, in_features]")
-    _need(src, rows_name, weight.dtype)
-    _need(weight, "weight")
+    dev = src.device
+    _operand(src, rows_name, weight.dtype, dev)
+    _operand(weight, "weight", weight.dtype, dev)
     E, N, K = weight.shape
-    if src.shape[1] != width:
-        raise ValueError(f"{rows_name} must have {width} columns, got {src.shape[1]}")
-    _grouped_plan_checks(offsets, E, row_index)
-    _same_device(src.device, weight=weight, offsets=offsets, row_index=row_index)
-    return (src.shape[0] if row_index is None else row_index.shape[0]), E, N, K
+    R, have = src.shape
+    if have != width:
+        raise ValueError(f"{rows_name} must have {width} columns, got {have}")
+    _grouped_plan_checks(offsets, E, row_index, dev)
+    return (R if row_index is None else row_index.shape[0]), E, N, K
 
 
-def _grouped_plan_checks(offsets, n_groups, row_index):
-    _need(offsets, "offsets", torch.int32)
+def _grouped_plan_checks(offsets, n_groups, row_index, dev):
+    _operand(offsets, "offsets", torch.int32, dev)
     if offsets.dim() != 1 or offsets.shape[0] != n_groups + 1:
         raise ValueError("offsets must hold n_groups + 1 values")
     if row_index is not None:
-        _need(row_index, "row_index", torch.int32)
+        _operand(row_index, "row_index", torch.int32, dev)
         if row_index.dim() != 1:
             raise ValueError("row_index must be one-dimensional")
 
 
-def _result(t, name, shape, dtype, dev):
+def _result(t, name, shape, dtype, dev, like=None):
+    """The given result tensor, checked, or a new one (`like`: a contiguous
+    operand of that shape and dtype, from which making one is cheaper)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
+        return torch.empty(shape, dtype=dtype, device=dev) if like is None else torch.empty_like(like)
+    _operand(t, name, dtype, dev)
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    _same_device(dev, **{name: t})
     return t
 
 
 def _scratch(workspace, need, dev):
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _need(workspace, "workspace", torch.uint8)
-    _same_device(dev, workspace=workspace)
+    _operand(workspace, "workspace", torch.uint8, dev)
     return workspace
 
 
@@ -574,10 +594,10 @@ def grouped_linear(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
     R, E, N, K = _grouped_checks("x", x, weight, offsets, weight.shape[-1], row_index)
     dev = x.device
     out_dtype = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
-    dims = make_grouped_dims(R, x.shape[0], E, K, N, x.dtype, out_dtype)
+    dims, need = _grouped_plan(R, x.shape[0], E, K, N, x.dtype, out_dtype)
     out = _result(out, "out", (R, N), out_dtype, dev)
-    ws = _scratch(workspace, grouped_workspace_size(dims), dev)
-    _call(dev, "inkling_grouped_linear", ctypes.byref(dims), x.data_ptr(), _ptr(row_index), weight.data_ptr(),
+    ws = _scratch(workspace, need, dev)
+    _call(dev, "inkling_grouped_linear", dims, x.data_ptr(), _ptr(row_index), weight.data_ptr(),
           offsets.data_ptr(), out.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
     return out
 
@@ -590,10 +610,10 @@ def grouped_input_grad(dout: torch.Tensor, weight: torch.Tensor, offsets: torch.
     R, E, N, K = _grouped_checks("dout", dout, weight, offsets, weight.shape[1], None)
     dev = dout.device
     dx_dtype = dx.dtype if dx is not None else dout.dtype if dx_dtype is None else dx_dtype
-    dims = make_grouped_dims(R, R, E, K, N, dout.dtype, dx_dtype)
+    dims, need = _grouped_plan(R, R, E, K, N, dout.dtype, dx_dtype)
     dx = _result(dx, "dx", (R, K), dx_dtype, dev)
-    ws = _scratch(workspace, grouped_workspace_size(dims), dev)
-    _call(dev, "inkling_grouped_input_grad", ctypes.byref(dims), dout.data_ptr(), weight.data_ptr(),
+    ws = _scratch(workspace, need, dev)
+    _call(dev, "inkling_grouped_input_grad", dims, dout.data_ptr(), weight.data_ptr(),
           offsets.data_ptr(), dx.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
     return dx
 
@@ -607,23 +627,22 @@ def grouped_weight_grad(dout: torch.Tensor, x: torch.Tensor, offsets: torch.Tens
     (`weight_grad_dtype`, or the dtype of the given `dweight`)."""
     if dout.dim() != 2 or x.dim() != 2:
         raise ValueError("dout and x must be [rows, features]")
-    _need(dout, "dout", x.dtype)
-    _need(x, "x")
+    dev = dout.device
+    _operand(dout, "dout", x.dtype, dev)
+    _operand(x, "x", x.dtype, dev)
     E = offsets.shape[0] - 1 if offsets.dim() == 1 else 0
-    _grouped_plan_checks(offsets, E, row_index)
+    _grouped_plan_checks(offsets, E, row_index, dev)
     R, N = dout.shape
     K = x.shape[1]
     if (x if row_index is None else row_index).shape[0] != R:
         raise ValueError("dout must have a row for each row of x, or for each entry of row_index")
-    dev = dout.device
-    _same_device(dev, x=x, offsets=offsets, row_index=row_index)
     wdt = dweight.dtype if dweight is not None else torch.float32 if weight_grad_dtype is None else weight_grad_dtype
     if weight_grad_dtype is not None and weight_grad_dtype != wdt:
         raise ValueError("weight_grad_dtype differs from the dtype of the given dweight")
-    dims = make_grouped_dims(R, x.shape[0], E, K, N, x.dtype, wdt)
+    dims, need = _grouped_weight_grad_plan(row_index is not None, R, x.shape[0], E, K, N, x.dtype, wdt)
     dweight = _result(dweight, "dweight", (E, N, K), wdt, dev)
-    ws = _scratch(workspace, grouped_weight_grad_workspace_size(dims, row_index is not None), dev)
-    _call(dev, "inkling_grouped_weight_grad", ctypes.byref(dims), dout.data_ptr(), x.data_ptr(), _ptr(row_index),
+    ws = _scratch(workspace, need, dev)
+    _call(dev, "inkling_grouped_weight_grad", dims, dout.data_ptr(), x.data_ptr(), _ptr(row_index),
           offsets.data_ptr(), dweight.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
     return dweight
 
@@ -643,16 +662,21 @@ def swiglu_checkpoint_size(dims: SwigluDims) -> int:
     return int(n.value)
 
 
+@functools.lru_cache(maxsize=1024)
+def _swiglu_plan(*sizes):
+    dims = make_swiglu_dims(*sizes)
+    return ctypes.byref(dims), swiglu_checkpoint_size(dims)
+
+
 def _row_checks(dev, rows, gamma, row_count):
     if gamma is not None:
-        _need(gamma, "gamma", torch.float32)
+        _operand(gamma, "gamma", torch.float32, dev)
         if gamma.numel() != rows:
             raise ValueError(f"gamma must hold {rows} values")
     if row_count is not None:
-        _need(row_count, "row_count", torch.int32)
+        _operand(row_count, "row_count", torch.int32, dev)
         if row_count.numel() != 1:
             raise ValueError("row_count must hold one value")
-    _same_device(dev, gamma=gamma, row_count=row_count)
 
 
 def swiglu_forward(h: torch.Tensor, gamma: Optional[torch.Tensor] = None, row_count: Optional[torch.Tensor] = None,
@@ -665,18 +689,21 @@ def swiglu_forward(h: torch.Tensor, gamma: Optional[torch.Tensor] = None, row_co
     row_count[0] on are left as they are."""
     if h.dim() != 2 or h.shape[1] % 2:
         raise ValueError("h must be [rows, 2 * intermediate]")
-    _need(h, "h")
-    R, I = h.shape[0], h.shape[1] // 2
     dev = h.device
+    _operand(h, "h", h.dtype, dev)
+    R, I = h.shape
+    I //= 2
     _row_checks(dev, R, gamma, row_count)
-    dims = make_swiglu_dims(R, I, h.dtype)
-    need = swiglu_checkpoint_size(dims)
+    dims, need = _swiglu_plan(R, I, h.dtype)
     out = _result(out, "out", (R, I), h.dtype, dev)
     if not save and checkpoint is not None:
         raise ValueError("save=False keeps no checkpoint: give none")
     if save:
-        checkpoint = _scratch(checkpoint, need, dev)
-    _call(dev, "inkling_swiglu_forward", ctypes.byref(dims), h.data_ptr(), _ptr(gamma), _ptr(row_count),
+        if checkpoint is None:
+            checkpoint = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _operand(checkpoint, "checkpoint", torch.uint8, dev)
+    _call(dev, "inkling_swiglu_forward", dims, h.data_ptr(), _ptr(gamma), _ptr(row_count),
           out.data_ptr(), _ptr(checkpoint), 0 if checkpoint is None else checkpoint.numel())
     return out, checkpoint
 
@@ -691,19 +718,18 @@ def swiglu_backward(dact: torch.Tensor, checkpoint: torch.Tensor, gamma: Optiona
     gradient) and dgamma are None where they are not wanted."""
     if dact.dim() != 2:
         raise ValueError("dact must be [rows, intermediate]")
-    _need(dact, "dact")
-    _need(checkpoint, "checkpoint", torch.uint8)
     R, I = dact.shape
     dev = dact.device
+    _operand(dact, "dact", dact.dtype, dev)
+    _operand(checkpoint, "checkpoint", torch.uint8, dev)
     _row_checks(dev, R, gamma, row_count)
-    _same_device(dev, checkpoint=checkpoint)
     if (act is not None and not want_act) or (dgamma is not None and not want_dgamma):
         raise ValueError("a result is both given and not wanted")
-    dims = make_swiglu_dims(R, I, dact.dtype)
+    dims, _ = _swiglu_plan(R, I, dact.dtype)
     dh = _result(dh, "dh", (R, 2 * I), dact.dtype, dev)
-    act = _result(act, "act", (R, I), dact.dtype, dev) if want_act else None
+    act = _result(act, "act", (R, I), dact.dtype, dev, like=dact) if want_act else None
     dgamma = _result(dgamma, "dgamma", (R,), torch.float32, dev) if want_dgamma else None
-    _call(dev, "inkling_swiglu_backward", ctypes.byref(dims), dact.data_ptr(), checkpoint.data_ptr(),
+    _call(dev, "inkling_swiglu_backward", dims, dact.data_ptr(), checkpoint.data_ptr(),
           checkpoint.numel(), _ptr(gamma), _ptr(row_count), dh.data_ptr(), _ptr(act), _ptr(dgamma))
     return {"dh": dh, "act": act, "dgamma": dgamma}
 
@@ -727,16 +753,22 @@ def norm_backward_workspace_size(dims: NormDims) -> int:
     return int(n.value)
 
 
+@functools.lru_cache(maxsize=1024)
+def _norm_plan(*sizes):
+    dims = make_norm_dims(*sizes)
+    return ctypes.byref(dims), norm_backward_workspace_size(dims)
+
+
 def _norm_checks(x, weight, bias):
     if x.dim() != 2:
         raise ValueError("x must be [rows, hidden]")
-    _need(x, "x")
+    dev, H = x.device, x.shape[1]
+    _operand(x, "x", x.dtype, dev)
     for t, n in ((weight, "weight"), (bias, "bias")):
         if t is not None:
-            _need(t, n, torch.float32)
-            if t.dim() != 1 or t.shape[0] != x.shape[1]:
-                raise ValueError(f"{n} must have shape ({x.shape[1]},)")
-    _same_device(x.device, weight=weight, bias=bias)
+            _operand(t, n, torch.float32, dev)
+            if t.dim() != 1 or t.shape[0] != H:
+                raise ValueError(f"{n} must have shape ({H},)")
 
 
 def norm_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -748,12 +780,12 @@ def norm_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Ten
     _norm_checks(x, weight, bias)
     R, H = x.shape
     dev = x.device
-    dims = make_norm_dims(R, H, kind, x.dtype, eps)
-    out = _result(out, "out", (R, H), x.dtype, dev)
+    dims, _ = _norm_plan(R, H, kind, x.dtype, eps)
+    out = _result(out, "out", (R, H), x.dtype, dev, like=x)
     if not save and stats is not None:
         raise ValueError("save=False keeps no stats: give none")
     stats = _result(stats, "stats", (R, 2), torch.float32, dev) if save else None
-    _call(dev, "inkling_norm_forward", ctypes.byref(dims), x.data_ptr(), weight.data_ptr(), _ptr(bias),
+    _call(dev, "inkling_norm_forward", dims, x.data_ptr(), weight.data_ptr(), _ptr(bias),
           out.data_ptr(), _ptr(stats))
     return out, stats
 
@@ -768,16 +800,15 @@ def norm_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, sta
     _norm_checks(x, weight, None)
     R, H = x.shape
     dev = x.device
-    _need(dout, "dout", x.dtype)
-    _need(stats, "stats", torch.float32)
+    _operand(dout, "dout", x.dtype, dev)
+    _operand(stats, "stats", torch.float32, dev)
     if dout.shape != x.shape or stats.shape != (R, 2):
         raise ValueError("dout must have x's shape and stats be [rows, 2]")
-    _same_device(dev, dout=dout, stats=stats)
-    dims = make_norm_dims(R, H, kind, x.dtype, 0.0)
-    ws = _scratch(workspace, norm_backward_workspace_size(dims), dev)
-    dx = _result(dx, "dx", (R, H), x.dtype, dev)
-    dweight = _result(dweight, "dweight", (H,), torch.float32, dev)
-    dbias = _result(dbias, "dbias", (H,), torch.float32, dev) if bias or dbias is not None else None
-    _call(dev, "inkling_norm_backward", ctypes.byref(dims), dout.data_ptr(), x.data_ptr(), weight.data_ptr(),
+    dims, need = _norm_plan(R, H, kind, x.dtype, 0.0)
+    ws = _scratch(workspace, need, dev)
+    dx = _result(dx, "dx", (R, H), x.dtype, dev, like=x)
+    dweight = _result(dweight, "dweight", (H,), torch.float32, dev, like=weight)
+    dbias = _result(dbias, "dbias", (H,), torch.float32, dev, like=weight) if bias or dbias is not None else None
+    _call(dev, "inkling_norm_backward", dims, dout.data_ptr(), x.data_ptr(), weight.data_ptr(),
           stats.data_ptr(), dx.data_ptr(), dweight.data_ptr(), _ptr(dbias), _ptr(ws), 0 if ws is None else ws.numel())
     return {"dx": dx, "dweight": dweight, "dbias": dbias}

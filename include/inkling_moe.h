@@ -304,8 +304,8 @@ typedef struct {
 /* workspace of inkling_grouped_linear and inkling_grouped_input_grad (0 for
  * small products: then it may be NULL) */
 int inkling_grouped_workspace_size(const inkling_grouped_dims_t* dims, size_t* bytes);
-/* workspace of inkling_grouped_weight_grad; `gathered`: called with a row_index */
-int inkling_grouped_weight_grad_workspace_size(const inkling_grouped_dims_t* dims, int gathered, size_t* bytes);
+/* workspace of inkling_grouped_weight_grad (0 likewise) */
+int inkling_grouped_weight_grad_workspace_size(const inkling_grouped_dims_t* dims, size_t* bytes);
 
 int inkling_grouped_linear(const inkling_grouped_dims_t* dims, const void* x, const int32_t* row_index,
                            const void* weight, const int32_t* offsets, void* out, void* workspace,

@@ -153,7 +153,7 @@ def load() -> ctypes.CDLL:
     gdims, sdims, ndims = (ctypes.POINTER(c) for c in (GroupedDims, SwigluDims, NormDims))
     for name, args in (
             ("inkling_grouped_workspace_size", [gdims, ctypes.POINTER(size)]),
-            ("inkling_grouped_weight_grad_workspace_size", [gdims, ctypes.c_int, ctypes.POINTER(size)]),
+            ("inkling_grouped_weight_grad_workspace_size", [gdims, ctypes.POINTER(size)]),
             ("inkling_grouped_linear", [gdims, ptr, ptr, ptr, ptr, ptr, ptr, size, ptr]),
             ("inkling_grouped_input_grad", [gdims, ptr, ptr, ptr, ptr, ptr, size, ptr]),
             ("inkling_grouped_weight_grad", [gdims, ptr, ptr, ptr, ptr, ptr, ptr, size, ptr]),
@@ -519,10 +519,10 @@ def grouped_workspace_size(dims: GroupedDims) -> int:
     return int(n.value)
 
 
-def grouped_weight_grad_workspace_size(dims: GroupedDims, gathered: bool = False) -> int:
-    """inkling_grouped_weight_grad_workspace_size; `gathered`: called with a row_index."""
+def grouped_weight_grad_workspace_size(dims: GroupedDims) -> int:
+    """inkling_grouped_weight_grad_workspace_size."""
     n = ctypes.c_size_t(0)
-    _check(load().inkling_grouped_weight_grad_workspace_size(ctypes.byref(dims), int(gathered), ctypes.byref(n)),
+    _check(load().inkling_grouped_weight_grad_workspace_size(ctypes.byref(dims), ctypes.byref(n)),
            "inkling_grouped_weight_grad_workspace_size")
     return int(n.value)
 
@@ -535,9 +535,9 @@ def _grouped_plan(*sizes):
 
 
 @functools.lru_cache(maxsize=1024)
-def _grouped_weight_grad_plan(gathered, *sizes):
+def _grouped_weight_grad_plan(*sizes):
     dims = make_grouped_dims(*sizes)
-    return ctypes.byref(dims), grouped_weight_grad_workspace_size(dims, gathered)
+    return ctypes.byref(dims), grouped_weight_grad_workspace_size(dims)
 
 
 def _grouped_checks(rows_name, src, weight, offsets, width, row_index):
@@ -639,7 +639,7 @@ def grouped_weight_grad(dout: torch.Tensor, x: torch.Tensor, offsets: torch.Tens
     wdt = dweight.dtype if dweight is not None else torch.float32 if weight_grad_dtype is None else weight_grad_dtype
     if weight_grad_dtype is not None and weight_grad_dtype != wdt:
         raise ValueError("weight_grad_dtype differs from the dtype of the given dweight")
-    dims, need = _grouped_weight_grad_plan(row_index is not None, R, x.shape[0], E, K, N, x.dtype, wdt)
+    dims, need = _grouped_weight_grad_plan(R, x.shape[0], E, K, N, x.dtype, wdt)
     dweight = _result(dweight, "dweight", (E, N, K), wdt, dev)
     ws = _scratch(workspace, need, dev)
     _call(dev, "inkling_grouped_weight_grad", dims, dout.data_ptr(), x.data_ptr(), _ptr(row_index),

@@ -702,7 +702,7 @@ int check_grouped_dims(const inkling_grouped_dims_t* d) {
 }
 
 struct GroupedLayout {
-    size_t offs, counters, num_tiles, tiles, x_sorted, total;
+    size_t offs, counters, num_tiles, tiles, total;
 };
 
 bool grouped_small(const inkling_grouped_dims_t* d, bool input_grad) {
@@ -714,8 +714,8 @@ bool grouped_small_wgrad(const inkling_grouped_dims_t* d) {
     return group_small_wgrad(d->dtype == INKLING_BF16 ? 1 : 0, d->n_groups, d->in_features, d->out_features);
 }
 
-// row_tiles: entries of the tile list; gather_bytes: rows of x in row order
-GroupedLayout make_grouped_layout(const inkling_grouped_dims_t* d, size_t row_tiles, size_t gather_bytes) {
+// row_tiles: entries of the tile list
+GroupedLayout make_grouped_layout(const inkling_grouped_dims_t* d, size_t row_tiles) {
     GroupedLayout L = {};
     size_t o = 0;
     auto take = [&](size_t bytes) {
@@ -727,7 +727,6 @@ GroupedLayout make_grouped_layout(const inkling_grouped_dims_t* d, size_t row_ti
     L.counters = take(kRoundCounters * 4);
     L.num_tiles = take(4);
     L.tiles = take(row_tiles * sizeof(RoutedTile));
-    L.x_sorted = take(gather_bytes);
     L.total = o;
     return L;
 }
@@ -737,10 +736,6 @@ size_t grouped_row_tiles(const inkling_grouped_dims_t* d) {
     const int rows = (int)d->rows, E = d->n_groups;
     return (size_t)std::max(group_max_row_tiles(rows, E, group_cfg(rows, E, false)),
                             group_max_row_tiles(rows, E, group_cfg(rows, E, true)));
-}
-
-size_t grouped_gather_bytes(const inkling_grouped_dims_t* d) {
-    return (size_t)d->rows * d->in_features * 2;   // bf16 (fp32 takes the small tiles)
 }
 
 GroupParams grouped_params(const inkling_grouped_dims_t* d, const GroupedLayout& L, void* ws, bool input_grad) {
@@ -775,7 +770,7 @@ int grouped_rows(const inkling_grouped_dims_t* d, bool input_grad, const void* s
         !aligned(row_index, 4))
         return INKLING_ERR_INVALID_ARGUMENT;
     const bool small = grouped_small(d, input_grad);   // takes no workspace
-    const GroupedLayout L = make_grouped_layout(d, grouped_row_tiles(d), 0);
+    const GroupedLayout L = make_grouped_layout(d, grouped_row_tiles(d));
     if (!small && (workspace == nullptr || workspace_bytes < L.total)) return INKLING_ERR_WORKSPACE;
     GroupParams p = grouped_params(d, L, workspace, input_grad);
     if ((small ? group_small_tiles(p.rows, p.E, p.n_cols) : group_max_tiles(p)) > INT32_MAX - 4096)
@@ -803,17 +798,15 @@ int inkling_grouped_workspace_size(const inkling_grouped_dims_t* dims, size_t* b
     if (rc != INKLING_OK) return rc;
     if (bytes == nullptr) return INKLING_ERR_INVALID_ARGUMENT;
     const bool small = grouped_small(dims, false) && grouped_small(dims, true);
-    *bytes = small ? 0 : make_grouped_layout(dims, grouped_row_tiles(dims), 0).total;
+    *bytes = small ? 0 : make_grouped_layout(dims, grouped_row_tiles(dims)).total;
     return INKLING_OK;
 }
 
-int inkling_grouped_weight_grad_workspace_size(const inkling_grouped_dims_t* dims, int gathered, size_t* bytes) {
+int inkling_grouped_weight_grad_workspace_size(const inkling_grouped_dims_t* dims, size_t* bytes) {
     const int rc = check_grouped_dims(dims);
     if (rc != INKLING_OK) return rc;
     if (bytes == nullptr) return INKLING_ERR_INVALID_ARGUMENT;
-    *bytes = grouped_small_wgrad(dims)
-                 ? 0
-                 : make_grouped_layout(dims, 0, gathered ? grouped_gather_bytes(dims) : 0).total;
+    *bytes = grouped_small_wgrad(dims) ? 0 : make_grouped_layout(dims, 0).total;
     return INKLING_OK;
 }
 
@@ -847,22 +840,16 @@ int inkling_grouped_weight_grad(const inkling_grouped_dims_t* dims, const void* 
     if (dims->n_groups * ((dims->out_features + side - 1) / side) * ((dims->in_features + side - 1) / side) >
         INT32_MAX - 4096)
         return INKLING_ERR_UNSUPPORTED;
-    const bool gather = row_index != nullptr && dims->rows > 0;
-    const GroupedLayout L = make_grouped_layout(dims, 0, gather ? grouped_gather_bytes(dims) : 0);
+    const GroupedLayout L = make_grouped_layout(dims, 0);
     if (!small && (workspace == nullptr || workspace_bytes < L.total)) return INKLING_ERR_WORKSPACE;
     GroupParams p = grouped_params(dims, L, workspace, false);
     hipStream_t s = (hipStream_t)stream;
+    p.row_index = dims->rows > 0 ? row_index : nullptr;
     if (small) {
-        p.row_index = row_index;
         HIP_TRY(launch_group_small_wgrad(p, offsets, x, dout, dims->in_features, dims->out_features, dweight, s));
         return INKLING_OK;
     }
     HIP_TRY(launch_group_plan(p, offsets, false, s));
-    if (gather) {
-        void* sorted = at<void>(workspace, L.x_sorted);
-        HIP_TRY(launch_group_gather(x, p.src_rows, row_index, p.offs, p.E, p.rows, dims->in_features, sorted, s));
-        x = sorted;
-    }
     HIP_TRY(launch_group_wgrad(p, x, dout, dims->in_features, dims->out_features, dweight, p.out_bf16, s));
     return INKLING_OK;
 }

@@ -150,10 +150,16 @@ struct GemmKArgs {
     const int32_t* pos;
     void* out_final;
     int out_final_bf16;
-    // kModeGroup: T is the rows that row_token gathers from (row_token NULL:
-    // row r reads row r); kModeGroup, kModeGroupDx: out_final_bf16 is the type
+    // kModeGroup, kModeGroupWgrad: T is the rows of x, which row_token gathers
+    // from (row_token NULL: row r reads row r); kModeGroup, kModeGroupDx: out_final_bf16 is the type
     // of out_routed
 };
+
+// an int at an address that is the same for the whole wave, written by an earlier
+// kernel only: a scalar load, which the waits for vector loads do not count
+__device__ __forceinline__ int uniform_load(const int32_t* p) {
+    return *(const __attribute__((address_space(4))) int32_t*)p;
+}
 
 // what the lanes past a K tail load (16 bytes serve every lane)
 __device__ uint4 zero_chunk = {0u, 0u, 0u, 0u};
@@ -373,6 +379,7 @@ __device__ __forceinline__ Tile<TE> decode_tile(const GemmKArgs& a, int L, int B
         t.N = a.wg_N;
         if (!t.is_shared) {
             const int r0 = a.offsets[pr];
+            t.grow0 = r0;
             if constexpr (MODE == kModeGroupWgrad) {
                 constexpr int kStage = 64 / (int)sizeof(TE);   // whole stages of 64 bytes of K
                 t.K = (a.offsets[pr + 1] - r0 + kStage - 1) / kStage * kStage;
@@ -655,6 +662,24 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
     const TE* b_src[B_PW];
     int a_k = 0, b_k = 0, rows_valid_ld = 1, seg_ld = 1, cnt_ld = 0, lda_ld = 0, ldb_ld = 0, m0_ld = 0;
     size_t a_seg = 0, a_seg_step = 0;
+    // kModeGroupWgrad with gathered rows of x: the row numbers of the K rows that
+    // this wave loads, for the next two stages, in scalar registers (they are the
+    // same for the 16 lanes of a K row): the loads of a stage find them there
+    constexpr bool GATHER_A = MODE == kModeGroupWgrad;
+    static_assert(!GATHER_A || SA == 2, "row numbers two stages ahead");
+    int a_idx[GATHER_A ? 2 : 1][GATHER_A ? A_PW : 1][GATHER_A ? RPIA : 1];
+    int r0_ld = 0;
+    auto row_numbers = [&](auto S_, int k) __attribute__((always_inline)) {
+        if constexpr (GATHER_A) {
+#pragma unroll
+            for (int q = 0; q < A_PW; ++q)
+#pragma unroll
+                for (int i = 0; i < RPIA; ++i) {
+                    const int r = __builtin_amdgcn_readfirstlane(r0_ld + min(k + RPIA * (wv + NW * q) + i, cnt_ld - 1));
+                    a_idx[decltype(S_)::value & 1][q][i] = uniform_load(a.row_token + r);
+                }
+        }
+    };
     auto setup = [&](const Tile<TE>& t) __attribute__((always_inline)) {
 #pragma unroll
         for (int q = 0; q < A_PW; ++q) {
@@ -662,7 +687,8 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
                 const int r = RPIA * (wv + NW * q) + lane / CHA;   // K row within a stage
                 const int c = (lane % CHA) ^ swk(r);                // chunk this lane's LDS position holds
                 const int n = min(t.n0 + c * EPC, t.N - EPC);      // columns past N re-read the last chunk
-                a_src[q] = t.A + (long long)(n / t.segn) * t.segstride + n % t.segn + (size_t)r * t.lda;
+                if (GATHER_A && a.row_token != nullptr) a_src[q] = reinterpret_cast<const TE*>(a.A_routed) + n;
+                else a_src[q] = t.A + (long long)(n / t.segn) * t.segstride + n % t.segn + (size_t)r * t.lda;
             } else {
                 const int r = RPL * (wv + NW * q) + lr;
                 a_src[q] = t.A + (size_t)min(t.n0 + r, t.N - 1) * t.lda + (lp ^ sw(r)) * EPC;   // rows past N re-read N-1
@@ -699,6 +725,11 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
         lda_ld = t.lda;
         ldb_ld = t.ldb;
         m0_ld = t.t0;
+        if (GATHER_A && a.row_token != nullptr && t.cnt > 0) {
+            r0_ld = t.grow0;
+            row_numbers(std::integral_constant<int, 0>{}, 0);
+            row_numbers(std::integral_constant<int, 1>{}, BK);
+        }
     };
     // Weight stage j is issued SA stage boundaries ahead of its use, token stage
     // j SB ahead (tokens first within a boundary).  A wave's weight loads per
@@ -711,6 +742,25 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
     // experts along K).
     auto issue_a = [&](auto S_) __attribute__((always_inline)) {
         uint8_t* __restrict__ dst = stage_a(S_);
+        if constexpr (GATHER_A) {
+            if (a.row_token != nullptr) {
+#pragma unroll
+                for (int q = 0; q < A_PW; ++q) {
+                    const int i = lane / CHA;   // of the wave load's RPIA K rows
+                    int row = a_idx[decltype(S_)::value & 1][q][0];
+#pragma unroll
+                    for (int j = 1; j < RPIA; ++j) row = i == j ? a_idx[decltype(S_)::value & 1][q][j] : row;
+                    row = max(0, min(row, a.T - 1));   // an index out of range reads a row in it
+                    const TE* src = a_src[q] + (size_t)row * lda_ld;
+                    if (a_k + RPIA * (wv + NW * q) + i >= cnt_ld) src = reinterpret_cast<const TE*>(&zero_chunk);
+                    __builtin_amdgcn_global_load_lds((glb_void_t*)src, (lds_void_t*)(dst + (wv + NW * q) * 1024), 16, 0,
+                                                     0);
+                }
+                a_k += BK;
+                row_numbers(S_, a_k + BK);
+                return;
+            }
+        }
         if constexpr (GRP) {
             // the stage that holds the K tail: rows (AKN) or chunks past it load zeros
             if (a_k + BK > cnt_ld) {

@@ -78,21 +78,6 @@ __global__ __launch_bounds__(kMaxGroups) void group_plan_kernel(const int32_t* _
     }
 }
 
-// out[r] = src[row_index[r]] for offs[0] <= r < offs[E] (an index out of range
-// takes the nearest row in it): rows of D elements, D a multiple of 8.
-__global__ __launch_bounds__(256) void group_gather_kernel(const bf16_t* __restrict__ src, int src_rows,
-                                                           const int32_t* __restrict__ row_index,
-                                                           const int32_t* __restrict__ offs, int E, int D,
-                                                           bf16_t* __restrict__ out) {
-    const int nv = D / 8;
-    for (int r = offs[0] + blockIdx.x; r < offs[E]; r += gridDim.x) {
-        const size_t row = (size_t)max(0, min(row_index[r], src_rows - 1));
-        const uint4* s = reinterpret_cast<const uint4*>(src + row * D);
-        uint4* o = reinterpret_cast<uint4*>(out + (size_t)r * D);
-        for (int v = threadIdx.x; v < nv; v += 256) o[v] = s[v];
-    }
-}
-
 // Tile configurations (see gemm.hip for what they measured in the layer):
 // 0: 256 output columns x 256 rows; 1: 128 x 16, weights streamed.
 int tile_rows(int cfg) { return cfg == 0 ? 256 : 16; }
@@ -228,20 +213,14 @@ hipError_t launch_group_rows(const GroupParams& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_group_gather(const void* src, int src_rows, const int32_t* row_index,
-                               const int32_t* offs, int E, int rows, int D, void* out, hipStream_t stream) {
-    const int blocks = std::min(rows, 4096);
-    hipLaunchKernelGGL(group_gather_kernel, dim3(blocks), dim3(256), 0, stream, static_cast<const bf16_t*>(src),
-                       src_rows, row_index, offs, E, D, static_cast<bf16_t*>(out));
-    return hipGetLastError();
-}
-
 hipError_t launch_group_wgrad(const GroupParams& p, const void* x, const void* dout, int n_in, int n_out, void* dw,
                               int dw_bf16, hipStream_t stream) {
     GemmKArgs a = {};
     a.round_counter = p.counters;
     a.offsets = p.offs;
     a.poff = p.offs;      // tile costs by row count
+    a.row_token = p.row_index;
+    a.T = p.src_rows;
     a.A_routed = x;
     a.B_routed = dout;
     a.lda_r = n_in;

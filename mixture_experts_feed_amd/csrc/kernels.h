@@ -171,7 +171,7 @@ struct GroupParams {
     int rows, E;
     const void* src;       // rows of k_len values
     const void* weight;    // [E][n_out][n_in]
-    const int32_t* row_index;   // row r reads src[row_index[r]] (NULL: src[r]); forward only
+    const int32_t* row_index;   // row r reads src[row_index[r]] (NULL: src[r]); not the input gradient
     int src_rows;
     void* out;             // [rows][n_cols]
     int out_bf16;
@@ -198,10 +198,7 @@ hipError_t launch_group_small_wgrad(const GroupParams& p, const int32_t* offsets
 // `tiles`: the row tiles too
 hipError_t launch_group_plan(const GroupParams& p, const int32_t* offsets, bool tiles, hipStream_t stream);
 hipError_t launch_group_rows(const GroupParams& p, hipStream_t stream);
-// out[r] = src[row_index[r]] for the rows of the plan
-hipError_t launch_group_gather(const void* src, int src_rows, const int32_t* row_index,
-                               const int32_t* offs, int E, int rows, int D, void* out, hipStream_t stream);
-// dw[e] = dout^T x over the rows of e (x and dout in row order)
+// dw[e] = dout^T x over the rows of e (dout in row order, x through row_index)
 hipError_t launch_group_wgrad(const GroupParams& p, const void* x, const void* dout, int n_in, int n_out, void* dw,
                               int dw_bf16, hipStream_t stream);
 

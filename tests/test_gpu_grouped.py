@@ -211,7 +211,7 @@ def test_large_tiles_in_graphs_that_share_a_workspace():
     need = 0
     for c in (a, b):
         dims = B.make_grouped_dims(c.R, c.x.shape[0], len(c.counts), c.K, c.N, BF16)
-        need = max(need, B.grouped_workspace_size(dims), B.grouped_weight_grad_workspace_size(dims, True))
+        need = max(need, B.grouped_workspace_size(dims), B.grouped_weight_grad_workspace_size(dims))
     ws = torch.full((need,), 0x7F, dtype=torch.uint8, device=DEV)
     sets = []
     for c in (a, b):
@@ -347,7 +347,7 @@ def test_repeatable_on_side_streams_and_with_a_stale_workspace():
     ref = _all(c, BF16)
     torch.cuda.synchronize()
     dims = B.make_grouped_dims(c.R, 77, 5, 200, 136, BF16)
-    ws = torch.full((max(B.grouped_workspace_size(dims), B.grouped_weight_grad_workspace_size(dims, True)),), 0xA5,
+    ws = torch.full((max(B.grouped_workspace_size(dims), B.grouped_weight_grad_workspace_size(dims)),), 0xA5,
                     dtype=torch.uint8, device=DEV)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -367,7 +367,7 @@ def test_two_graphs_that_share_a_workspace():
     a, b = Case([30, 0, 400], 136, 72, BF16, tokens=40), Case([3, 5, 1], 72, 264, BF16)
     dims = [B.make_grouped_dims(c.R, c.x.shape[0], 3, c.K, c.N, BF16) for c in (a, b)]
     ws = torch.empty(max([B.grouped_workspace_size(d) for d in dims] +
-                         [B.grouped_weight_grad_workspace_size(d, True) for d in dims]), dtype=torch.uint8, device=DEV)
+                         [B.grouped_weight_grad_workspace_size(d) for d in dims]), dtype=torch.uint8, device=DEV)
     graphs, outs = [], []
     for c in (a, b):
         bufs = (_marked((c.R, c.N), BF16), _marked((c.R, c.K), BF16), _marked((3, c.N, c.K), F32))

@@ -46,7 +46,7 @@ def _grouped(**kw):
 def test_grouped_dims(lib, kw, code):
     d, n = _grouped(**kw), ctypes.c_size_t(0)
     assert lib.inkling_grouped_workspace_size(ctypes.byref(d), ctypes.byref(n)) == code
-    assert lib.inkling_grouped_weight_grad_workspace_size(ctypes.byref(d), 1, ctypes.byref(n)) == code
+    assert lib.inkling_grouped_weight_grad_workspace_size(ctypes.byref(d), ctypes.byref(n)) == code
     assert lib.inkling_grouped_linear(ctypes.byref(d), FAKE, FAKE, FAKE, FAKE, FAKE2, FAKE, BIG, None) == code
     assert lib.inkling_grouped_input_grad(ctypes.byref(d), FAKE, FAKE, FAKE, FAKE2, FAKE, BIG, None) == code
     assert lib.inkling_grouped_weight_grad(ctypes.byref(d), FAKE, FAKE, FAKE, FAKE, FAKE2, FAKE, BIG, None) == code
@@ -76,12 +76,10 @@ def test_grouped_pointers(lib):
                dict(out=ODD)):
         assert dw(**kw) == bad, kw
     n = ctypes.c_size_t(0)
-    big = _grouped(n_groups=64, in_features=2048, out_features=2048)   # gathers x into the workspace
-    assert lib.inkling_grouped_weight_grad_workspace_size(ctypes.byref(big), 0, ctypes.byref(n)) == 0
-    plain = n.value
-    assert lib.inkling_grouped_weight_grad_workspace_size(ctypes.byref(big), 1, ctypes.byref(n)) == 0
-    assert n.value >= plain + 100 * 2048 * 2
-    assert lib.inkling_grouped_weight_grad(ctypes.byref(big), FAKE, FAKE2, FAKE, FAKE, FAKE3, FAKE, plain,
+    big = _grouped(n_groups=64, in_features=2048, out_features=2048)
+    assert lib.inkling_grouped_weight_grad_workspace_size(ctypes.byref(big), ctypes.byref(n)) == 0
+    assert n.value > 0
+    assert lib.inkling_grouped_weight_grad(ctypes.byref(big), FAKE, FAKE2, FAKE, FAKE, FAKE3, FAKE, n.value - 1,
                                            None) == B.INKLING_ERR_WORKSPACE
     assert lib.inkling_grouped_workspace_size(ctypes.byref(d), None) == bad
 

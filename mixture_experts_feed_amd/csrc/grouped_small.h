@@ -112,7 +112,7 @@ __global__ __launch_bounds__(256) void small_product_kernel(const SmallArgs a) {
     __shared__ __attribute__((aligned(16))) uint8_t sb[2][SIZE_B];
     const TE* A = static_cast<const TE*>(a.A);
     const TE* B = static_cast<const TE*>(a.B);
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     // ---- tile --------------------------------------------------------------------
     int n0, m0, rows, K;    // first column, first row of out, rows of the tile
@@ -224,6 +224,9 @@ __global__ __launch_bounds__(256) void small_product_kernel(const SmallArgs a) {
             return v;
         }
     };
+    // 16-blocks of the wave that hold columns and rows: the others are skipped (an
+    // fp32 tile of few rows would be bound by the products of its empty ones)
+    const int nvi = (a.N - n0 - an + 15) >> 4, nvj = (rows - bm + 15) >> 4;
     f32x4_t acc[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -252,7 +255,8 @@ __global__ __launch_bounds__(256) void small_product_kernel(const SmallArgs a) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) mma16<TE>(acc[i][j], fa[i], fb[j]);
+                        for (int j = 0; j < 2; ++j)
+                            if (i < nvi && j < nvj) mma16<TE>(acc[i][j], fa[i], fb[j]);
                 }
             }
         });

@@ -707,11 +707,13 @@ struct GroupedLayout {
 
 bool grouped_small(const inkling_grouped_dims_t* d, bool input_grad) {
     return group_small(d->dtype == INKLING_BF16 ? 1 : 0, (int)d->rows, d->n_groups,
-                       input_grad ? d->in_features : d->out_features);
+                       input_grad ? d->in_features : d->out_features,
+                       input_grad ? d->out_features : d->in_features);
 }
 
 bool grouped_small_wgrad(const inkling_grouped_dims_t* d) {
-    return group_small_wgrad(d->dtype == INKLING_BF16 ? 1 : 0, d->n_groups, d->in_features, d->out_features);
+    return group_small_wgrad(d->dtype == INKLING_BF16 ? 1 : 0, (int)d->rows, d->n_groups, d->in_features,
+                             d->out_features);
 }
 
 // row_tiles: entries of the tile list

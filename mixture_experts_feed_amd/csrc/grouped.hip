@@ -120,20 +120,32 @@ hipError_t launch_group_plan(const GroupParams& p, const int32_t* offsets, bool 
     return hipGetLastError();
 }
 
-// 64 x 64 tiles below one 256 x 256 tile a CU.  Measured, us, forward, 64 x 64
-// against 256 x 256: 13 / 19 at 12 experts of 30 rows (512 x 512), 28 / 40 at 16
-// of 256 rows (1024 x 1024, 128 large tiles), 46 / 45 at 16 of 512 (192), 50 / 46 at
-// 8 of 512 (2048 x 1024, 192).  fp32 takes them at every size: 13 / 34 us at 8
-// experts of 83 rows (136 x 200), 50 / 84 at 32 of 64 (1024 x 1024), and up to 22%
-// slower on large products (727 / 594 at 16 of 512, 2048 x 2048), which bf16 is for.
-bool group_small(int dtype, int rows, int E, int n_cols) {
+// The row products (forward, input gradient) on 64 x 64 tiles:
+// - below one 256 x 256 tile a CU.  Forward, us, 64 x 64 against 256 x 256: 13 / 19
+//   at 12 experts of 30 rows (512 x 512), 28 / 40 at 16 of 256 rows (1024 x 1024, 128
+//   large tiles), 46 / 45 at 16 of 512 (192), 46 / 45 at 8 of 512 (2048 x 1024, 192);
+// - with at most 64 rows an expert while the weights are at most 2^27 values (beyond,
+//   streaming them past 16-row tiles wins).  Forward and input gradient: 32, 32 against
+//   50, 38 at 64 experts of 40 rows (1024 x 1024), 17, 17 against 16, 28 at 128 of 2
+//   (512 x 512), 48, 48 against 46, 58 at 128 of 2 (1024 x 1024); 207, 210 against 155,
+//   206 at 128 of 2 (2048 x 2048, 2^29 values);
+// - fp32 at every size: 11 / 34 us at 8 experts of 83 rows (136 x 200), 50 / 84 at 32
+//   of 64 (1024 x 1024), and up to 24% slower on large products (737 / 594 at 16 of
+//   512, 2048 x 2048), which bf16 is for.
+bool group_small(int dtype, int rows, int E, int n_cols, int k_len) {
     if (dtype == 0) return true;
+    if (rows <= 64LL * E && (double)E * n_cols * k_len <= (double)(1 << 27)) return true;
     return group_max_row_tiles(rows, E, 0) * ((n_cols + 255) / 256) < 256;
 }
 
-bool group_small_wgrad(int dtype, int E, int n_in, int n_out) {
+// The weight gradients on 64 x 64 tiles: up to 256 rows an expert and 24 M
+// values.  us, against 128 x 256 tiles: 22 / 30 at 64 experts of 100 rows (512 x
+// 512), 31 / 33 at 16 of 256 (1024 x 1024), 22 / 30 at 40 of 3 (1024 x 512); 49 / 40 at
+// 16 of 512 (1024 x 1024), 42 / 38 at 32 of 128 (1024 x 1024, 34 M values), 54 / 41 at
+// 12 of 30 (2048 x 2048, 50 M).  fp32 at every size, as above.
+bool group_small_wgrad(int dtype, int rows, int E, int n_in, int n_out) {
     if (dtype == 0) return true;
-    return (long long)E * ((n_out + 255) / 256) * ((n_in + 127) / 128) < 256;
+    return rows <= 256LL * E && (double)E * n_in * n_out <= 24e6;
 }
 
 long long group_small_tiles(int rows, int E, int n_cols) {

@@ -188,8 +188,8 @@ long long group_max_row_tiles(int rows, int E, int cfg);
 long long group_max_tiles(const GroupParams& p);   // row tiles x column tiles
 // whether the products run on 64 x 64 tiles, from the caller's offsets: without
 // a plan (offs, tiles, num_tiles and counters unused)
-bool group_small(int dtype, int rows, int E, int n_cols);
-bool group_small_wgrad(int dtype, int E, int n_in, int n_out);
+bool group_small(int dtype, int rows, int E, int n_cols, int k_len);
+bool group_small_wgrad(int dtype, int rows, int E, int n_in, int n_out);
 long long group_small_tiles(int rows, int E, int n_cols);
 hipError_t launch_group_small(const GroupParams& p, const int32_t* offsets, hipStream_t stream);
 hipError_t launch_group_small_wgrad(const GroupParams& p, const int32_t* offsets, const void* x, const void* dout,

@@ -157,11 +157,11 @@ LARGE = {
     # (counts, K, N): past one 256 x 256 tile a CU, so that the tiles of the
     # larger products run, with few rows an expert, many, and both sides of the
     # weight gradients' row counts
-    "streamed_ragged": ([3, 0, 17, 48, 1, 33, 16, 20] * 8, 264, 1032),
+    "streamed_ragged": ([3, 0, 17, 48, 1, 33, 16, 20] * 8, 1032, 2056),
     "around_256": ([255, 256, 257, 1, 0, 511, 513, 70] * 4, 520, 2056),
     "many_rows": ([1100, 900, 0, 1300, 1000, 1, 1500, 2000], 1032, 1544),
     "narrow_output": ([300, 270] * 100, 72, 264),
-    "one_has_all": ([0] * 30 + [5000] + [0] * 33, 264, 1288),
+    "one_has_all": ([0] * 30 + [5000] + [0] * 33, 264, 2568),
 }
 
 
@@ -207,7 +207,7 @@ def test_large_tiles_in_graphs_that_share_a_workspace():
     """The plan and the tile counters live in the workspace: two captured graphs
     and eager calls take turns with one."""
     a = Case([300, 270] * 40, 264, 1032, BF16, tokens=400, seed=6)
-    b = Case([3, 0, 17, 48] * 16, 520, 1288, BF16, seed=7)
+    b = Case([3, 0, 17, 48] * 16, 1032, 2056, BF16, seed=7)
     need = 0
     for c in (a, b):
         dims = B.make_grouped_dims(c.R, c.x.shape[0], len(c.counts), c.K, c.N, BF16)
@@ -439,8 +439,8 @@ def test_refusals():
         with pytest.raises(ValueError):
             B.grouped_linear(**kw)
     with pytest.raises(B.InklingError) as e:
-        B.grouped_linear(_rand((64, 64), BF16, 3), _rand((64, 1024, 64), BF16, 4), torch.arange(65, dtype=torch.int32, device=DEV),
-                         workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+        B.grouped_linear(_rand((4480, 64), BF16, 3), _rand((64, 1024, 64), BF16, 4),
+                         torch.arange(65, dtype=torch.int32, device=DEV) * 70, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     assert e.value.code == B.INKLING_ERR_WORKSPACE
     with pytest.raises(B.InklingError) as e:
         B.grouped_linear(x[:, :60].contiguous(), w[:, :, :60].contiguous(), off)   # 60 columns: not a multiple of 8

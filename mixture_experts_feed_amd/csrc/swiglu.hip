@@ -15,7 +15,10 @@
 // Both passes are one read of their inputs and one write of their outputs, so
 // HBM bounds them: per row of I columns bf16 moves 8 I bytes forward (4 I in,
 // 2 I + 2 I out) and 10 I backward (2 I + 2 I in, 4 I + 2 I out).  A lane holds
-// 16 columns (8 pairs): 16-byte accesses to the bytes and to bf16 act.
+// 16 bytes of h (8 bf16 or 4 fp32 columns), so that every access of a wave is
+// one contiguous run; with 16 columns a lane, two accesses 32 bytes apart, the
+// backward took 268 us for 65536 rows of 2048 where this takes 234 (5.7 TB/s; the
+// forward 201 us, 5.4 TB/s).
 #include <algorithm>
 
 #include "common.h"
@@ -26,7 +29,11 @@ namespace inkling {
 
 namespace {
 
-constexpr int kCols = 16;   // columns of h a lane holds; two lanes share an exponent
+// columns of h a lane holds, and lanes that share an exponent
+template <typename TE>
+constexpr int cols() { return 16 / (int)sizeof(TE); }
+template <typename TE>
+constexpr int block_lanes() { return 32 / cols<TE>(); }
 
 // bf16 rows take the hardware exponential and reciprocal (a relative error of a
 // few 2^-22 for |v| < 40, far below bf16's half step 2^-8); fp32 rows the
@@ -37,13 +44,6 @@ __device__ __forceinline__ float sigmoid_of(float v) {
     else return 1.0f / (1.0f + expf(-v));
 }
 
-template <typename TE, int N>
-__device__ __forceinline__ void load_cols(const TE* p, float* v) {
-    constexpr int V = 16 / sizeof(TE);
-#pragma unroll
-    for (int i = 0; i < N; i += V) widen(load_raw<TE, V>(p + i), v + i);
-}
-
 // Kept byte of the exponent for a block whose largest |h| has these bits.
 // Adding 0x1FFFF carries into the exponent exactly when the significand passes
 // 127/64 = 1.1111110b, the largest that 127 steps of 2^(exponent - 6) hold.
@@ -52,74 +52,80 @@ __device__ __forceinline__ int exponent_byte(uint32_t top) {
     return max((int)((top + 0x1FFFFu) >> 23) - 6, 1);
 }
 
-template <typename TE>
+template <typename TE, bool NT>
 __global__ __launch_bounds__(256) void swiglu_forward_kernel(const TE* __restrict__ h, const float* __restrict__ gamma,
                                                              const int32_t* __restrict__ row_count, int row0, int rows,
                                                              int I, TE* __restrict__ act, int8_t* __restrict__ kept,
                                                              uint8_t* __restrict__ exps) {
+    constexpr int C = cols<TE>(), P = C / 2, BL = block_lanes<TE>();
     const int end = row_count != nullptr ? max(0, min(rows, *row_count - row0)) : rows;
-    const uint32_t per_row = (uint32_t)I / 8;                 // lanes a row takes
+    const uint32_t per_row = 2u * (uint32_t)I / C;            // lanes a row takes
     const uint32_t total = (uint32_t)end * per_row;           // < 2^31 (launcher)
     for (uint32_t c = blockIdx.x * 256 + threadIdx.x; c < total; c += gridDim.x * 256) {
         const size_t row = row0 + c / per_row;
-        const int col = (int)(c % per_row);                   // 16 columns of h, 8 of act
-        const size_t at = row * 2 * I + (size_t)col * kCols;
-        float v[kCols];
-        load_cols<TE, kCols>(h + at, v);
+        const uint32_t lane = c % per_row;
+        const size_t at = row * 2 * I + (size_t)lane * C;
+        float v[C];
+        widen<TE, C>(get<Raw<TE, C>, NT>(h + at), v);
         const float gm = gamma != nullptr ? gamma[row] : 1.0f;
-        float a[kCols / 2];
+        float a[P];
 #pragma unroll
-        for (int i = 0; i < kCols / 2; ++i) a[i] = gm * (v[2 * i] * sigmoid_of<TE>(v[2 * i]) * v[2 * i + 1]);
-        store_vec<TE, kCols / 2>(act + row * I + (size_t)col * (kCols / 2), a);
+        for (int i = 0; i < P; ++i) a[i] = gm * (v[2 * i] * sigmoid_of<TE>(v[2 * i]) * v[2 * i + 1]);
+        put<NT>(act + at / 2, narrow<TE, P>(a));
         if (kept != nullptr) {
             uint32_t top = 0;   // integer order of |h|: NaN above infinity
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-            top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+            for (int i = 0; i < C; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int d = 1; d < BL; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
             const int e = exponent_byte(top);
             const float inv = e == 255 ? 0.0f : __uint_as_float((uint32_t)(254 - e) << 23);
             // h / 2^e + 1.5 2^23 rounds to an integer, nearest even, whose low
             // byte is the int8
-            uint32_t w[4];
+            Raw<int8_t, C> w;
+            uint32_t word[C / 4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < C / 4; ++j) {
                 uint32_t b[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(__builtin_fmaf(v[4 * j + i], inv, 12582912.0f));
-                w[j] = (b[0] & 0xFFu) | (b[1] & 0xFFu) << 8 | (b[2] & 0xFFu) << 16 | b[3] << 24;
+                word[j] = (b[0] & 0xFFu) | (b[1] & 0xFFu) << 8 | (b[2] & 0xFFu) << 16 | b[3] << 24;
             }
-            *reinterpret_cast<uint4*>(kept + at) = make_uint4(w[0], w[1], w[2], w[3]);
-            if ((col & 1) == 0) exps[row * (size_t)(I / 16) + (col >> 1)] = (uint8_t)e;
+            __builtin_memcpy(&w, word, sizeof(w));
+            put<NT>(kept + at, w);
+            if (lane % BL == 0) exps[row * (size_t)(I / 16) + lane / BL] = (uint8_t)e;
         }
     }
 }
 
 // G lanes a row (a row's lanes are neighbours in a wave): dgamma is the sum of
 // a fixed order over a lane's columns, then over the lanes.
-template <typename TE, int G>
+template <typename TE, int G, bool NT>
 __global__ __launch_bounds__(256) void swiglu_backward_kernel(
     const TE* __restrict__ dact, const int8_t* __restrict__ kept, const uint8_t* __restrict__ exps,
     const float* __restrict__ gamma, const int32_t* __restrict__ row_count, int rows, int I, TE* __restrict__ dh,
     TE* __restrict__ act, float* __restrict__ dgamma) {
+    constexpr int C = cols<TE>(), P = C / 2, BL = block_lanes<TE>(), kRows = 256 / G;
     const int end = row_count != nullptr ? max(0, min(rows, *row_count)) : rows;
-    const int sub = threadIdx.x % G, per_row = I / 8;
-    constexpr int kRows = 256 / G;
+    const int sub = threadIdx.x % G, per_row = 2 * I / C;
     for (long long r = (long long)blockIdx.x * kRows + threadIdx.x / G; r < end; r += (long long)gridDim.x * kRows) {
         const size_t row = (size_t)r;
         const float gm = gamma != nullptr ? gamma[row] : 1.0f;
         float part = 0.0f;
-        for (int col = sub; col < per_row; col += G) {
-            const size_t at = row * 2 * I + (size_t)col * kCols;
-            const uint4 q = *reinterpret_cast<const uint4*>(kept + at);
-            const int e = exps[row * (size_t)(I / 16) + (col >> 1)];
+#pragma unroll 4
+        for (int lane = sub; lane < per_row; lane += G) {
+            const size_t at = row * 2 * I + (size_t)lane * C;
+            const Raw<int8_t, C> q = get<Raw<int8_t, C>, NT>(kept + at);
+            const int e = exps[row * (size_t)(I / 16) + lane / BL];
             const float scale = __uint_as_float(e == 255 ? 0x7FC00000u : (uint32_t)e << 23);
-            float da[kCols / 2];
-            load_cols<TE, kCols / 2>(dact + row * I + (size_t)col * (kCols / 2), da);
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-            float dv[kCols], av[kCols / 2];
+            float da[P];
+            widen<TE, P>(get<Raw<TE, P>, NT>(dact + at / 2), da);
+            uint32_t word[C / 4];
+            __builtin_memcpy(word, &q, sizeof(q));
+            float dv[C], av[P];
 #pragma unroll
-            for (int i = 0; i < kCols / 2; ++i) {
-                const uint32_t pair = w[i >> 1] >> (16 * (i & 1));
+            for (int i = 0; i < P; ++i) {
+                const uint32_t pair = word[i >> 1] >> (16 * (i & 1));
                 const float g = (float)(int8_t)(pair & 0xFFu) * scale;
                 const float u = (float)(int8_t)((pair >> 8) & 0xFFu) * scale;
                 const float s = sigmoid_of<TE>(g);
@@ -130,8 +136,8 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(
                 dv[2 * i] = dp * u * s * (1.0f + g * (1.0f - s));
                 dv[2 * i + 1] = dp * si;
             }
-            store_vec<TE, kCols>(dh + at, dv);
-            if (act != nullptr) store_vec<TE, kCols / 2>(act + row * I + (size_t)col * (kCols / 2), av);
+            put<NT>(dh + at, narrow<TE, C>(dv));
+            if (act != nullptr) put<NT>(act + at / 2, narrow<TE, P>(av));
         }
         if (dgamma != nullptr) {
             part = lanes_sum<G>(part);
@@ -140,14 +146,16 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(
     }
 }
 
-// Lanes a row: the width that leaves the fewest lanes without columns, the
-// larger of equals (fewer steps a row).
+// Lanes a row: the widest of which three quarters or more have columns (few
+// steps a row: 104 vectors take 64 lanes twice, 4.4 us for 1003 rows, against 9.1
+// with 8 lanes 13 times), else the one with the fewest idle.
 int lanes_per_row(int per_row) {
     int best = 8;
     double most = 0.0;
-    for (int g = 8; g <= 64; g *= 2) {
+    for (int g = 64; g >= 8; g /= 2) {
         const double used = (double)per_row / ((per_row + g - 1) / g * g);
-        if (used >= most) {
+        if (used >= 0.75) return g;
+        if (used > most) {
             most = used;
             best = g;
         }
@@ -155,34 +163,51 @@ int lanes_per_row(int per_row) {
     return best;
 }
 
+// Data that the 256 MB of the last cache cannot hold goes past it (65536 rows of
+// 2048 bf16: forward 201 against 215 us, backward 234 against 240; the stores
+// make the difference); smaller data is left for the next reader.
+bool past_caches(const SwigluParams& p, double bytes_per_value) {
+    return (double)p.rows * p.I * bytes_per_value > 256e6;
+}
+
 template <typename TE>
 hipError_t backward_typed(const SwigluParams& p, hipStream_t stream) {
-    const int G = lanes_per_row(p.I / 8);
+    const int G = lanes_per_row(2 * p.I / cols<TE>());
     const long long blocks = ((long long)p.rows * G + 255) / 256;
     const dim3 grid((unsigned)std::min<long long>(blocks, (long long)device_cu_count() * 32));
-    auto go = [&](auto g) {
-        constexpr int kG = decltype(g)::value;
-        hipLaunchKernelGGL((swiglu_backward_kernel<TE, kG>), grid, dim3(256), 0, stream,
-                           static_cast<const TE*>(p.dact), p.kept, p.exps, p.gamma, p.row_count, p.rows, p.I,
+    auto go = [&](auto g, auto nt) {
+        hipLaunchKernelGGL((swiglu_backward_kernel<TE, decltype(g)::value, decltype(nt)::value>), grid, dim3(256), 0,
+                           stream, static_cast<const TE*>(p.dact), p.kept, p.exps, p.gamma, p.row_count, p.rows, p.I,
                            static_cast<TE*>(p.dh), static_cast<TE*>(p.act), p.dgamma);
     };
-    if (G == 64) go(std::integral_constant<int, 64>{});
-    else if (G == 32) go(std::integral_constant<int, 32>{});
-    else if (G == 16) go(std::integral_constant<int, 16>{});
-    else go(std::integral_constant<int, 8>{});
+    auto width = [&](auto nt) {
+        if (G == 64) go(std::integral_constant<int, 64>{}, nt);
+        else if (G == 32) go(std::integral_constant<int, 32>{}, nt);
+        else if (G == 16) go(std::integral_constant<int, 16>{}, nt);
+        else go(std::integral_constant<int, 8>{}, nt);
+    };
+    if (past_caches(p, 2.0 + 4 * sizeof(TE))) width(std::true_type{});
+    else width(std::false_type{});
     return hipGetLastError();
 }
 
 template <typename TE>
 hipError_t forward_typed(const SwigluParams& p, hipStream_t stream) {
+    const unsigned per_row = 2u * (unsigned)p.I / cols<TE>();
+    const bool nt = past_caches(p, (p.kept != nullptr ? 2.0 : 0.0) + 3 * sizeof(TE));
     // bands of rows whose lanes a 32-bit index counts (with room for the stride)
-    const int band = std::max(1, (int)((1u << 30) / (unsigned)(p.I / 8)));
+    const int band = std::max(1, (int)((1u << 30) / per_row));
     for (int row0 = 0; row0 < p.rows; row0 += std::min(band, p.rows - row0)) {
         const int n = std::min(band, p.rows - row0);
-        const long long blocks = ((long long)n * (p.I / 8) + 255) / 256;
+        const long long blocks = ((long long)n * per_row + 255) / 256;
         const dim3 grid((unsigned)std::min<long long>(blocks, (long long)device_cu_count() * 32));
-        hipLaunchKernelGGL(swiglu_forward_kernel<TE>, grid, dim3(256), 0, stream, static_cast<const TE*>(p.h), p.gamma,
-                           p.row_count, row0, n, p.I, static_cast<TE*>(p.act), p.kept, p.exps);
+        auto go = [&](auto past) {
+            hipLaunchKernelGGL((swiglu_forward_kernel<TE, decltype(past)::value>), grid, dim3(256), 0, stream,
+                               static_cast<const TE*>(p.h), p.gamma, p.row_count, row0, n, p.I,
+                               static_cast<TE*>(p.act), p.kept, p.exps);
+        };
+        if (nt) go(std::true_type{});
+        else go(std::false_type{});
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -1,5 +1,5 @@
-// Vectors of 1, 4 or 8 consecutive values widened to fp32, and back (shared by
-// the elementwise and row kernels).
+// Vectors of consecutive values widened to fp32, and back (shared by the
+// elementwise and row kernels).
 #pragma once
 
 #include "common.h"
@@ -17,65 +17,67 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// a vector as loaded, V values of TE
+// V values of TE as loaded: 2, 8 or 16 bytes (fp32: 4, 8 or 16)
+template <int BYTES>
+struct RawBytes;
+template <>
+struct RawBytes<2> { typedef uint16_t type; };
+template <>
+struct RawBytes<4> { typedef uint32_t type; };
+template <>
+struct RawBytes<8> { typedef uint32_t type __attribute__((ext_vector_type(2))); };
+template <>
+struct RawBytes<16> { typedef uint32_t type __attribute__((ext_vector_type(4))); };
 template <typename TE, int V>
-struct RawOf;
-template <>
-struct RawOf<bf16_t, 1> { using type = bf16_t; };
-template <>
-struct RawOf<bf16_t, 8> { using type = uint4; };
-template <>
-struct RawOf<float, 1> { using type = float; };
-template <>
-struct RawOf<float, 4> { using type = float4; };
-template <typename TE, int V>
-using Raw = typename RawOf<TE, V>::type;
+using Raw = typename RawBytes<V * (int)sizeof(TE)>::type;
 
-template <typename TE, int V>
-__device__ __forceinline__ Raw<TE, V> load_raw(const TE* p) {
-    return *reinterpret_cast<const Raw<TE, V>*>(p);
+// NT: past the caches (data that is larger than they are, read or written once)
+template <typename R, bool NT>
+__device__ __forceinline__ R get(const void* p) {
+    if constexpr (NT) return __builtin_nontemporal_load(static_cast<const R*>(p));
+    else return *static_cast<const R*>(p);
+}
+template <bool NT, typename R>
+__device__ __forceinline__ void put(void* p, const R& v) {
+    if constexpr (NT) __builtin_nontemporal_store(v, static_cast<R*>(p));
+    else *static_cast<R*>(p) = v;
 }
 
-__device__ __forceinline__ void widen(bf16_t r, float* v) { v[0] = bf16_to_f32(r); }
-__device__ __forceinline__ void widen(float r, float* v) { v[0] = r; }
-__device__ __forceinline__ void widen(const float4& r, float* v) {
-    v[0] = r.x;
-    v[1] = r.y;
-    v[2] = r.z;
-    v[3] = r.w;
-}
-__device__ __forceinline__ void widen(const uint4& r, float* v) {
-    v[0] = bf16_lo(r.x);
-    v[1] = bf16_hi(r.x);
-    v[2] = bf16_lo(r.y);
-    v[3] = bf16_hi(r.y);
-    v[4] = bf16_lo(r.z);
-    v[5] = bf16_hi(r.z);
-    v[6] = bf16_lo(r.w);
-    v[7] = bf16_hi(r.w);
-}
-
-// V fp32 values rounded once and stored
+// values of a raw vector as fp32
 template <typename TE, int V>
-__device__ __forceinline__ void store_vec(TE* p, const float* v) {
-    if constexpr (sizeof(TE) == 4) {
-        if constexpr (V == 1) {
-            *p = v[0];
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; i += 4)
-                *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        }
+__device__ __forceinline__ void widen(const Raw<TE, V>& r, float* v) {
+    if constexpr (V == 1) {
+        if constexpr (sizeof(TE) == 2) v[0] = bf16_to_f32((bf16_t)r);
+        else v[0] = __uint_as_float(r);
     } else {
-        if constexpr (V == 1) {
-            *p = (bf16_t)(pack_bf16x2(v[0], 0.f) & 0xFFFFu);
-        } else {
+        constexpr int W = V * (int)sizeof(TE) / 4;
 #pragma unroll
-            for (int i = 0; i < V; i += 8)
-                *reinterpret_cast<uint4*>(p + i) =
-                    make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]),
-                               pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
+        for (int i = 0; i < W; ++i) {
+            if constexpr (sizeof(TE) == 2) {
+                v[2 * i] = bf16_lo(r[i]);
+                v[2 * i + 1] = bf16_hi(r[i]);
+            } else {
+                v[i] = __uint_as_float(r[i]);
+            }
         }
+    }
+}
+
+// V fp32 values, rounded once to TE
+template <typename TE, int V>
+__device__ __forceinline__ Raw<TE, V> narrow(const float* v) {
+    if constexpr (V == 1) {
+        if constexpr (sizeof(TE) == 2) return (uint16_t)(pack_bf16x2(v[0], 0.f) & 0xFFFFu);
+        else return __float_as_uint(v[0]);
+    } else {
+        Raw<TE, V> r;
+        constexpr int W = V * (int)sizeof(TE) / 4;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if constexpr (sizeof(TE) == 2) r[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            else r[i] = __float_as_uint(v[i]);
+        }
+        return r;
     }
 }
 

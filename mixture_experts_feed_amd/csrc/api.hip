@@ -701,6 +701,9 @@ int check_grouped_dims(const inkling_grouped_dims_t* d) {
     return INKLING_OK;
 }
 
+// a workgroup of 256 threads a tile, and a launch has fewer than 2^32 threads
+constexpr long long kSmallTilesMax = (1LL << 24) - 1;
+
 struct GroupedLayout {
     size_t offs, counters, num_tiles, tiles, total;
 };
@@ -775,7 +778,7 @@ int grouped_rows(const inkling_grouped_dims_t* d, bool input_grad, const void* s
     const GroupedLayout L = make_grouped_layout(d, grouped_row_tiles(d));
     if (!small && (workspace == nullptr || workspace_bytes < L.total)) return INKLING_ERR_WORKSPACE;
     GroupParams p = grouped_params(d, L, workspace, input_grad);
-    if ((small ? group_small_tiles(p.rows, p.E, p.n_cols) : group_max_tiles(p)) > INT32_MAX - 4096)
+    if (small ? group_small_tiles(p.rows, p.E, p.n_cols) > kSmallTilesMax : group_max_tiles(p) > INT32_MAX - 4096)
         return INKLING_ERR_UNSUPPORTED;
     p.src = src;
     p.weight = weight;
@@ -840,7 +843,7 @@ int inkling_grouped_weight_grad(const inkling_grouped_dims_t* dims, const void* 
     const bool small = grouped_small_wgrad(dims);   // takes no workspace
     const long long side = small ? 64 : 128;   // at least this wide a tile each way
     if (dims->n_groups * ((dims->out_features + side - 1) / side) * ((dims->in_features + side - 1) / side) >
-        INT32_MAX - 4096)
+        (small ? kSmallTilesMax : INT32_MAX - 4096))
         return INKLING_ERR_UNSUPPORTED;
     const GroupedLayout L = make_grouped_layout(dims, 0);
     if (!small && (workspace == nullptr || workspace_bytes < L.total)) return INKLING_ERR_WORKSPACE;

@@ -91,6 +91,19 @@ def test_grouped_tile_count_limit(lib):
                                       None) == B.INKLING_ERR_UNSUPPORTED
 
 
+def test_grouped_launch_size_limit(lib):
+    """fp32 products launch 256 threads for each 64 x 64 tile, and a launch has fewer than
+    2^32: 2^16 row tiles (and one for the ragged end) against 2^8 column tiles are too many."""
+    d = _grouped(rows=1 << 22, x_rows=1 << 22, n_groups=1, in_features=1 << 14, out_features=1 << 14,
+                 dtype=B.INKLING_F32, out_dtype=B.INKLING_F32)
+    un = B.INKLING_ERR_UNSUPPORTED
+    assert lib.inkling_grouped_linear(ctypes.byref(d), FAKE, None, FAKE2, FAKE, FAKE3, None, 0, None) == un
+    assert lib.inkling_grouped_input_grad(ctypes.byref(d), FAKE, FAKE2, FAKE, FAKE3, None, 0, None) == un
+    d = _grouped(n_groups=64, in_features=1 << 15, out_features=1 << 15, dtype=B.INKLING_F32,
+                 out_dtype=B.INKLING_F32)
+    assert lib.inkling_grouped_weight_grad(ctypes.byref(d), FAKE, FAKE2, None, FAKE, FAKE3, None, 0, None) == un
+
+
 def test_grouped_no_rows_is_a_noop(lib):
     d = _grouped(rows=0, x_rows=0)
     assert lib.inkling_grouped_linear(ctypes.byref(d), None, None, None, None, None, None, 0, None) == B.INKLING_OK

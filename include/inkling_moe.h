@@ -287,8 +287,8 @@ int inkling_dense_mlp_forward(const inkling_dense_dims_t* dims, const void* x, c
  * Limits (INKLING_ERR_UNSUPPORTED otherwise): in_features and out_features
  * multiples of 8 up to 2^20, 1 <= n_groups <= 512, rows and x_rows at most
  * 2^31 - 257, fewer than 2^31 output tiles (fp32: fewer than 2^24, of 64 x 64).
- * Tensor pointers must be 16-byte aligned, offsets and row_index 4-byte; the
- * output must not overlap an operand.  Same conventions and errors as
+ * Tensor pointers and workspace must be 16-byte aligned, offsets and row_index
+ * 4-byte; the output must not overlap an operand.  Same conventions and errors as
  * inkling_moe_forward otherwise; rows == 0 is a no-op for the first two and
  * writes zeros in weight_grad.
  */

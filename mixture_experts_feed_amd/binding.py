@@ -565,6 +565,15 @@ def _grouped_plan_checks(offsets, n_groups, row_index, dev):
             raise ValueError("row_index must be one-dimensional")
 
 
+def _result_dtype(name, t, wanted, otherwise):
+    """The dtype of the given result t, else the wanted one, else `otherwise`."""
+    if t is None:
+        return otherwise if wanted is None else wanted
+    if wanted is not None and wanted != t.dtype:
+        raise ValueError(f"the dtype wanted for {name} is {wanted}, and the given {name} has {t.dtype}")
+    return t.dtype
+
+
 def _result(t, name, shape, dtype, dev, like=None):
     """The given result tensor, checked, or a new one (`like`: a contiguous
     operand of that shape and dtype, from which making one is cheaper)."""
@@ -593,7 +602,7 @@ def grouped_linear(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
     made here: unset)."""
     R, E, N, K = _grouped_checks("x", x, weight, offsets, weight.shape[-1], row_index)
     dev = x.device
-    out_dtype = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
+    out_dtype = _result_dtype("out", out, out_dtype, x.dtype)
     dims, need = _grouped_plan(R, x.shape[0], E, K, N, x.dtype, out_dtype)
     out = _result(out, "out", (R, N), out_dtype, dev)
     ws = _scratch(workspace, need, dev)
@@ -609,7 +618,7 @@ def grouped_input_grad(dout: torch.Tensor, weight: torch.Tensor, offsets: torch.
     row_index in the forward, the rows of one x row are for the caller to sum."""
     R, E, N, K = _grouped_checks("dout", dout, weight, offsets, weight.shape[1], None)
     dev = dout.device
-    dx_dtype = dx.dtype if dx is not None else dout.dtype if dx_dtype is None else dx_dtype
+    dx_dtype = _result_dtype("dx", dx, dx_dtype, dout.dtype)
     dims, need = _grouped_plan(R, R, E, K, N, dout.dtype, dx_dtype)
     dx = _result(dx, "dx", (R, K), dx_dtype, dev)
     ws = _scratch(workspace, need, dev)
@@ -636,9 +645,7 @@ def grouped_weight_grad(dout: torch.Tensor, x: torch.Tensor, offsets: torch.Tens
     K = x.shape[1]
     if (x if row_index is None else row_index).shape[0] != R:
         raise ValueError("dout must have a row for each row of x, or for each entry of row_index")
-    wdt = dweight.dtype if dweight is not None else torch.float32 if weight_grad_dtype is None else weight_grad_dtype
-    if weight_grad_dtype is not None and weight_grad_dtype != wdt:
-        raise ValueError("weight_grad_dtype differs from the dtype of the given dweight")
+    wdt = _result_dtype("dweight", dweight, weight_grad_dtype, torch.float32)
     dims, need = _grouped_weight_grad_plan(R, x.shape[0], E, K, N, x.dtype, wdt)
     dweight = _result(dweight, "dweight", (E, N, K), wdt, dev)
     ws = _scratch(workspace, need, dev)
@@ -780,7 +787,7 @@ def norm_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Ten
     _norm_checks(x, weight, bias)
     R, H = x.shape
     dev = x.device
-    dims, _ = _norm_plan(R, H, kind, x.dtype, eps)
+    dims, _ = _norm_plan(R, H, kind, x.dtype, float(eps))
     out = _result(out, "out", (R, H), x.dtype, dev, like=x)
     if not save and stats is not None:
         raise ValueError("save=False keeps no stats: give none")

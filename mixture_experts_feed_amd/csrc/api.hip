@@ -772,7 +772,7 @@ int grouped_rows(const inkling_grouped_dims_t* d, bool input_grad, const void* s
     if (!input_grad && (row_index == nullptr ? d->x_rows != d->rows : d->x_rows == 0))
         return INKLING_ERR_INVALID_ARGUMENT;
     if (!aligned(src, 16) || !aligned(weight, 16) || !aligned(out, 16) || !aligned(offsets, 4) ||
-        !aligned(row_index, 4))
+        !aligned(row_index, 4) || !aligned(workspace, 16))
         return INKLING_ERR_INVALID_ARGUMENT;
     const bool small = grouped_small(d, input_grad);   // takes no workspace
     const GroupedLayout L = make_grouped_layout(d, grouped_row_tiles(d));
@@ -838,7 +838,7 @@ int inkling_grouped_weight_grad(const inkling_grouped_dims_t* dims, const void* 
     if (row_index == nullptr ? dims->x_rows != dims->rows : dims->rows > 0 && dims->x_rows == 0)
         return INKLING_ERR_INVALID_ARGUMENT;
     if (!aligned(x, 16) || !aligned(dout, 16) || !aligned(dweight, 16) || !aligned(offsets, 4) ||
-        !aligned(row_index, 4))
+        !aligned(row_index, 4) || !aligned(workspace, 16))
         return INKLING_ERR_INVALID_ARGUMENT;
     const bool small = grouped_small_wgrad(dims);   // takes no workspace
     const long long side = small ? 64 : 128;   // at least this wide a tile each way
@@ -1008,7 +1008,7 @@ int inkling_norm_backward(const inkling_norm_dims_t* dims, const void* dout, con
         return INKLING_ERR_INVALID_ARGUMENT;
     if (dims->kind == INKLING_NORM_RMS && dbias != nullptr) return INKLING_ERR_INVALID_ARGUMENT;
     if (!aligned(dout, 16) || !aligned(x, 16) || !aligned(weight, 16) || !aligned(stats, 16) || !aligned(dx, 16) ||
-        !aligned(dweight, 16) || !aligned(dbias, 16))
+        !aligned(dweight, 16) || !aligned(dbias, 16) || !aligned(workspace, 16))
         return INKLING_ERR_INVALID_ARGUMENT;
     if (workspace == nullptr || workspace_bytes < norm_part_bytes(dims)) return INKLING_ERR_WORKSPACE;
     NormParams p = norm_params(dims);

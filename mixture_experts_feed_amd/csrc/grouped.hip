@@ -2,7 +2,8 @@
 //   out[r] = W_e x[row_index[r]]   dx[r] = W_e^T dout[r]   dW_e = sum_r dout[r] (x) x[row_index[r]]
 // for the rows offsets[e] <= r < offsets[e + 1] of expert e.  Two kernels:
 //   small_product_kernel (grouped_small.h)  64 x 64 tiles, one launch without a
-//     plan: fp32, and bf16 products with too few large tiles for the card;
+//     plan: fp32, and bf16 products with too few large tiles for the card or few
+//     rows an expert against small weights (group_small, group_small_wgrad);
 //   moe_gemm_kernel (gemm_kernel.h)  the layer's tiles, in its grouped modes:
 //     everything else, after a plan (the caller's offsets made safe, row tiles).
 #include <algorithm>
@@ -88,7 +89,15 @@ int grid_of(long long tiles, int per_cu) {
     return (grid + 7) / 8 * 8;
 }
 
-// sched: see prefill_sched in gemm.hip
+// Forward and input gradient on 256 x 256 tiles, one workgroup a CU: bound by the
+// matrix units once an expert has some hundred rows (each stage of 64 K moves 64 KB
+// through LDS for 8.4 MFLOP).  Forward, 128 experts of 512 rows on average, 6144 x
+// 4096: 3290 us, 1.00 PFLOP/s; input gradient, 64 of 384, 2048 x 1536: 205 us, 0.75
+// PFLOP/s (768 tiles, half of each expert's last row tile empty).  128 x 256 and 256 x
+// 128 tiles, two workgroups a CU, were 5 to 30% slower at 1.2 to 24 rounds, and one
+// wave a SIMD with 128 x 128 tiles of its own 0 to 10% faster on even experts only.
+// kSchedGroup (gemm_kernel.h) starts the tiles that share rows or weights on one
+// XCD together: 1 to 25% faster than the other walks.
 template <int SCHED, int MODE>
 void launch_256(const GemmKArgs& a, long long max_tiles, hipStream_t stream) {
     hipLaunchKernelGGL((moe_gemm_kernel<bf16_t, 256, 256, 4, 2, 2, 2, 128, 8, SCHED, MODE>),
@@ -100,7 +109,7 @@ void launch_256(const GemmKArgs& a, long long max_tiles, hipStream_t stream) {
 // Up to 48 rows an expert on average, the forward streams the weights past tiles
 // of 16 rows (the layer's decode tiles): 805 us at 2 rows an expert, 6144 x 4096,
 // 6.9 TB/s.  Input gradients always take 256 x 256 tiles (whose few-row form
-// skips the row blocks without rows): 408 us at 64 rows, 4096 x 2048, 5.4 TB/s.
+// skips the row blocks without rows): 407 us at 64 rows, 4096 x 2048, 5.4 TB/s.
 int group_cfg(int rows, int E, bool input_grad) {
     return !input_grad && (double)rows / E <= 48.0 ? 1 : 0;
 }
@@ -121,14 +130,15 @@ hipError_t launch_group_plan(const GroupParams& p, const int32_t* offsets, bool 
 }
 
 // The row products (forward, input gradient) on 64 x 64 tiles:
-// - below one 256 x 256 tile a CU.  Forward, us, 64 x 64 against 256 x 256: 13 / 19
-//   at 12 experts of 30 rows (512 x 512), 28 / 40 at 16 of 256 rows (1024 x 1024, 128
-//   large tiles), 46 / 45 at 16 of 512 (192), 46 / 45 at 8 of 512 (2048 x 1024, 192);
+// - below one 256 x 256 tile a CU.  Forward, us, 64 x 64 against the large tiles: 7 /
+//   11 at 12 experts of 30 rows (512 x 512), 25 / 36 at 16 of 256 rows (1024 x 1024, 128
+//   large tiles), 43 / 40 at 16 of 512 (192); forward and input gradient 41, 40 / 39, 56
+//   at 8 of 512 (2048 x 1024, 192);
 // - with at most 64 rows an expert while the weights are at most 2^27 values (beyond,
-//   streaming them past 16-row tiles wins).  Forward and input gradient: 32, 32 against
-//   50, 38 at 64 experts of 40 rows (1024 x 1024), 17, 17 against 16, 28 at 128 of 2
-//   (512 x 512), 48, 48 against 46, 58 at 128 of 2 (1024 x 1024); 207, 210 against 155,
-//   206 at 128 of 2 (2048 x 2048, 2^29 values);
+//   streaming them past 16-row tiles wins).  Forward and input gradient: 32, 32 / 50, 38
+//   at 64 experts of 40 rows (1024 x 1024), 16, 17 / 17, 28 at 128 of 2 (512 x 512), 48,
+//   47 / 46, 57 at 128 of 2 (1024 x 1024), 65, 71 / 64, 66 at 128 of 64 (1024 x 1024);
+//   209, 209 / 156, 206 at 128 of 2 (2048 x 2048, 2^29 values);
 // - fp32 at every size: 11 / 34 us at 8 experts of 83 rows (136 x 200), 50 / 84 at 32
 //   of 64 (1024 x 1024), and up to 24% slower on large products (737 / 594 at 16 of
 //   512, 2048 x 2048), which bf16 is for.
@@ -139,10 +149,10 @@ bool group_small(int dtype, int rows, int E, int n_cols, int k_len) {
 }
 
 // The weight gradients on 64 x 64 tiles: up to 256 rows an expert and 24 M
-// values.  us, against 128 x 256 tiles: 22 / 30 at 64 experts of 100 rows (512 x
-// 512), 31 / 33 at 16 of 256 (1024 x 1024), 22 / 30 at 40 of 3 (1024 x 512); 49 / 40 at
-// 16 of 512 (1024 x 1024), 42 / 38 at 32 of 128 (1024 x 1024, 34 M values), 54 / 41 at
-// 12 of 30 (2048 x 2048, 50 M).  fp32 at every size, as above.
+// values.  bf16, us, against 128 x 256 tiles: 22 / 28 at 64 experts of 100 rows (512 x
+// 512), 18 / 26 at 16 of 64 and 32 / 31 at 16 of 256 (1024 x 1024), 22 / 28 at 40 of 3
+// (1024 x 512); 46 / 36 at 16 of 512 (1024 x 1024), 38 / 35 at 32 of 128 (1024 x 1024,
+// 34 M values), 52 / 39 at 12 of 30 (2048 x 2048, 50 M).  fp32 at every size, as above.
 bool group_small_wgrad(int dtype, int rows, int E, int n_in, int n_out) {
     if (dtype == 0) return true;
     return rows <= 256LL * E && (double)E * n_in * n_out <= 24e6;
@@ -225,6 +235,12 @@ hipError_t launch_group_rows(const GroupParams& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Weight gradients on 128 x 256 tiles, two workgroups a CU: tiles with a K of a
+// few hundred rows are mostly stores (dW is written once, 1536 x 2048 x 4 bytes an
+// expert against 384 rows read), and one workgroup stores while the other multiplies.
+// 64 experts of 384 rows (2048 x 1536): 264 us in fp32, 287 with gathered rows of x
+// (1.0 GB, 3.8 TB/s; a gathered copy first took 20 us more); 16 of 512 (2048 x 6144),
+// bf16: 238 us, 0.87 PFLOP/s.
 hipError_t launch_group_wgrad(const GroupParams& p, const void* x, const void* dout, int n_in, int n_out, void* dw,
                               int dw_bf16, hipStream_t stream) {
     GemmKArgs a = {};

@@ -1,5 +1,6 @@
-// Grouped matrix products on 64 x 64 tiles, one tile a workgroup: fp32 products,
-// and bf16 ones with too few large tiles to fill the card (gfx950).
+// Grouped matrix products on 64 x 64 tiles, one tile a workgroup: fp32 products, and
+// bf16 ones with too few large tiles to fill the card, or few rows an expert against
+// small weights (gfx950; the rules and both sides' times are in grouped.hip).
 //
 //   out[m][n] = sum_k B[m][k] A[n][k] over the rows m of one expert, as
 //   kProdRows   A = weight [n][k], B = rows (gathered through row_index), K = in_features

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(256) void swiglu_forward_kernel(const TE* __restric
                                                              int I, TE* __restrict__ act, int8_t* __restrict__ kept,
                                                              uint8_t* __restrict__ exps) {
     constexpr int C = cols<TE>(), P = C / 2, BL = block_lanes<TE>();
-    const int end = row_count != nullptr ? max(0, min(rows, *row_count - row0)) : rows;
+    const int end = row_count != nullptr ? min(rows, max(*row_count, row0) - row0) : rows;
     const uint32_t per_row = 2u * (uint32_t)I / C;            // lanes a row takes
     const uint32_t total = (uint32_t)end * per_row;           // < 2^31 (launcher)
     for (uint32_t c = blockIdx.x * 256 + threadIdx.x; c < total; c += gridDim.x * 256) {

@@ -428,6 +428,73 @@ def test_row_offsets_past_32_bits():
     assert int(out[:-2].count_nonzero()) == 0
 
 
+def _spots_close(name, got, want, absum, n):
+    _close(name, got, want, absum, n, BF16)
+
+
+def test_row_offsets_past_32_bits():
+    """x, out, dout and dx of more than 2^31 values: rows at both ends and around value 2^31, zeros elsewhere."""
+    K, N = 4096, 4104
+    R = (1 << 31) // K + 500
+    edge = (1 << 31) // N - 8                         # before K's own edge at (1 << 31) / K
+    spots = [0, edge, (1 << 31) // K - 8, R - 16]
+    off = torch.tensor([0, 16, edge + 16, R], dtype=torch.int32, device=DEV)
+    live = _rand((64, K), BF16, 31), _rand((64, N), BF16, 32)
+    w = _rand((3, N, K), BF16, 33, 0.1)
+    x, d = torch.zeros((R, K), dtype=BF16, device=DEV), torch.zeros((R, N), dtype=BF16, device=DEV)
+    for n, at in enumerate(spots):
+        x[at:at + 16], d[at:at + 16] = live[0][16 * n:16 * n + 16], live[1][16 * n:16 * n + 16]
+    _say(f"[grouped] {R} rows of {K} and {N}")
+    out = B.grouped_linear(x, w, off)
+    dx = B.grouped_input_grad(d, w, off)
+    dw = B.grouped_weight_grad(d, x, off)
+    torch.cuda.synchronize()
+    wf, lx, ld = _f64(w), _f64(live[0]), _f64(live[1])
+    want = np.zeros((3, N, K))
+    ab = np.zeros((3, N, K))
+    for n, at in enumerate(spots):
+        r = slice(16 * n, 16 * n + 16)
+        e = 0 if at < 16 else 1 if at < edge + 16 else 2
+        _spots_close(f"out at {at}", out[at:at + 16], lx[r] @ wf[e].T, np.abs(lx[r]) @ np.abs(wf[e]).T, K)
+        _spots_close(f"dx at {at}", dx[at:at + 16], ld[r] @ wf[e], np.abs(ld[r]) @ np.abs(wf[e]), N)
+        want[e] += ld[r].T @ lx[r]
+        ab[e] += np.abs(ld[r]).T @ np.abs(lx[r])
+    _close("dw", dw, want, ab, 32, F32)               # zeros add nothing, and no rounding
+    for t in (out, dx):
+        keep = torch.ones(R, dtype=torch.bool, device=DEV)
+        for at in spots:
+            keep[at:at + 16] = False
+        assert not bool(t.any(dim=1)[keep].any())
+
+
+def test_weight_offsets_past_32_bits():
+    """Weights and weight gradients of more than 2^32 values, in few-row tiles and in tiles of 256 rows."""
+    E, N, K = 512, 1032, 8192
+    w = torch.zeros((E, N, K), dtype=BF16, device=DEV)
+    used = [0, 255, 511]                              # value 2^31 lies in expert 254, 2^32 in 508
+    for n, e in enumerate(used):
+        w[e] = _rand((N, K), BF16, 40 + n, 0.1)
+    for rows in (2, 70):
+        c = np.zeros(E, np.int64)
+        c[used] = rows
+        c[300] = 60 * E if rows == 70 else 0          # on zero weights: more than 48 rows an expert on average
+        ends = np.concatenate([[0], np.cumsum(c)])
+        R = int(ends[-1])
+        off = torch.tensor(ends, dtype=torch.int32, device=DEV)
+        x, d = _rand((R, K), BF16, 50), _rand((R, N), BF16, 51)
+        _say(f"[grouped] {E} x {N} x {K} weights, {R} rows")
+        out, dx = B.grouped_linear(x, w, off), B.grouped_input_grad(d, w, off)
+        dw = B.grouped_weight_grad(d, x, off, weight_grad_dtype=BF16)
+        torch.cuda.synchronize()
+        for e in used:
+            r = slice(int(ends[e]), int(ends[e + 1]))
+            xe, de, we = _f64(x[r]), _f64(d[r]), _f64(w[e])
+            _spots_close(f"out of {e}", out[r], xe @ we.T, np.abs(xe) @ np.abs(we).T, K)
+            _spots_close(f"dx of {e}", dx[r], de @ we, np.abs(de) @ np.abs(we), N)
+            _spots_close(f"dw of {e}", dw[e], de.T @ xe, np.abs(de).T @ np.abs(xe), rows)
+        assert not bool(dw[509].any()) and not bool(dw[1].any())
+        del out, dx, dw
+
 def test_refusals():
     x, w = _rand((10, 64), BF16, 1), _rand((3, 40, 64), BF16, 2)
     off = torch.tensor([0, 3, 3, 10], dtype=torch.int32, device=DEV)

@@ -297,6 +297,41 @@ def test_byte_offsets_past_32_bits():
     assert int(r["dh"][:-64].count_nonzero()) == 0
 
 
+def test_more_rows_than_one_launch_counts():
+    """2^30 lanes and beyond: the forward goes over the rows in bands.  Rows at both ends, where element offsets
+    pass 2^31 and 2^32 and on both sides of the band's end are those of a short call, and the others zeros."""
+    I, dtype = 64, BF16
+    band = (1 << 30) // (2 * I // 8)
+    R = band + 40
+    h, gamma, dact = _make(64, I, dtype, 21)
+    spots = [0, (1 << 31) // (2 * I) - 4, (1 << 32) // (2 * I) - 4, band - 4, R - 8]
+    want, ck = B.swiglu_forward(h, gamma)
+    grads = B.swiglu_backward(dact, ck, gamma)
+    q, e = _split(ck, 64, I)
+    H = torch.zeros((R, 2 * I), dtype=dtype, device=DEV)
+    G = torch.zeros(R, device=DEV)
+    D = torch.zeros((R, I), dtype=dtype, device=DEV)
+    for n, at in enumerate(spots):
+        H[at:at + 8], G[at:at + 8], D[at:at + 8] = h[8 * n:8 * n + 8], gamma[8 * n:8 * n + 8], dact[8 * n:8 * n + 8]
+    act, CK = B.swiglu_forward(H, G)
+    for n, at in enumerate(spots):
+        assert torch.equal(act[at:at + 8], want[8 * n:8 * n + 8]), at
+        kept = CK[at * 2 * I:(at + 8) * 2 * I].cpu().numpy().view(np.int8).reshape(8, 2 * I)
+        exps = CK[R * 2 * I + at * (I // 16):R * 2 * I + (at + 8) * (I // 16)].cpu().numpy().reshape(8, I // 16)
+        assert np.array_equal(kept, q[8 * n:8 * n + 8]) and np.array_equal(exps, e[8 * n:8 * n + 8]), at
+    assert int(act.count_nonzero()) == int(want[:40].count_nonzero())
+    got = B.swiglu_backward(D, CK, G, act=act)
+    for n, at in enumerate(spots):
+        for k in ("dh", "act", "dgamma"):
+            assert torch.equal(got[k][at:at + 8], grads[k][8 * n:8 * n + 8]), (k, at)
+    assert int(got["dh"].count_nonzero()) == int(grads["dh"][:40].count_nonzero())
+    # a count below zero, as small as it can be, is no rows in any band
+    act.fill_(-776.0)
+    B.swiglu_forward(H, G, row_count=torch.tensor([-2 ** 31], dtype=torch.int32, device=DEV), out=act, save=False)
+    torch.cuda.synchronize()
+    assert bool((act[:64] == -776.0).all()) and bool((act[band - 64:] == -776.0).all())
+
+
 def test_refusals():
     h, gamma, da = _make(10, 32, BF16, 17)
     _, ck = B.swiglu_forward(h, gamma)

@@ -4,6 +4,7 @@ import ctypes
 import os
 
 import pytest
+import torch
 
 from mixture_experts_feed_amd import binding as B
 
@@ -58,7 +59,7 @@ def test_grouped_pointers(lib):
     fwd = lambda x=FAKE, i=None, w=FAKE2, o=FAKE, out=FAKE3, ws=FAKE, n=BIG, dd=d: lib.inkling_grouped_linear(  # noqa: E731
         ctypes.byref(dd), x, i, w, o, out, ws, n, None)
     for kw in (dict(x=None), dict(w=None), dict(o=None), dict(out=None), dict(out=FAKE), dict(out=FAKE2),
-               dict(x=ODD), dict(w=ODD), dict(out=ODD), dict(o=FAKE + 2), dict(i=FAKE + 1)):
+               dict(x=ODD), dict(w=ODD), dict(out=ODD), dict(o=FAKE + 2), dict(i=FAKE + 1), dict(ws=ODD)):
         assert fwd(**kw) == bad, kw
     large = _grouped(rows=9000, x_rows=9000, n_groups=64, in_features=2048, out_features=2048)
     assert fwd(dd=large, ws=None) == B.INKLING_ERR_WORKSPACE
@@ -192,8 +193,35 @@ def test_norm_pointers(lib):
         lib.inkling_norm_backward(ctypes.byref(dd), dy, x, w, st, dx, dw, db, ws, size, None))
     for kw in (dict(dy=None), dict(x=None), dict(w=None), dict(st=None), dict(dx=None), dict(dw=None), dict(dx=FAKE),
                dict(dx=FAKE2), dict(db=0x50000), dict(dw=FAKE3), dict(dy=ODD), dict(x=ODD), dict(dx=ODD),
-               dict(dw=0x50008), dict(db=0x60008), dict(dd=r, db=0x60000)):
+               dict(dw=0x50008), dict(db=0x60008), dict(dd=r, db=0x60000), dict(ws=ODD)):
         assert bwd(**kw) == bad, kw
     assert bwd(ws=None) == B.INKLING_ERR_WORKSPACE
     assert bwd(size=n.value - 1) == B.INKLING_ERR_WORKSPACE
     assert lib.inkling_norm_forward(ctypes.byref(_norm(rows=0)), None, None, None, None, None, None) == B.INKLING_OK
+
+
+def test_a_plan_holds_values_not_tensors(lib):
+    """eps may come as a 0-d tensor; changing it in place must reach the next call."""
+    seen = []
+    real = B._call
+    x, w, out = torch.zeros((2, 8)), torch.ones(8), torch.zeros((2, 8))
+    eps = torch.tensor(1e-3)
+    B._call = lambda dev, name, dims, *a: seen.append(ctypes.cast(dims, ctypes.POINTER(B.NormDims)).contents.eps)
+    checks, operand, B._norm_checks, B._operand = B._norm_checks, B._operand, lambda *a: None, lambda *a: None
+    try:
+        B.norm_forward(x, w, eps=eps, out=out, save=False)
+        eps.fill_(0.5)
+        B.norm_forward(x, w, eps=eps, out=out, save=False)
+    finally:
+        B._call, B._norm_checks, B._operand = real, checks, operand
+    assert seen[0] == eps.new_tensor(1e-3).item() and seen[1] == 0.5
+
+
+def test_a_wanted_dtype_must_be_that_of_the_given_result():
+    assert B._result_dtype("out", None, None, torch.bfloat16) is torch.bfloat16
+    assert B._result_dtype("out", None, torch.float32, torch.bfloat16) is torch.float32
+    t = torch.zeros(1)
+    assert B._result_dtype("out", t, None, torch.bfloat16) is torch.float32
+    assert B._result_dtype("out", t, torch.float32, torch.bfloat16) is torch.float32
+    with pytest.raises(ValueError):
+        B._result_dtype("out", t, torch.bfloat16, torch.float32)

@@ -238,9 +238,8 @@ hipError_t launch_group_rows(const GroupParams& p, hipStream_t stream) {
 // Weight gradients on 128 x 256 tiles, two workgroups a CU: tiles with a K of a
 // few hundred rows are mostly stores (dW is written once, 1536 x 2048 x 4 bytes an
 // expert against 384 rows read), and one workgroup stores while the other multiplies.
-// 64 experts of 384 rows (2048 x 1536): 264 us in fp32, 287 with gathered rows of x
-// (1.0 GB, 3.8 TB/s; a gathered copy first took 20 us more); 16 of 512 (2048 x 6144),
-// bf16: 238 us, 0.87 PFLOP/s.
+// 64 experts of 384 rows (2048 x 1536): 261 us in fp32 (1.0 GB, 3.8 TB/s), with
+// gathered rows of x or without; 16 of 512 (2048 x 6144), bf16: 240 us, 0.86 PFLOP/s.
 hipError_t launch_group_wgrad(const GroupParams& p, const void* x, const void* dout, int n_in, int n_out, void* dw,
                               int dw_bf16, hipStream_t stream) {
     GemmKArgs a = {};

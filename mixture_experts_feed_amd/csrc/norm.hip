@@ -38,11 +38,11 @@ constexpr int kMaxWaves = 16;
 // one vector a lane up to 1024 lanes; several a lane need the registers of 512
 template <int NV, int G>
 constexpr int max_threads() { return G != 0 ? 256 : NV == 1 ? 1024 : 512; }
-// waves a SIMD that the registers allow: 6 with one vector a lane (80 registers),
-// so that two workgroups of 12 waves share a CU (the backward, 8192 x 6144 bf16:
-// 75 us with 76 registers, 90 with 86)
-template <int NV>
-constexpr int min_waves() { return NV == 1 ? 6 : 2; }
+// Waves a SIMD that the registers have to leave room for (second launch bound): 6
+// with one vector a lane (80 registers), so that two workgroups of 12 waves share a
+// CU (the backward, 8192 x 6144 bf16: 75 us with 76 registers, 90 with 86); 4 for
+// the backward of narrow rows, which 80 registers make spill (98304 x 512 bf16: 77
+// us against 84); 2 with several vectors a lane.
 
 // Sums over the lanes that hold a row: G lanes of a wave (G < 64 or one wave),
 // or G == 0: the workgroup.  `buf` alternates from call to call, so that one
@@ -119,14 +119,16 @@ struct Row {
         }
     }
     // fp32 columns of w, b or of a partial row
+    static __device__ __forceinline__ void column(float* c, const float* p, int j, int t, int lanes, int H) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int col = (j * lanes + t) * V + i;
+            c[i] = p != nullptr && (TAIL ? col < H : (j * lanes + t) * V < H) ? p[col] : 0.0f;
+        }
+    }
     static __device__ __forceinline__ void columns(float (*c)[V], const float* p, int t, int lanes, int H) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int col = (j * lanes + t) * V + i;
-                c[j][i] = p != nullptr && (TAIL ? col < H : (j * lanes + t) * V < H) ? p[col] : 0.0f;
-            }
+        for (int j = 0; j < NV; ++j) column(c[j], p, j, t, lanes, H);
     }
 };
 
@@ -150,7 +152,7 @@ struct Place {
 };
 
 template <typename TE, int NV, int G, bool TAIL, bool RMS, bool NT>
-__global__ __launch_bounds__((max_threads<NV, G>()), (min_waves<NV>())) void norm_forward_kernel(
+__global__ __launch_bounds__((max_threads<NV, G>()), (NV == 1 ? 6 : 2)) void norm_forward_kernel(
     const TE* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, int rows, int H, float eps,
     TE* __restrict__ out, float* __restrict__ stats) {
     using R = Row<TE, NV, TAIL, NT>;
@@ -212,7 +214,7 @@ __global__ __launch_bounds__((max_threads<NV, G>()), (min_waves<NV>())) void nor
 
 // part [partial rows][parts][H]: dw, and db where parts is 2
 template <typename TE, int NV, int G, bool TAIL, bool RMS, bool NT>
-__global__ __launch_bounds__((max_threads<NV, G>()), (min_waves<NV>())) void norm_backward_kernel(
+__global__ __launch_bounds__((max_threads<NV, G>()), (NV != 1 ? 2 : G != 0 ? 4 : 6)) void norm_backward_kernel(
     const TE* __restrict__ dout, const TE* __restrict__ x, const float* __restrict__ stats,
     const float* __restrict__ w, int rows, int H, int parts, TE* __restrict__ dx, float* __restrict__ part) {
     using R = Row<TE, NV, TAIL, NT>;
@@ -230,7 +232,8 @@ __global__ __launch_bounds__((max_threads<NV, G>()), (min_waves<NV>())) void nor
         R::load(cd, dout + (size_t)row * H, t, lanes, full, last);
     }
     float wr[NV][V], dw[NV][V], db[NV][V];
-    R::columns(wr, w, t, lanes, H);
+    constexpr bool kHoldW = NV < 8 || RMS;
+    if constexpr (kHoldW) R::columns(wr, w, t, lanes, H);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -251,6 +254,14 @@ __global__ __launch_bounds__((max_threads<NV, G>()), (min_waves<NV>())) void nor
             float d[V];
             widen<TE, V>(cx[j], xh[j]);
             widen<TE, V>(cd[j], d);
+            if constexpr (!kHoldW) {
+                // read for each row (from the L2): held over the rows, more registers
+                // spill (2048 x 12288 fp32: 97 us against 130; the RMS norm, which
+                // holds them, 63 against 71)
+                const float* wp = w;
+                __asm__ volatile("" : "+s"(wp), "+v"(s[0]));
+                R::column(wr[j], wp, j, t, lanes, H);
+            }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 xh[j][i] = (xh[j][i] - m) * r;
@@ -394,10 +405,13 @@ hipError_t forward_typed(const NormParams& p, hipStream_t stream) {
 // Workgroups of the backward pass.  Each ends with one partial row (narrow rows:
 // four) that is written and read back, so each takes 4 rows a lane or more, and
 // 16 or more where 512 workgroups are enough; at most what the card holds.
+// Several vectors a lane: one workgroup a CU is what the registers allow (256
+// against 512 workgroups, 4096 x 12288 bf16: 76 us against 92; 8192 x 16384: 174
+// against 198; 16384 x 8192 fp32: 296 against 312).
 int backward_grid(const Shape& s, int rows) {
     const int per = s.g == 0 ? 1 : 256 / s.g;
     const int steps = (rows + per - 1) / per;
-    const int most = std::min(std::max(512, steps / 16), 256 * std::max(1, 2048 / s.threads));
+    const int most = s.nv > 1 ? 256 : std::min(std::max(512, steps / 16), 256 * std::max(1, 2048 / s.threads));
     return std::max(1, std::min((steps + 3) / 4, most));
 }
 

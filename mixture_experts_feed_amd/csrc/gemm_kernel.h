@@ -38,6 +38,7 @@
 
 #include "common.h"
 #include "kernels.h"
+#include "tile_ranges.h"
 
 namespace inkling {
 
@@ -84,7 +85,6 @@ constexpr bool b_kn() { return wgrad_mode<MODE>(); }
 enum { kSchedStride = 0, kSchedRound = 1, kSchedQueue = 2, kSchedGroup = 3 };
 constexpr int kGroupMax = 8;
 constexpr int kSpinLimit = 400;   // polls of a tile-round wait (about 100-400 us at most)
-constexpr int kWgradEpi = 128;    // K-equivalent cost of a weight-gradient tile's fp32 epilogue
 // Cache policy of the weight (A) loads.  Tiles of at most 16 token rows (the
 // decode configuration) read each weight byte once per call: those loads carry
 // the non-temporal bit, which streams the weights at about 6.7 TB/s instead of
@@ -600,26 +600,9 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
     auto range_start = [&](int x) -> int {
         if (x >= 8) return nb_real;
         if constexpr (WG) {
-            // a tile of problem p costs its K plus kWgradEpi (the fp32 tile
-            // write); routed costs accumulate in poff
-            const int per_p = a.wg_mtiles * a.wg_ntiles, E = a.wg_E;
-            const long long routed = (long long)per_p * (a.poff[E] + (long long)E * kWgradEpi);
-            const long long total = routed + (long long)per_p * a.S * (a.K_s + kWgradEpi);
-            const long long c = total * x / 8;
-            if (c <= 0) return 0;
-            if (c >= routed) {
-                const long long per_tile = a.K_s + kWgradEpi;
-                return min(nb_real, E * per_p + (int)((c - routed + per_tile - 1) / per_tile));
-            }
-            int lo = 0, hi = E - 1;   // last problem p with cost(problems < p) <= c
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if ((long long)per_p * (a.poff[mid] + (long long)mid * kWgradEpi) <= c) lo = mid;
-                else hi = mid - 1;
-            }
-            const long long before = (long long)per_p * (a.poff[lo] + (long long)lo * kWgradEpi);
-            const long long per_tile = (long long)(a.poff[lo + 1] - a.poff[lo]) + kWgradEpi;
-            return min(nb_real, lo * per_p + (int)min<long long>(per_p, (c - before + per_tile - 1) / per_tile));
+            // by cost: the layer's padded row counts, or the caller's row offsets
+            return wgrad_range_start<MODE == kModeGroupWgrad>(x, a.poff, a.wg_E, a.S, a.wg_mtiles * a.wg_ntiles, a.K_s,
+                                                              nb_real);
         }
         const long long c = cost_all * x / 8;
         if (c <= 0) return 0;                                   // also K_s == 0 (no shared blocks)

@@ -1,0 +1,124 @@
+"""Grouped products over some of the rows: the offsets of a rank's own experts
+begin and end far inside the rows.  Rows and experts outside hold NaN, results
+lie between guard values, and the bits are those of the whole call."""
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_feed_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BF16, F32 = torch.bfloat16, torch.float32
+MARK = -777.0
+GUARD = 1 << 16
+
+
+def _say(msg):
+    print(msg, file=sys.stderr, flush=True)
+
+
+def _rand(shape, dtype, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(dtype).to(DEV)
+
+
+def _guarded(shape, dtype):
+    """A result between guard values, and the whole buffer."""
+    n = int(np.prod(shape))
+    buf = torch.full((GUARD + n + GUARD,), MARK, dtype=dtype, device=DEV)
+    return buf[GUARD:GUARD + n].view(shape), buf
+
+
+def _untouched(buf):
+    return bool((buf[:GUARD] == MARK).all()) and bool((buf[-GUARD:] == MARK).all())
+
+
+K, N = 1544, 2056
+COUNTS = [500, 812, 0, 256, 700, 1, 333, 900, 512, 0, 640, 255, 1100, 17, 400, 766]
+
+
+@pytest.fixture(scope="module")
+def data():
+    ends = np.concatenate([[0], np.cumsum(COUNTS)])
+    R = int(ends[-1])
+    return dict(ends=ends, R=R, x=_rand((R, K), BF16, 1), dout=_rand((R, N), BF16, 2),
+                w=_rand((len(COUNTS), N, K), BF16, 3, 0.1),
+                index=torch.tensor(np.random.default_rng(4).permutation(R), dtype=torch.int32, device=DEV))
+
+
+SPANS = [(0, 16), (8, 16), (4, 16), (12, 16), (2, 10), (15, 16)]
+
+
+@pytest.mark.parametrize("gather", [False, True], ids=["", "gathered"])
+@pytest.mark.parametrize("wdtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("span", SPANS, ids=lambda s: f"{s[0]}to{s[1]}")
+def test_weight_gradients_of_some_experts(data, span, wdtype, gather):
+    a, b = span
+    _say(f"[spans] weight gradients of experts {a} to {b}, {wdtype}, gathered {gather}")
+    off = torch.tensor(data["ends"], dtype=torch.int32, device=DEV)
+    x, d, idx = data["x"], data["dout"], data["index"] if gather else None
+    dims = B.make_grouped_dims(data["R"], data["R"], b - a, K, N, BF16, wdtype)
+    assert B.grouped_weight_grad_workspace_size(dims) > 0            # the large tiles
+    whole = B.grouped_weight_grad(d, x, off, row_index=idx, weight_grad_dtype=wdtype)
+    lo, hi = int(data["ends"][a]), int(data["ends"][b])
+    d2, x2 = d.clone(), x.clone()
+    outside = torch.ones(data["R"], dtype=torch.bool, device=DEV)
+    outside[lo:hi] = False
+    d2[outside] = float("nan")
+    x2[data["index"][outside].long() if gather else outside] = float("nan")
+    dw, buf = _guarded((b - a, N, K), wdtype)
+    B.grouped_weight_grad(d2, x2, off[a:b + 1].contiguous(), row_index=idx, dweight=dw)
+    torch.cuda.synchronize()
+    assert _untouched(buf)
+    assert torch.equal(dw, whole[a:b])
+
+
+@pytest.mark.parametrize("gather", [False, True], ids=["", "gathered"])
+@pytest.mark.parametrize("span", [(8, 16), (2, 10)], ids=lambda s: f"{s[0]}to{s[1]}")
+def test_rows_of_some_experts(data, span, gather):
+    a, b = span
+    _say(f"[spans] rows of experts {a} to {b}, gathered {gather}")
+    off = torch.tensor(data["ends"], dtype=torch.int32, device=DEV)
+    idx = data["index"] if gather else None
+    part = off[a:b + 1].contiguous()
+    lo, hi = int(data["ends"][a]), int(data["ends"][b])
+    dims = B.make_grouped_dims(data["R"], data["R"], b - a, K, N, BF16)
+    assert B.grouped_workspace_size(dims) > 0
+    for whole, call, cols in (
+            (B.grouped_linear(data["x"], data["w"], off, row_index=idx),
+             lambda out: B.grouped_linear(data["x"], data["w"][a:b], part, row_index=idx, out=out), N),
+            (B.grouped_input_grad(data["dout"], data["w"], off),
+             lambda out: B.grouped_input_grad(data["dout"], data["w"][a:b], part, dx=out), K)):
+        out, buf = _guarded((data["R"], cols), BF16)
+        call(out)
+        torch.cuda.synchronize()
+        assert _untouched(buf)
+        assert torch.equal(out[lo:hi], whole[lo:hi])
+        assert bool((out[:lo] == MARK).all()) and bool((out[hi:] == MARK).all())
+
+
+@pytest.mark.parametrize("wdtype", [F32, BF16], ids=["f32", "bf16"])
+def test_offsets_at_the_end_of_the_rows(data, wdtype):
+    """Every group empty behind the last row, offsets past the rows, and all rows with the last expert."""
+    R, E = data["R"], 8
+    for ends in ([R] * 9, [R + 5] * 9, [2 ** 31 - 1] * 9, [-3] * 9, [R - 1000] * 8 + [R], [R - 1000] + [R] * 8):
+        _say(f"[spans] offsets {ends[:2]} .. {ends[-2:]}, {wdtype}")
+        off = torch.tensor(ends, dtype=torch.int64).clamp(max=2 ** 31 - 1).to(torch.int32).to(DEV)
+        dw, buf = _guarded((E, N, K), wdtype)
+        B.grouped_weight_grad(data["dout"], data["x"], off, row_index=data["index"], dweight=dw)
+        safe = np.maximum.accumulate(np.clip(np.array(ends, np.int64), 0, R))
+        torch.cuda.synchronize()
+        assert _untouched(buf)
+        for e in range(E):
+            n = int(safe[e + 1] - safe[e])
+            if n == 0:
+                assert not bool(dw[e].any())
+            else:
+                one = torch.tensor([safe[e], safe[e + 1]], dtype=torch.int32, device=DEV)
+                ref = B.grouped_weight_grad(data["dout"], data["x"], one, row_index=data["index"],
+                                            weight_grad_dtype=wdtype)
+                assert n == 1000 and torch.equal(dw[e], ref[0]) and bool(ref.any())

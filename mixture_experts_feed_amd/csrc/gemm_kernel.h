@@ -502,6 +502,7 @@ __device__ __forceinline__ Tile<TE> decode_tile(const GemmKArgs& a, int L, int B
 template <typename TE, int BN, int BM, int WN, int WM, int SA, int SB, int ROWB, int GM, int SCHED, int MODE>
 __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_kernel(const GemmKArgs a) {
     constexpr int NW = WN * WM;                     // waves per workgroup
+    static_assert(SCHED != kSchedGroup || !wgrad_mode<MODE>(), "one slot for the next tile: every tile has a K loop");
     static_assert(NW == 8 || NW == 4, "eight waves (two per SIMD), or four (two workgroups per CU)");
     static_assert(SB >= 2 && SA <= 8 && (SA == SB || SA == SB + 1), "weight stages = token stages (+1)");
     // stages unrolled per K-loop iteration: every weight and token buffer index
@@ -617,9 +618,10 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
     if (L >= L_end) return;
     // kSchedQueue: tiles L_beg + nloc + q for q = 0, 1, ... of the XCD's counter
     // (zero at launch); thread 0 draws the next one while the current tile
-    // runs and hands it to the workgroup through LDS
-    __shared__ int q_next;
-    int q_val = 0;
+    // runs and hands it to the workgroup through LDS (next_slot; tiles that always
+    // have a K loop, whose barriers keep the turns apart, take one slot)
+    __shared__ int q_next[WG ? kNextSlots : 1];
+    int q_val = 0, turn = 0;
     auto draw = [&]() __attribute__((always_inline)) {
         if constexpr (SCHED == kSchedQueue)
             if (tid == 0)
@@ -1149,14 +1151,15 @@ __global__ __launch_bounds__(WN * WM * 64, 512 / (WN * WM * 64)) void moe_gemm_k
         if constexpr (SCHED == kSchedGroup) {
             // the next tile is taken now that this workgroup is free
             if (tid == 0)
-                q_next = __hip_atomic_fetch_add(a.round_counter + xcd, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                q_next[0] = __hip_atomic_fetch_add(a.round_counter + xcd, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             __syncthreads();
-            L = L_beg + nloc + q_next;
+            L = L_beg + nloc + q_next[0];
         } else if constexpr (SCHED == kSchedQueue) {
             // (no loads are in flight here: the last stage waited for all)
-            if (tid == 0) q_next = q_val;
+            const int slot = WG ? next_slot(turn++) : 0;
+            if (tid == 0) q_next[slot] = q_val;
             __syncthreads();
-            L = L_beg + nloc + q_next;
+            L = L_beg + nloc + q_next[slot];
         } else {
             L += nloc;
         }

@@ -1,5 +1,6 @@
-// Where each XCD's range of weight-gradient tiles begins.  Plain constexpr
-// arithmetic, so that a host program can run it over offsets of any kind.
+// Where each XCD's range of weight-gradient tiles begins, and where a workgroup
+// finds its next tile.  Plain constexpr arithmetic, so that a host program can
+// run it over offsets of any kind.
 #pragma once
 
 #include <algorithm>
@@ -43,5 +44,14 @@ constexpr int wgrad_range_start(int x, const int32_t* poff, int E, int S, int pe
     // (BASED: whatever the offsets hold, no range starts before the first tile)
     return BASED ? std::clamp(at, 0, tiles) : tiles < at ? tiles : at;
 }
+
+// The LDS slot that hands the workgroup's tile of this turn from thread 0 to the
+// other waves: write, barrier, read.  A weight-gradient tile of an expert without
+// rows has no K loop, so no other barrier: in one slot, thread 0 could write the
+// next turn's tile before a slower wave has read this one's.  With two in turn,
+// it writes a slot again only after the barrier of the turn between, which every
+// wave reaches after its read.
+constexpr int kNextSlots = 2;
+constexpr int next_slot(int turn) { return turn % kNextSlots; }
 
 }  // namespace inkling

@@ -122,3 +122,34 @@ def test_offsets_at_the_end_of_the_rows(data, wdtype):
                 ref = B.grouped_weight_grad(data["dout"], data["x"], one, row_index=data["index"],
                                             weight_grad_dtype=wdtype)
                 assert n == 1000 and torch.equal(dw[e], ref[0]) and bool(ref.any())
+
+
+def test_weight_gradients_of_mostly_empty_experts():
+    """Tiles without a K loop in a row: most experts have no rows, and each workgroup takes several of their tiles."""
+    E, k, n = 256, 264, 520
+    counts = np.zeros(E, np.int64)
+    counts[[0, 7, 100, 101, 255]] = [300, 1, 700, 64, 33]
+    ends = np.concatenate([[40], 40 + np.cumsum(counts)])
+    R = int(ends[-1]) + 9
+    dims = B.make_grouped_dims(R, R, E, k, n, BF16, F32)
+    assert B.grouped_weight_grad_workspace_size(dims) > 0
+    x, d = _rand((R, k), BF16, 5), _rand((R, n), BF16, 6)
+    off = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    _say(f"[spans] {E} experts, 5 with rows")
+    first = None
+    for turn in range(4):
+        dw, buf = _guarded((E, n, k), F32)
+        B.grouped_weight_grad(d, x, off, dweight=dw)
+        torch.cuda.synchronize()
+        assert _untouched(buf)
+        assert first is None or torch.equal(dw, first), f"turn {turn}"
+        first = dw
+    full = torch.ones(E, dtype=torch.bool, device=DEV)
+    for e in np.flatnonzero(counts):
+        r = slice(int(ends[e]), int(ends[e + 1]))
+        d64, x64 = d[r].cpu().double(), x[r].cpu().double()
+        # products of bf16 are exact in fp32; n sums move by at most 2 n 2^-24 of the magnitudes
+        bound = 2 * float(counts[e]) * 2.0 ** -24 * (d64.abs().t() @ x64.abs()) + 1e-30
+        assert bool(((first[e].cpu().double() - d64.t() @ x64).abs() <= bound).all()), e
+        full[e] = False
+    assert not bool(first[full].any())

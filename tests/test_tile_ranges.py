@@ -1,6 +1,7 @@
 """Where each XCD's range of weight-gradient tiles begins (csrc/tile_ranges.h),
 compiled for the host: whatever offsets a caller gives, the eight ranges cover
-every tile once, from 0 to the tile count."""
+every tile once, from 0 to the tile count.  And the slots through which a
+workgroup's waves learn their next tile."""
 import ctypes
 import os
 import shutil
@@ -22,6 +23,8 @@ void starts(int based, const int32_t* poff, int E, int S, int per_p, int K_s, in
                        : inkling::wgrad_range_start<false>(x, poff, E, S, per_p, K_s, tiles);
 }
 int tile_cost() { return inkling::kWgradEpi; }
+int next_slot(int turn) { return inkling::next_slot(turn); }
+int next_slots() { return inkling::kNextSlots; }
 }
 """
 
@@ -124,3 +127,37 @@ def test_row_offsets_need_the_base(lib):
     late = _uniform(16, 512)[8:]
     assert _starts(lib, late, 384, based=False).min() < 0
     assert _starts(lib, late, 384).min() == 0
+
+
+def _wrong_reads(slot_of, slots, turns=4):
+    """Every order in which thread 0's wave (write, barrier, read) and another (barrier, read) can take their
+    steps over `turns` tiles without a K loop: the turns at which a wave can read another turn's tile."""
+    programs = [[step for t in range(turns) for step in (("write", t), ("wait", t), ("read", t))],
+                [step for t in range(turns) for step in (("wait", t), ("read", t))]]
+    wrong, seen = set(), set()
+    todo = [((0, 0), (None,) * slots)]
+    while todo:
+        at, held = state = todo.pop()
+        if state in seen:
+            continue
+        seen.add(state)
+        steps = [p[i] if i < len(p) else None for p, i in zip(programs, at)]
+        if all(s is not None and s[0] == "wait" for s in steps):
+            todo.append(((at[0] + 1, at[1] + 1), held))   # the barrier lets both go
+            continue
+        for w, s in enumerate(steps):
+            if s is None or s[0] == "wait":
+                continue
+            now = list(held)
+            if s[0] == "write":
+                now[slot_of(s[1])] = s[1]
+            elif held[slot_of(s[1])] != s[1]:
+                wrong.add(s[1])
+            todo.append(((at[0] + (w == 0), at[1] + (w == 1)), tuple(now)))
+    return wrong
+
+
+def test_every_wave_reads_its_turns_tile(lib):
+    assert lib.next_slots() == 2 and {lib.next_slot(t) for t in range(9)} == {0, 1}
+    assert _wrong_reads(lib.next_slot, lib.next_slots()) == set()
+    assert _wrong_reads(lambda t: 0, 1)      # one slot: a slow wave can read the next turn's tile

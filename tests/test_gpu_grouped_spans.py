@@ -153,3 +153,34 @@ def test_weight_gradients_of_mostly_empty_experts():
         assert bool(((first[e].cpu().double() - d64.t() @ x64).abs() <= bound).all()), e
         full[e] = False
     assert not bool(first[full].any())
+
+
+@pytest.fixture(scope="module")
+def far_rows():
+    """x of 2^29 + 64 rows of 16 bytes, and 40 of its rows on both sides of bytes 2^31, 2^32 and 2^33."""
+    x = torch.zeros(((1 << 29) + 64, 8), dtype=BF16, device=DEV)
+    at = torch.cat([torch.arange(b - 5, b + 5) for b in (1 << 27, 1 << 28, (1 << 29) - 5, (1 << 29) + 59)])
+    rows = _rand((40, 8), BF16, 11)
+    x[at.to(DEV)] = rows
+    return x, at, rows
+
+
+@pytest.mark.parametrize("E,R,n", [(2, 300, 40), (2, 5000, 4096), (512, 1000, 40960)],
+                         ids=["small_tiles", "large_tiles", "streamed_weights"])
+def test_gathered_rows_past_32_bits(far_rows, E, R, n):
+    """Rows of x whose byte offsets pass 2^32, against the same rows of a short x."""
+    x, at, rows = far_rows
+    near = torch.tensor(np.random.default_rng(R).integers(0, 40, R), dtype=torch.int32)
+    far = at[near.long()].to(torch.int32).to(DEV)
+    near = near.to(DEV)
+    ends = np.sort(np.random.default_rng(E).integers(0, R + 1, E + 1))
+    ends[0], ends[-1] = 0, R
+    off = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    w, d = _rand((E, n, 8), BF16, 12), _rand((R, n), BF16, 13)
+    _say(f"[spans] gathered rows past 2^32 bytes, {E} experts, {R} rows, {n} columns")
+    out, want = B.grouped_linear(x, w, off, row_index=far), B.grouped_linear(rows, w, off, row_index=near)
+    dw, dwant = (B.grouped_weight_grad(d, x, off, row_index=far),
+                 B.grouped_weight_grad(d, rows, off, row_index=near))
+    torch.cuda.synchronize()
+    assert bool(want.any()) and torch.equal(out, want)
+    assert bool(dwant.any()) and torch.equal(dw, dwant)

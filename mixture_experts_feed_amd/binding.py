@@ -554,8 +554,9 @@ def _grouped_weight_grad_plan(*sizes):
     return ctypes.byref(dims), grouped_weight_grad_workspace_size(dims)
 
 
-def _grouped_checks(rows_name, src, weight, offsets, width, row_index):
-    """Checks shared by the row products; returns (rows, E, N, K)."""
+def _grouped_checks(rows_name, src, weight, offsets, axis, row_index):
+    """Checks shared by the row products, whose rows are as wide as weight's
+    `axis`; returns (rows, E, N, K)."""
     if src.dim() != 2 or weight.dim() != 3:
         raise ValueError(f"{rows_name} must be [rows, features] and weight [n_groups, out_features, in_features]")
     dev = src.device
@@ -563,8 +564,8 @@ def _grouped_checks(rows_name, src, weight, offsets, width, row_index):
     _operand(weight, "weight", weight.dtype, dev)
     E, N, K = weight.shape
     R, have = src.shape
-    if have != width:
-        raise ValueError(f"{rows_name} must have {width} columns, got {have}")
+    if have != weight.shape[axis]:
+        raise ValueError(f"{rows_name} must have {weight.shape[axis]} columns, got {have}")
     _grouped_plan_checks(offsets, E, row_index, dev)
     return (R if row_index is None else row_index.shape[0]), E, N, K
 
@@ -614,7 +615,7 @@ def grouped_linear(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
     any number of rows), weight [E, N, K], offsets [E + 1] int32 on the device;
     out [rows, N].  Rows outside the groups are left as they are (in an `out`
     made here: unset)."""
-    R, E, N, K = _grouped_checks("x", x, weight, offsets, weight.shape[-1], row_index)
+    R, E, N, K = _grouped_checks("x", x, weight, offsets, 2, row_index)
     dev = x.device
     out_dtype = _result_dtype("out", out, out_dtype, x.dtype)
     dims, need = _grouped_plan(R, x.shape[0], E, K, N, x.dtype, out_dtype)
@@ -630,7 +631,7 @@ def grouped_input_grad(dout: torch.Tensor, weight: torch.Tensor, offsets: torch.
                        workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """inkling_grouped_input_grad: dx[r] = weight[e]^T dout[r], [rows, K]; with a
     row_index in the forward, the rows of one x row are for the caller to sum."""
-    R, E, N, K = _grouped_checks("dout", dout, weight, offsets, weight.shape[1], None)
+    R, E, N, K = _grouped_checks("dout", dout, weight, offsets, 1, None)
     dev = dout.device
     dx_dtype = _result_dtype("dx", dx, dx_dtype, dout.dtype)
     dims, need = _grouped_plan(R, R, E, K, N, dout.dtype, dx_dtype)

@@ -35,3 +35,12 @@ def test_the_library_refuses_what_32_bits_hold():
     with pytest.raises(B.InklingError) as e:
         B._norm_plan(1, 2 ** 31 - 1, "layer", BF16, 1e-6)
     assert e.value.code == B.INKLING_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("shape", [(), (64,), (64, 64), (1, 2, 64, 64)])
+def test_a_weight_of_other_dimensions_is_a_value_error(shape):
+    rows, w, off = torch.zeros((3, 64), dtype=BF16), torch.zeros(shape, dtype=BF16), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="n_groups, out_features, in_features"):
+        B.grouped_linear(rows, w, off)
+    with pytest.raises(ValueError, match="n_groups, out_features, in_features"):
+        B.grouped_input_grad(rows, w, off)

@@ -246,7 +246,8 @@ __global__ __launch_bounds__((max_threads<NV, G>()), (NV != 1 ? 2 : G != 0 ? 4 :
             R::load(nd, dout + next * H, t, lanes, full, last);
         }
         const float m = RMS ? 0.0f : st.x, r = st.y;
-        // columns that do not exist have dout 0 and w 0: they add nothing
+        // columns that do not exist have dout 0 and w 0, and xh 0: they add nothing
+        // ((0 - m) r may overflow where no xh of the row does, and 0 inf is NaN)
         float xh[NV][V], c[NV][V];
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -262,9 +263,12 @@ __global__ __launch_bounds__((max_threads<NV, G>()), (NV != 1 ? 2 : G != 0 ? 4 :
                 __asm__ volatile("" : "+s"(wp), "+v"(s[0]));
                 R::column(wr[j], wp, j, t, lanes, H);
             }
+            const int left = H - (j * lanes + t) * V;   // columns of this vector that exist
+            const float rj = RMS || left > 0 ? r : 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                xh[j][i] = (xh[j][i] - m) * r;
+                xh[j][i] = (xh[j][i] - m) * rj;
+                if constexpr (TAIL && !RMS) xh[j][i] = i < left ? xh[j][i] : 0.0f;
                 c[j][i] = d[i] * wr[j][i];
                 dw[j][i] += d[i] * xh[j][i];
                 if constexpr (!RMS) {

@@ -6,8 +6,10 @@
 //   dw = sum over rows of dy xh,  db = sum over rows of dy.
 //
 // HBM bounds both passes: x is read once and kept in registers for the second
-// moment about the mean (two passes over registers, so a large mean costs no
-// digits), the result is written once.
+// moment about the mean, the result is written once.  A large mean costs no
+// digits: fp32 rows also take the sum of x - m in that second pass over the
+// registers, which gives back what the first sum was rounded by (the sum of bf16
+// rows is exact wherever that would matter).
 //
 // A row is held in 16-byte vectors, one a lane where the width allows: rows of
 // up to 64 vectors by 8 to 64 neighbouring lanes of a wave (no LDS), wider ones
@@ -157,7 +159,13 @@ __global__ __launch_bounds__((max_threads<NV, G>()), (NV == 1 ? 6 : 2)) void nor
     TE* __restrict__ out, float* __restrict__ stats) {
     using R = Row<TE, NV, TAIL, NT>;
     constexpr int V = R::V;
-    __shared__ float sums[2][2][kMaxWaves][1];
+    // fp32 rows: the sum of x - m too.  (bf16 rows whose mean is large against their
+    // spread have values of one or two exponents, so at most 2^14 multiples of one
+    // step below 2^9 of them: their sum is exact.  8192 x 6144 would take 46 us
+    // instead of 40; fp32, 2048 x 12288, takes 47 instead of 46.)
+    constexpr bool kShift = !RMS && sizeof(TE) == 4;
+    constexpr int kSums = kShift ? 2 : 1;
+    __shared__ float first[2][kMaxWaves][1], second[2][kMaxWaves][kSums];
     const Place<G> at;
     const int full = H / V, last = H - full * V, t = at.t, lanes = at.lanes;
     const float n = (float)H;
@@ -181,32 +189,50 @@ __global__ __launch_bounds__((max_threads<NV, G>()), (NV == 1 ? 6 : 2)) void nor
         }
         float m = 0.0f;
         if constexpr (!RMS) {
-            row_sums<G, 1>(s, sums[turn][0]);
+            row_sums<G, 1>(s, first[turn]);
             m = s[0] / n;   // a quotient, not contracted into x - m
         }
-        s[0] = 0.0f;
+        // d = x - m.  The mean of d is what the rounding of a long sum left in m: with
+        // it, mean and variance are as exact as those of values around 0
+        float q[kSums];
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) q[i] = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int left = H - (j * lanes + t) * V;   // columns of this vector that exist
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float d = v[j][i] - m;
-                s[0] += (RMS || (TAIL ? i < left : left > 0)) ? d * d : 0.0f;   // RMS: absent columns are 0
+                const bool real = RMS || (TAIL ? i < left : left > 0);   // RMS: absent columns are 0
+                if constexpr (kShift) {
+                    v[j][i] = real ? v[j][i] - m : 0.0f;   // d from here on
+                    q[1] += v[j][i];
+                    q[0] += v[j][i] * v[j][i];
+                } else {
+                    const float d = v[j][i] - m;
+                    q[0] += real ? d * d : 0.0f;
+                }
             }
         }
-        row_sums<G, 1>(s, sums[turn][1]);
-        const float r = 1.0f / sqrtf(s[0] / n + eps);
+        row_sums<G, kSums>(q, second[turn]);
+        float shift = 0.0f, var = q[0] / n;
+        if constexpr (kShift) {
+            shift = q[1] / n;
+            var -= shift * shift;
+            if (var < 0.0f) var = 0.0f;   // (a NaN stays)
+        }
+        const float r = 1.0f / sqrtf(var + eps);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             float y[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                y[i] = (v[j][i] - m) * r * wr[j][i];
+                y[i] = (v[j][i] - (kShift ? shift : m)) * r * wr[j][i];
                 if constexpr (!RMS) y[i] += br[j][i];
             }
             R::store(out + (size_t)row * H, j, t, lanes, full, last, y);
         }
-        if (stats != nullptr && t == 0) *reinterpret_cast<float2*>(stats + 2 * (size_t)row) = make_float2(m, r);
+        if (stats != nullptr && t == 0)
+            *reinterpret_cast<float2*>(stats + 2 * (size_t)row) = make_float2(kShift ? m + shift : m, r);
 #pragma unroll
         for (int j = 0; j < NV; ++j) cur[j] = nxt[j];
     }

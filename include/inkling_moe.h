@@ -288,7 +288,8 @@ int inkling_dense_mlp_forward(const inkling_dense_dims_t* dims, const void* x, c
  * multiples of 8 up to 2^20, 1 <= n_groups <= 512, rows and x_rows at most
  * 2^31 - 257, fewer than 2^31 output tiles (fp32: fewer than 2^24, of 64 x 64).
  * Tensor pointers and workspace must be 16-byte aligned, offsets and row_index
- * 4-byte; the output must not overlap an operand.  Same conventions and errors as
+ * 4-byte; the output and the workspace must not overlap each other or an operand
+ * (INKLING_ERR_INVALID_ARGUMENT).  Same conventions and errors as
  * inkling_moe_forward otherwise; rows == 0 is a no-op for the first two and
  * writes zeros in weight_grad.
  */
@@ -340,7 +341,8 @@ int inkling_grouped_weight_grad(const inkling_grouped_dims_t* dims, const void* 
  * h, act, dact and dh in dims->dtype; arithmetic in fp32, rounded once.
  * Limits: intermediate a multiple of 16 up to 2^20, rows <= 2^31 - 257.
  * Tensor pointers 16-byte aligned (gamma, dgamma and row_count 4-byte); outputs
- * must not overlap operands.  No workspace; rows == 0 is a no-op.
+ * must not overlap each other or an operand (INKLING_ERR_INVALID_ARGUMENT).  No
+ * workspace; rows == 0 is a no-op.
  */
 typedef struct {
     int64_t rows;
@@ -378,8 +380,8 @@ int inkling_swiglu_backward(const inkling_swiglu_dims_t* dims, const void* dact,
  * forward and gives zero dweight and dbias in the backward.
  * Limits: hidden <= 16384 (any width; multiples of 8 bf16 or 4 fp32 values are
  * the fast path), rows <= 2^31 - 65537, 0 <= eps finite (eps 0 and a constant
- * row: infinite rstd).  Tensor pointers 16-byte aligned; outputs must not
- * overlap operands.
+ * row: infinite rstd).  Tensor pointers 16-byte aligned; outputs and workspace
+ * must not overlap each other or an operand (INKLING_ERR_INVALID_ARGUMENT).
  */
 typedef enum { INKLING_NORM_LAYER = 0, INKLING_NORM_RMS = 1 } inkling_norm_kind_t;
 

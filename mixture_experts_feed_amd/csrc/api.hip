@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/inkling_moe.h"
@@ -688,6 +689,28 @@ namespace {
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// n bytes from p (NULL: none)
+struct Bytes {
+    const void* p;
+    size_t n;
+};
+bool overlap(const Bytes& a, const Bytes& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p != nullptr && b.p != nullptr && a.n > 0 && b.n > 0 && (x < y ? y - x < a.n : x - y < b.n);
+}
+// whether what a call writes overlaps something that it reads, or itself
+bool writes_overlap(std::initializer_list<Bytes> writes, std::initializer_list<Bytes> reads) {
+    for (const Bytes* w = writes.begin(); w != writes.end(); ++w) {
+        for (const Bytes& r : reads)
+            if (overlap(*w, r)) return true;
+        for (const Bytes* o = w + 1; o != writes.end(); ++o)
+            if (overlap(*w, *o)) return true;
+    }
+    return false;
+}
+
+size_t value_bytes(int dtype) { return dtype == INKLING_BF16 ? 2 : 4; }
+
 int check_grouped_dims(const inkling_grouped_dims_t* d) {
     if (d == nullptr) return INKLING_ERR_INVALID_ARGUMENT;
     if (d->rows < 0 || d->x_rows < 0 || d->n_groups <= 0 || d->in_features <= 0 || d->out_features <= 0)
@@ -780,6 +803,13 @@ int grouped_rows(const inkling_grouped_dims_t* d, bool input_grad, const void* s
     GroupParams p = grouped_params(d, L, workspace, input_grad);
     if (small ? group_small_tiles(p.rows, p.E, p.n_cols) > kSmallTilesMax : group_max_tiles(p) > INT32_MAX - 4096)
         return INKLING_ERR_UNSUPPORTED;
+    const size_t es = value_bytes(d->dtype), rows = (size_t)d->rows;
+    if (writes_overlap({{out, rows * p.n_cols * value_bytes(d->out_dtype)}, {small ? nullptr : workspace, L.total}},
+                       {{src, (input_grad ? rows : (size_t)d->x_rows) * p.k_len * es},
+                        {weight, (size_t)d->n_groups * p.n_cols * p.k_len * es},
+                        {offsets, ((size_t)d->n_groups + 1) * 4},
+                        {row_index, rows * 4}}))
+        return INKLING_ERR_INVALID_ARGUMENT;
     p.src = src;
     p.weight = weight;
     p.row_index = row_index;
@@ -847,6 +877,15 @@ int inkling_grouped_weight_grad(const inkling_grouped_dims_t* dims, const void* 
         return INKLING_ERR_UNSUPPORTED;
     const GroupedLayout L = make_grouped_layout(dims, 0);
     if (!small && (workspace == nullptr || workspace_bytes < L.total)) return INKLING_ERR_WORKSPACE;
+    const size_t es = value_bytes(dims->dtype), rows = (size_t)dims->rows;
+    if (writes_overlap({{dweight, (size_t)dims->n_groups * dims->out_features * dims->in_features *
+                                      value_bytes(dims->out_dtype)},
+                        {small ? nullptr : workspace, L.total}},
+                       {{dout, rows * dims->out_features * es},
+                        {x, (size_t)dims->x_rows * dims->in_features * es},
+                        {offsets, ((size_t)dims->n_groups + 1) * 4},
+                        {row_index, rows * 4}}))
+        return INKLING_ERR_INVALID_ARGUMENT;
     GroupParams p = grouped_params(dims, L, workspace, false);
     hipStream_t s = (hipStream_t)stream;
     p.row_index = dims->rows > 0 ? row_index : nullptr;
@@ -940,6 +979,10 @@ int inkling_swiglu_forward(const inkling_swiglu_dims_t* dims, const void* h, con
         !aligned(row_count, 4))
         return INKLING_ERR_INVALID_ARGUMENT;
     if (checkpoint != nullptr && checkpoint_bytes < swiglu_checkpoint_bytes(dims)) return INKLING_ERR_WORKSPACE;
+    const size_t rows = (size_t)dims->rows, act_bytes = rows * dims->intermediate * value_bytes(dims->dtype);
+    if (writes_overlap({{act, act_bytes}, {checkpoint, swiglu_checkpoint_bytes(dims)}},
+                       {{h, 2 * act_bytes}, {gamma, rows * 4}, {row_count, 4}}))
+        return INKLING_ERR_INVALID_ARGUMENT;
     SwigluParams p = swiglu_params(dims, gamma, row_count, checkpoint);
     p.h = h;
     p.act = act;
@@ -960,6 +1003,13 @@ int inkling_swiglu_backward(const inkling_swiglu_dims_t* dims, const void* dact,
         !aligned(gamma, 4) || !aligned(dgamma, 4) || !aligned(row_count, 4))
         return INKLING_ERR_INVALID_ARGUMENT;
     if (checkpoint_bytes < swiglu_checkpoint_bytes(dims)) return INKLING_ERR_WORKSPACE;
+    const size_t rows = (size_t)dims->rows, act_bytes = rows * dims->intermediate * value_bytes(dims->dtype);
+    if (writes_overlap({{dh, 2 * act_bytes}, {act, act_bytes}, {dgamma, rows * 4}},
+                       {{dact, act_bytes},
+                        {checkpoint, swiglu_checkpoint_bytes(dims)},
+                        {gamma, rows * 4},
+                        {row_count, 4}}))
+        return INKLING_ERR_INVALID_ARGUMENT;
     SwigluParams p = swiglu_params(dims, gamma, row_count, const_cast<void*>(checkpoint));
     p.dact = dact;
     p.dh = dh;
@@ -977,6 +1027,10 @@ int inkling_norm_forward(const inkling_norm_dims_t* dims, const void* x, const f
     if (x == nullptr || weight == nullptr || out == nullptr || out == x) return INKLING_ERR_INVALID_ARGUMENT;
     if (dims->kind == INKLING_NORM_RMS && bias != nullptr) return INKLING_ERR_INVALID_ARGUMENT;
     if (!aligned(x, 16) || !aligned(out, 16) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(stats, 16))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    const size_t rows = (size_t)dims->rows, x_bytes = rows * dims->hidden * value_bytes(dims->dtype);
+    const size_t w_bytes = (size_t)dims->hidden * 4;
+    if (writes_overlap({{out, x_bytes}, {stats, rows * 8}}, {{x, x_bytes}, {weight, w_bytes}, {bias, w_bytes}}))
         return INKLING_ERR_INVALID_ARGUMENT;
     NormParams p = norm_params(dims);
     p.x = x;
@@ -1011,6 +1065,11 @@ int inkling_norm_backward(const inkling_norm_dims_t* dims, const void* dout, con
         !aligned(dweight, 16) || !aligned(dbias, 16) || !aligned(workspace, 16))
         return INKLING_ERR_INVALID_ARGUMENT;
     if (workspace == nullptr || workspace_bytes < norm_part_bytes(dims)) return INKLING_ERR_WORKSPACE;
+    const size_t rows = (size_t)dims->rows, x_bytes = rows * dims->hidden * value_bytes(dims->dtype);
+    const size_t w_bytes = (size_t)dims->hidden * 4;
+    if (writes_overlap({{dx, x_bytes}, {dweight, w_bytes}, {dbias, w_bytes}, {workspace, norm_part_bytes(dims)}},
+                       {{dout, x_bytes}, {x, x_bytes}, {weight, w_bytes}, {stats, rows * 8}}))
+        return INKLING_ERR_INVALID_ARGUMENT;
     NormParams p = norm_params(dims);
     p.dout = dout;
     p.x = x;

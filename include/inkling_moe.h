@@ -327,8 +327,9 @@ int inkling_grouped_weight_grad(const inkling_grouped_dims_t* dims, const void* 
  * The checkpoint holds each value as an int8 and one power of two for every 32
  * columns of a row: the smallest 2^e, e >= -126, with max|h| <= 127 * 2^e; the
  * int8 is h / 2^e to nearest, ties to even.  A value comes back off by at most
- * 2^(e-1), so by at most max|h| / 127 of its 32 columns; a block that holds an
- * infinity or a NaN comes back as NaN.  Layout: [rows][2*I] int8, then
+ * 2^(e-1), so by at most the larger of max|h| / 127 of its 32 columns and 2^-127
+ * (which is the larger for blocks of max|h| <= 127 * 2^-127, where e is -126); a
+ * block that holds an infinity or a NaN comes back as NaN.  Layout: [rows][2*I] int8, then
  * [rows][2*I/32] bytes e + 127 (255: NaN block); 2.0625 * I bytes a row, against
  * 8 * I of inkling_moe_forward_train's fp32 projections.
  * The backward is the derivative of act at the values that come back: with

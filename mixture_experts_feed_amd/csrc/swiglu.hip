@@ -3,8 +3,9 @@
 // h [R][2I] holds [g0, u0, g1, u1, ...]; act = gamma g sigmoid(g) u.  For the
 // backward pass h is kept as one byte a value: 32 consecutive columns share a
 // power of two 2^e, the smallest (e >= -126) with max|h| <= 127 2^e, and each
-// value is the int8 nearest to h / 2^e (ties to even), off by at most 2^(e-1),
-// that is max|h| / 127 of its block.  A power of two makes h / 2^e and q 2^e
+// value is the int8 nearest to h / 2^e (ties to even), off by at most 2^(e-1).
+// That is at most max|h| / 127 of its block while e > -126, that is from
+// max|h| > 127 2^-127 on; below, at most 2^-127.  A power of two makes h / 2^e and q 2^e
 // exact, so that the kept values do not depend on how a quotient is rounded.
 // The exponent is a byte, e + 127; 255 marks a block with an infinity or a NaN,
 // whose values come back as NaN.
@@ -35,9 +36,12 @@ constexpr int cols() { return 16 / (int)sizeof(TE); }
 template <typename TE>
 constexpr int block_lanes() { return 32 / cols<TE>(); }
 
-// bf16 rows take the hardware exponential and reciprocal (a relative error of a
-// few 2^-22 for |v| < 40, far below bf16's half step 2^-8); fp32 rows the
-// library exponential and a division.
+// bf16 rows take the hardware exponential and reciprocal: exp(-v) as 2^(-v log2 e)
+// is off by (1.5 |v| + 2) 2^-24 of itself (the rounding of v log2 e grows with |v|),
+// the sum and the reciprocal by 3 steps more: 2^-18 at |v| = 40, against bf16's
+// half step of 2^-8.  fp32 rows take the library exponential and a division.  Below
+// v = -87.3, where the sigmoid is less than 2^-126, it may come out as 0 (exp(-v)
+// passes fp32 at -88.7).
 template <typename TE>
 __device__ __forceinline__ float sigmoid_of(float v) {
     if constexpr (sizeof(TE) == 2) return __builtin_amdgcn_rcpf(1.0f + __expf(-v));

@@ -1,5 +1,5 @@
 """The 8-bit checkpoint's stated error on blocks of values near fp32's smallest,
-and the sigmoid where its exponential passes fp32."""
+the sigmoid where its exponential passes fp32, and data past the caches."""
 import numpy as np
 import pytest
 import torch
@@ -57,3 +57,35 @@ def test_gates_below_the_exponentials_range(dtype):
     rel = (1.5 * np.minimum(np.abs(g), 128.0) + 16.0) * 2.0 ** -24 + (2.0 ** -8 if dtype == BF16 else 0.0)
     bound = np.abs(want) * rel + np.where(g < -87.3, np.abs(g) * 1.5 * 2.0 ** -126, 0.0)
     assert (np.abs(act[0].cpu().double().numpy() - want) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype,R,I", [(BF16, 30011, 1024), (F32, 20011, 1024), (BF16, 200003, 208), (F32, 400009, 48)],
+                         ids=lambda v: str(v).replace("torch.", ""))
+def test_data_past_the_caches(dtype, R, I):
+    """More than 256 MB takes kernels that store past the caches: the bits are those of short calls on bands of the
+    rows, which do not, and rows from the count on are left as they were."""
+    es = 2 if dtype == BF16 else 4
+    assert R * I * (2 + 3 * es) > 256e6 and 1000 * I * (2 + 4 * es) < 256e6
+    g = torch.Generator(device=DEV).manual_seed(R)
+    h = (torch.randn((R, 2 * I), generator=g, device=DEV) * 2).to(dtype)
+    da = torch.randn((R, I), generator=g, device=DEV).to(dtype)
+    gamma = torch.rand((R,), generator=g, device=DEV)
+    used = R - 77
+    n = torch.tensor([used], dtype=torch.int32, device=DEV)
+    bufs = [torch.full((R, w), -777.0, dtype=dtype, device=DEV) for w in (I, 2 * I, I)]
+    dgamma = torch.full((R,), -777.0, device=DEV)
+    act, ck = B.swiglu_forward(h, gamma, row_count=n, out=bufs[0])
+    r = B.swiglu_backward(da, ck, gamma, row_count=n, dh=bufs[1], act=bufs[2], dgamma=dgamma)
+    for i in (0, 1000, R // 2, used - 1000):
+        rows = slice(i, i + 1000)
+        want, ck2 = B.swiglu_forward(h[rows], gamma[rows])
+        r2 = B.swiglu_backward(da[rows], ck2, gamma[rows])
+        torch.cuda.synchronize()
+        assert torch.equal(act[rows], want), i
+        assert torch.equal(ck[i * 2 * I:(i + 1000) * 2 * I], ck2[:1000 * 2 * I]), i
+        at = R * 2 * I + i * (I // 16)
+        assert torch.equal(ck[at:at + 1000 * (I // 16)], ck2[1000 * 2 * I:]), i
+        for k in ("dh", "act", "dgamma"):
+            assert torch.equal(r[k][rows], r2[k]), (k, i)
+    for t in (*bufs, dgamma):
+        assert bool((t[used:] == -777.0).all()) and not bool((t[:used] == -777.0).any())

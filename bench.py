@@ -36,7 +36,7 @@ ROOT = os.path.dirname(os.path.abspath(__file__))
 # the GEMM sources hash to the value recorded beside them.
 TRAFFIC_PROFILE = os.path.join(ROOT, "profiles", "gate_up_prefill_h6144_traffic.md")
 GEMM_SOURCES = [os.path.join(ROOT, "mixture_experts_feed_amd", "csrc", f)
-                for f in ("gemm.hip", "gemm_kernel.h", "common.h")]
+                for f in ("gemm.hip", "gemm_kernel.h", "tile_ranges.h", "common.h")]
 
 
 def log(msg):

@@ -278,7 +278,8 @@ int inkling_dense_mlp_forward(const inkling_dense_dims_t* dims, const void* x, c
  * offsets [n_groups + 1] int32 on the device, non-decreasing, the last at most
  * `rows`.  Rows before offsets[0] and from offsets[n_groups] on are neither
  * read nor written; an expert without rows is skipped, and its dweight is
- * zeros.  Offsets that break this are clamped to [0, rows] and raised to the
+ * zeros.  (offsets + a with the weights from expert a on and n_groups fewer is so
+ * the call for a range of the experts.)  Offsets that break this are clamped to [0, rows] and raised to the
  * largest before them, and an index outside [0, x_rows) takes the nearest row
  * inside: wrong values, never an access out of bounds.
  * Operands in dtype, sums in fp32 (for INKLING_F32 fp32 products too), rounded
@@ -373,7 +374,8 @@ int inkling_swiglu_backward(const inkling_swiglu_dims_t* dims, const void* dact,
  *                       be NULL)
  * weight, bias, dweight and dbias are [hidden] fp32; x, out, dout and dx in
  * dims->dtype; statistics and sums in fp32, the variance about the mean (no
- * difference of large squares), each result rounded once.
+ * difference of large squares), each result rounded once.  A row whose sum or
+ * squares pass fp32's range (3.4e38) gives what their infinity gives.
  *   stats  [rows][2] fp32: mean (0 for RMS) and rstd; forward: may be NULL
  * The backward returns gradients of sum(dout * out); dweight and dbias are
  * overwritten and summed over the rows in a fixed order (bit-reproducible).

@@ -91,11 +91,14 @@ int grid_of(long long tiles, int per_cu) {
 
 // Forward and input gradient on 256 x 256 tiles, one workgroup a CU: bound by the
 // matrix units once an expert has some hundred rows (each stage of 64 K moves 64 KB
-// through LDS for 8.4 MFLOP).  Forward, 128 experts of 512 rows on average, 6144 x
-// 4096: 3290 us, 1.00 PFLOP/s; input gradient, 64 of 384, 2048 x 1536: 205 us, 0.75
-// PFLOP/s (768 tiles, half of each expert's last row tile empty).  128 x 256 and 256 x
-// 128 tiles, two workgroups a CU, were 5 to 30% slower at 1.2 to 24 rounds, and one
-// wave a SIMD with 128 x 128 tiles of its own 0 to 10% faster on even experts only.
+// through LDS for 8.4 MFLOP), less what the last row tile of an expert lacks.
+// Forward, 128 experts of 512 rows each, 6144 x 4096: 2934 us, 1.12 PFLOP/s; of 316
+// to 754 rows, whose tiles hold 1.23 times the rows: 3392 us, 0.97 PFLOP/s.  Input
+// gradient, 64 experts of 27 to 1200 rows (384 on average), 2048 columns from 1536:
+// 205 us, 0.75 PFLOP/s (128 row tiles, a quarter of their rows empty, by 8 column
+// tiles: four rounds).  128 x 256 and 256 x 128 tiles, two workgroups a CU, were 5 to
+// 30% slower at 1.2 to 24 rounds, and one wave a SIMD with 128 x 128 tiles of its own
+// 0 to 10% faster on even experts only.
 // kSchedGroup (gemm_kernel.h) starts the tiles that share rows or weights on one
 // XCD together: 1 to 25% faster than the other walks.
 template <int SCHED, int MODE>
@@ -108,8 +111,11 @@ void launch_256(const GemmKArgs& a, long long max_tiles, hipStream_t stream) {
 
 // Up to 48 rows an expert on average, the forward streams the weights past tiles
 // of 16 rows (the layer's decode tiles): 805 us at 2 rows an expert, 6144 x 4096,
-// 6.9 TB/s.  Input gradients always take 256 x 256 tiles (whose few-row form
-// skips the row blocks without rows): 407 us at 64 rows, 4096 x 2048, 5.4 TB/s.
+// 6.9 TB/s.  The host knows the average only: where one expert of 128 holds all of
+// 6000 rows, its weights stream past 375 tiles, 1588 us, and the same rows given as
+// one expert take 305 (46 rows in each: 2421).  Input gradients always take 256 x 256
+// tiles (whose few-row form skips the row blocks without rows): 407 us at 64 rows,
+// 4096 x 2048, 5.4 TB/s.
 int group_cfg(int rows, int E, bool input_grad) {
     return !input_grad && (double)rows / E <= 48.0 ? 1 : 0;
 }
@@ -140,8 +146,9 @@ hipError_t launch_group_plan(const GroupParams& p, const int32_t* offsets, bool 
 //   47 / 46, 57 at 128 of 2 (1024 x 1024), 65, 71 / 64, 66 at 128 of 64 (1024 x 1024);
 //   209, 209 / 156, 206 at 128 of 2 (2048 x 2048, 2^29 values);
 // - fp32 at every size: 11 / 34 us at 8 experts of 83 rows (136 x 200), 50 / 84 at 32
-//   of 64 (1024 x 1024), and up to 24% slower on large products (737 / 594 at 16 of
-//   512, 2048 x 2048), which bf16 is for.
+//   of 64 (1024 x 1024).  At 16 of 512 (2048 x 2048), even or not: 594 to 654 (105 to
+//   116 TFLOP/s; input gradient 585 to 615, weight gradient 622 to 639), where the large
+//   tiles, whose fp32 form is gone, took 594.
 bool group_small(int dtype, int rows, int E, int n_cols, int k_len) {
     if (dtype == 0) return true;
     if (rows <= 64LL * E && (double)E * n_cols * k_len <= (double)(1 << 27)) return true;

@@ -181,23 +181,18 @@ def _dtype_code(dt: torch.dtype) -> int:
     raise ValueError(f"unsupported dtype {dt}")
 
 
-def _i32(value, name: str) -> int:
-    """An int that a C int32 field holds (ctypes would keep its low 32 bits)."""
-    value = int(value)
-    if not -2 ** 31 <= value < 2 ** 31:
-        raise ValueError(f"{name} must fit in 32 bits, got {value}")
-    return value
-
-
-def _sizes32(**sizes):
-    return [_i32(v, n) for n, v in sizes.items()]
+def _ints32(*sizes):
+    """Ints that C int32 fields hold (ctypes would keep their low 32 bits)."""
+    sizes = [int(v) for v in sizes]
+    if max(sizes) >= 2 ** 31 or min(sizes) < -2 ** 31:
+        raise ValueError(f"sizes must fit in 32 bits, got {sizes}")
+    return sizes
 
 
 def make_dims(T, hidden, n_routed, top_k, n_shared, intermediate, dtype, out_dtype=None) -> Dims:
     code = dtype if isinstance(dtype, int) else _dtype_code(dtype)
     ocode = code if out_dtype is None else (out_dtype if isinstance(out_dtype, int) else _dtype_code(out_dtype))
-    return Dims(int(T), *_sizes32(hidden=hidden, n_routed=n_routed, top_k=top_k, n_shared=n_shared,
-                                  intermediate=intermediate), code, ocode)
+    return Dims(int(T), *_ints32(hidden, n_routed, top_k, n_shared, intermediate), code, ocode)
 
 
 def workspace_size(dims: Dims) -> int:
@@ -384,7 +379,7 @@ def set_stage_events(events: Optional[ctypes.Array]) -> None:
 def make_dense_dims(T, hidden, intermediate, dtype, out_dtype=None) -> DenseDims:
     code = dtype if isinstance(dtype, int) else _dtype_code(dtype)
     ocode = code if out_dtype is None else (out_dtype if isinstance(out_dtype, int) else _dtype_code(out_dtype))
-    return DenseDims(int(T), *_sizes32(hidden=hidden, intermediate=intermediate), code, ocode)
+    return DenseDims(int(T), *_ints32(hidden, intermediate), code, ocode)
 
 
 def dense_workspace_size(dims: DenseDims) -> int:
@@ -521,8 +516,7 @@ def _call(dev, name: str, *args) -> None:
 def make_grouped_dims(rows, x_rows, n_groups, in_features, out_features, dtype, out_dtype=None) -> GroupedDims:
     code = dtype if isinstance(dtype, int) else _dtype_code(dtype)
     ocode = code if out_dtype is None else (out_dtype if isinstance(out_dtype, int) else _dtype_code(out_dtype))
-    return GroupedDims(int(rows), int(x_rows), *_sizes32(n_groups=n_groups, in_features=in_features,
-                                                         out_features=out_features), code, ocode)
+    return GroupedDims(int(rows), int(x_rows), *_ints32(n_groups, in_features, out_features), code, ocode)
 
 
 def grouped_workspace_size(dims: GroupedDims) -> int:
@@ -673,7 +667,7 @@ def grouped_weight_grad(dout: torch.Tensor, x: torch.Tensor, offsets: torch.Tens
 
 
 def make_swiglu_dims(rows, intermediate, dtype) -> SwigluDims:
-    return SwigluDims(int(rows), _i32(intermediate, "intermediate"), dtype if isinstance(dtype, int) else _dtype_code(dtype))
+    return SwigluDims(int(rows), *_ints32(intermediate), dtype if isinstance(dtype, int) else _dtype_code(dtype))
 
 
 def swiglu_checkpoint_size(dims: SwigluDims) -> int:
@@ -764,7 +758,7 @@ def make_norm_dims(rows, hidden, kind, dtype, eps) -> NormDims:
         if kind not in NORM_KINDS:
             raise ValueError(f"kind must be one of {sorted(NORM_KINDS)}")
         kind = NORM_KINDS[kind]
-    return NormDims(int(rows), _i32(hidden, "hidden"), kind, dtype if isinstance(dtype, int) else _dtype_code(dtype),
+    return NormDims(int(rows), *_ints32(hidden), kind, dtype if isinstance(dtype, int) else _dtype_code(dtype),
                     float(eps))
 
 

@@ -184,3 +184,64 @@ def test_gathered_rows_past_32_bits(far_rows, E, R, n):
     torch.cuda.synchronize()
     assert bool(want.any()) and torch.equal(out, want)
     assert bool(dwant.any()) and torch.equal(dw, dwant)
+
+
+def _step(data, off, w, bufs, ws=None, wws=None):
+    B.grouped_linear(data["x"], w, off, row_index=data["index"], out=bufs[0], workspace=ws)
+    B.grouped_input_grad(data["dout"], w, off, dx=bufs[1], workspace=ws)
+    B.grouped_weight_grad(data["dout"], data["x"], off, row_index=data["index"], dweight=bufs[2], workspace=wws)
+
+
+def _bufs(data, E):
+    return [torch.full(s, MARK, dtype=BF16, device=DEV) for s in ((data["R"], N), (data["R"], K), (E, N, K))]
+
+
+def test_a_graph_whose_offsets_move(data):
+    """Captured with the later experts' offsets, replayed with others in the same memory: late, early, all at the
+    end, none; each replay against eager calls of the same offsets."""
+    E, ends, R = 8, data["ends"], data["R"]
+    off = torch.tensor(ends[8:], dtype=torch.int32, device=DEV)
+    w, bufs = data["w"][:E], _bufs(data, E)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _step(data, off, w, bufs)
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _step(data, off, w, bufs)
+    for moved in (ends[8:], ends[:9], [R - 2500] * 8 + [R], [R] * 9, ends[4:13], [R // 2] * 4 + [R] * 5):
+        off.copy_(torch.tensor(np.asarray(moved), dtype=torch.int32))
+        for t in bufs:
+            t.fill_(MARK)
+        g.replay()
+        torch.cuda.synchronize()
+        want = _bufs(data, E)
+        _step(data, off, w, want)
+        torch.cuda.synchronize()
+        for a, b in zip(bufs, want):
+            assert torch.equal(a, b), list(moved)[:3]
+
+
+def test_two_calls_at_once(data):
+    """Two streams, each with workspaces of its own, over the two halves of the experts."""
+    off = torch.tensor(data["ends"], dtype=torch.int32, device=DEV)
+    halves = [(off[:9].contiguous(), data["w"][:8]), (off[8:].contiguous(), data["w"][8:])]
+    want = [_bufs(data, 8) for _ in halves]
+    for (o, w), b in zip(halves, want):
+        _step(data, o, w, b)
+    torch.cuda.synchronize()
+    dims = B.make_grouped_dims(data["R"], data["R"], 8, K, N, BF16)
+    streams = [torch.cuda.Stream() for _ in halves]
+    got = [_bufs(data, 8) for _ in halves]
+    spaces = [[torch.empty(n, dtype=torch.uint8, device=DEV) for n in
+               (B.grouped_workspace_size(dims), B.grouped_weight_grad_workspace_size(dims))] for _ in halves]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for st, (o, w), b, (ws, wws) in zip(streams, halves, got, spaces):
+            with torch.cuda.stream(st):
+                _step(data, o, w, b, ws, wws)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        for t, u in zip(a, b):
+            assert torch.equal(t, u)

@@ -278,10 +278,11 @@ int inkling_dense_mlp_forward(const inkling_dense_dims_t* dims, const void* x, c
  * offsets [n_groups + 1] int32 on the device, non-decreasing, the last at most
  * `rows`.  Rows before offsets[0] and from offsets[n_groups] on are neither
  * read nor written; an expert without rows is skipped, and its dweight is
- * zeros.  (offsets + a with the weights from expert a on and n_groups fewer is so
- * the call for a range of the experts.)  Offsets that break this are clamped to [0, rows] and raised to the
- * largest before them, and an index outside [0, x_rows) takes the nearest row
- * inside: wrong values, never an access out of bounds.
+ * zeros.  (So offsets + a, with the weights from expert a on and n_groups the
+ * number of experts wanted, is the call for a range of the experts.)  Offsets
+ * that break this are clamped to [0, rows] and raised to the largest before them,
+ * and an index outside [0, x_rows) takes the nearest row inside: wrong values,
+ * never an access out of bounds.
  * Operands in dtype, sums in fp32 (for INKLING_F32 fp32 products too), rounded
  * once to out_dtype (out, dx or dweight); infinities and NaN propagate.  Each
  * sum's order is fixed, so results are bit-reproducible.
@@ -291,8 +292,8 @@ int inkling_dense_mlp_forward(const inkling_dense_dims_t* dims, const void* x, c
  * Tensor pointers and workspace must be 16-byte aligned, offsets and row_index
  * 4-byte; the output and the workspace must not overlap each other or an operand
  * (INKLING_ERR_INVALID_ARGUMENT).  Same conventions and errors as
- * inkling_moe_forward otherwise; rows == 0 is a no-op for the first two and
- * writes zeros in weight_grad.
+ * inkling_moe_forward otherwise; rows == 0 is a no-op for the first two and writes
+ * zeros in weight_grad.
  */
 typedef struct {
     int64_t rows;          /* rows of out, dout, dx and row_index */

@@ -404,6 +404,77 @@ int inkling_norm_backward(const inkling_norm_dims_t* dims, const void* dout, con
                           const float* stats, void* dx, float* dweight, float* dbias, void* workspace,
                           size_t workspace_bytes, void* stream);
 
+/*
+ * Tokens sorted by expert, and back, for callers with a router of their own, or
+ * that put the parts above together themselves.
+ *
+ * inkling_expert_order sorts the slots t*top_k + i of the chosen experts by
+ * expert, and by slot within one:
+ *   topk_indices   [T][top_k] int32.  An expert may stand more than once in a
+ *                  token's row.  A value outside [0, n_routed) has no row (a
+ *                  dropped choice, or an expert of another GPU).
+ *   padding_mask   [T] uint8 (nonzero: the token's slots have no rows) or NULL
+ *   expert_counts  [n_routed] int32, or NULL
+ *   expert_offsets [n_routed + 1] int32
+ *   sorted_slots   [T * top_k] int32: the slot of each row, -1 behind the last
+ *                  row; or NULL
+ *   positions      [T][top_k] int32: the row of each slot, -1 where it has none
+ * (What inkling_moe_route gives for the same indices, and the inverse of its
+ * sorted_slots.)  T == 0 gives zero counts and offsets.
+ *
+ * With p = positions[t][i], for the slots whose p is in [0, rows) (the others
+ * have no part in anything), w = weights[t][i] or 1 where weights is NULL:
+ *   dispatch_forward   rows[p] = w * x[t]
+ *   dispatch_backward  dx[t] = sum_i w * drows[p]; dweights[t][i] = <x[t], drows[p]>
+ *   combine_forward    out[t] = addend[t] + sum_i w * rows[p]  (addend NULL: 0)
+ *   combine_backward   drows[p] = w * dout[t]; dweights[t][i] = <dout[t], rows[p]>
+ * (the addend's gradient is dout).  dweights may be NULL; then dispatch_backward's
+ * x and combine_backward's rows are not read and may be NULL.  combine_backward's
+ * drows may be NULL where dweights is wanted.  dweights of a slot without a row
+ * is 0.  Rows that no position names are left as they are: a row must not be
+ * named twice by what dispatch_forward and combine_backward write (one of the two
+ * is kept, in parts).  rows smaller than T * top_k drops what lies past it.
+ * x, dx, out, addend, dout [T][hidden] in token_dtype; rows, drows [rows][hidden]
+ * in rows_dtype; weights and dweights [T][top_k] fp32; sums in fp32, in the order
+ * of the slots (dweights: a fixed order), rounded once: bit-reproducible.
+ * Infinities and NaN propagate.  T == 0 is a no-op; rows == 0 gives zero dweights and dx and
+ * the addend as out.
+ * Limits (INKLING_ERR_UNSUPPORTED): 1 <= top_k <= 32, n_routed <= 512, T * top_k
+ * and rows <= 2^31 - 257, any hidden <= 2^20, T * (hidden / 256 + 1) < 2^25.
+ * Tensor pointers and workspace 16-byte aligned (int32, fp32 weights and the mask
+ * at their own alignment); outputs and workspace must not overlap each other or
+ * an operand (INKLING_ERR_INVALID_ARGUMENT).
+ */
+typedef struct {
+    int64_t T;
+    int32_t n_routed;
+    int32_t top_k;
+} inkling_order_dims_t;
+
+typedef struct {
+    int64_t T;
+    int64_t rows;
+    int32_t top_k;
+    int32_t hidden;
+    int32_t token_dtype; /* inkling_dtype_t of x, dx, out, addend, dout */
+    int32_t rows_dtype;  /* inkling_dtype_t of rows, drows               */
+} inkling_dispatch_dims_t;
+
+/* workspace of inkling_expert_order (0 for few slots: then it may be NULL) */
+int inkling_expert_order_workspace_size(const inkling_order_dims_t* dims, size_t* bytes);
+int inkling_expert_order(const inkling_order_dims_t* dims, const int32_t* topk_indices, const uint8_t* padding_mask,
+                         int32_t* expert_counts, int32_t* expert_offsets, int32_t* sorted_slots, int32_t* positions,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+int inkling_dispatch_forward(const inkling_dispatch_dims_t* dims, const void* x, const int32_t* positions,
+                             const float* weights, void* rows, void* stream);
+int inkling_dispatch_backward(const inkling_dispatch_dims_t* dims, const void* drows, const int32_t* positions,
+                              const float* weights, const void* x, void* dx, float* dweights, void* stream);
+int inkling_combine_forward(const inkling_dispatch_dims_t* dims, const void* rows, const int32_t* positions,
+                            const float* weights, const void* addend, void* out, void* stream);
+int inkling_combine_backward(const inkling_dispatch_dims_t* dims, const void* dout, const int32_t* positions,
+                             const float* weights, const void* rows, void* drows, float* dweights, void* stream);
+
 /* Stage timing (instrumentation for benchmarks).  When `events` is non-NULL,
  * each later inkling_moe_forward on the calling thread records, on its stream,
  * events[0] before the first launch and events[i] after stage i:

@@ -34,7 +34,9 @@ EXPORTED = ("inkling_moe_workspace_size", "inkling_moe_route", "inkling_moe_forw
             "inkling_grouped_workspace_size", "inkling_grouped_weight_grad_workspace_size",
             "inkling_grouped_linear", "inkling_grouped_input_grad", "inkling_grouped_weight_grad",
             "inkling_swiglu_checkpoint_size", "inkling_swiglu_forward", "inkling_swiglu_backward",
-            "inkling_norm_forward", "inkling_norm_backward_workspace_size", "inkling_norm_backward")
+            "inkling_norm_forward", "inkling_norm_backward_workspace_size", "inkling_norm_backward",
+            "inkling_expert_order_workspace_size", "inkling_expert_order", "inkling_dispatch_forward",
+            "inkling_dispatch_backward", "inkling_combine_forward", "inkling_combine_backward")
 INKLING_NORM_LAYER = 0
 INKLING_NORM_RMS = 1
 NORM_KINDS = {"layer": INKLING_NORM_LAYER, "rms": INKLING_NORM_RMS}
@@ -72,6 +74,15 @@ class SwigluDims(ctypes.Structure):
 class NormDims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int32), ("kind", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class OrderDims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("n_routed", ctypes.c_int32), ("top_k", ctypes.c_int32)]
+
+
+class DispatchDims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("rows", ctypes.c_int64), ("top_k", ctypes.c_int32),
+                ("hidden", ctypes.c_int32), ("token_dtype", ctypes.c_int32), ("rows_dtype", ctypes.c_int32)]
 
 
 class Gate(ctypes.Structure):
@@ -150,7 +161,8 @@ def load() -> ctypes.CDLL:
                                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.inkling_moe_forward_train.restype = ctypes.c_int
     ptr, size = ctypes.c_void_p, ctypes.c_size_t
-    gdims, sdims, ndims = (ctypes.POINTER(c) for c in (GroupedDims, SwigluDims, NormDims))
+    gdims, sdims, ndims, odims, ddims = (ctypes.POINTER(c) for c in (GroupedDims, SwigluDims, NormDims, OrderDims,
+                                                                     DispatchDims))
     for name, args in (
             ("inkling_grouped_workspace_size", [gdims, ctypes.POINTER(size)]),
             ("inkling_grouped_weight_grad_workspace_size", [gdims, ctypes.POINTER(size)]),
@@ -162,7 +174,13 @@ def load() -> ctypes.CDLL:
             ("inkling_swiglu_backward", [sdims, ptr, ptr, size, ptr, ptr, ptr, ptr, ptr, ptr]),
             ("inkling_norm_forward", [ndims, ptr, ptr, ptr, ptr, ptr, ptr]),
             ("inkling_norm_backward_workspace_size", [ndims, ctypes.POINTER(size)]),
-            ("inkling_norm_backward", [ndims, ptr, ptr, ptr, ptr, ptr, ptr, ptr, ptr, size, ptr])):
+            ("inkling_norm_backward", [ndims, ptr, ptr, ptr, ptr, ptr, ptr, ptr, ptr, size, ptr]),
+            ("inkling_expert_order_workspace_size", [odims, ctypes.POINTER(size)]),
+            ("inkling_expert_order", [odims, ptr, ptr, ptr, ptr, ptr, ptr, ptr, size, ptr]),
+            ("inkling_dispatch_forward", [ddims, ptr, ptr, ptr, ptr, ptr]),
+            ("inkling_dispatch_backward", [ddims, ptr, ptr, ptr, ptr, ptr, ptr, ptr]),
+            ("inkling_combine_forward", [ddims, ptr, ptr, ptr, ptr, ptr, ptr]),
+            ("inkling_combine_backward", [ddims, ptr, ptr, ptr, ptr, ptr, ptr, ptr])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = ctypes.c_int
     _LIB = lib
@@ -829,3 +847,171 @@ def norm_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, sta
     _call(dev, "inkling_norm_backward", dims, dout.data_ptr(), x.data_ptr(), weight.data_ptr(),
           stats.data_ptr(), dx.data_ptr(), dweight.data_ptr(), _ptr(dbias), _ptr(ws), 0 if ws is None else ws.numel())
     return {"dx": dx, "dweight": dweight, "dbias": dbias}
+
+
+# ---- tokens sorted by expert, and back ----------------------------------------------
+
+
+def make_order_dims(T, n_routed, top_k) -> OrderDims:
+    return OrderDims(int(T), *_ints32(n_routed, top_k))
+
+
+def expert_order_workspace_size(dims: OrderDims) -> int:
+    """inkling_expert_order_workspace_size."""
+    n = ctypes.c_size_t(0)
+    _check(load().inkling_expert_order_workspace_size(ctypes.byref(dims), ctypes.byref(n)),
+           "inkling_expert_order_workspace_size")
+    return int(n.value)
+
+
+@functools.lru_cache(maxsize=1024)
+def _order_plan(*sizes):
+    dims = make_order_dims(*sizes)
+    return ctypes.byref(dims), expert_order_workspace_size(dims)
+
+
+def expert_order(topk_indices: torch.Tensor, n_routed: int, padding_mask: Optional[torch.Tensor] = None,
+                 expert_counts: Optional[torch.Tensor] = None, expert_offsets: Optional[torch.Tensor] = None,
+                 sorted_slots: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> dict:
+    """inkling_expert_order: dict(expert_counts [E], expert_offsets [E + 1],
+    sorted_slots [T * k], positions [T, k]), all int32, of topk_indices [T, k]
+    int32: the slots t * k + i sorted by expert (ascending within one; -1 behind
+    the last row) and the row of each slot (-1: a padded token's, or an expert
+    outside [0, n_routed))."""
+    if topk_indices.dim() != 2:
+        raise ValueError("topk_indices must be [T, top_k]")
+    dev = topk_indices.device
+    _operand(topk_indices, "topk_indices", torch.int32, dev)
+    T, k = topk_indices.shape
+    if padding_mask is not None:
+        _operand(padding_mask, "padding_mask", torch.uint8, dev)
+        if padding_mask.dim() != 1 or padding_mask.shape[0] != T:
+            raise ValueError("padding_mask must hold a value for each token")
+    dims, need = _order_plan(T, n_routed, k)
+    i32 = torch.int32
+    res = {"expert_counts": _result(expert_counts, "expert_counts", (n_routed,), i32, dev),
+           "expert_offsets": _result(expert_offsets, "expert_offsets", (n_routed + 1,), i32, dev),
+           "sorted_slots": _result(sorted_slots, "sorted_slots", (T * k,), i32, dev),
+           "positions": _result(positions, "positions", (T, k), i32, dev, like=topk_indices)}
+    ws = _scratch(workspace, need, dev)
+    _call(dev, "inkling_expert_order", dims, topk_indices.data_ptr(), _ptr(padding_mask),
+          res["expert_counts"].data_ptr(), res["expert_offsets"].data_ptr(), res["sorted_slots"].data_ptr(),
+          res["positions"].data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
+    return res
+
+
+def make_dispatch_dims(T, rows, top_k, hidden, token_dtype, rows_dtype) -> DispatchDims:
+    codes = [d if isinstance(d, int) else _dtype_code(d) for d in (token_dtype, rows_dtype)]
+    return DispatchDims(int(T), int(rows), *_ints32(top_k, hidden), *codes)
+
+
+@functools.lru_cache(maxsize=1024)
+def _dispatch_plan(*sizes):
+    return ctypes.byref(make_dispatch_dims(*sizes))
+
+
+def _dispatch_checks(name, src, positions, weights):
+    """Checks shared by the four row operators; returns (T, k, H, device)."""
+    if src.dim() != 2:
+        raise ValueError(f"{name} must be two-dimensional")
+    dev = src.device
+    _operand(src, name, src.dtype, dev)
+    _operand(positions, "positions", torch.int32, dev)
+    if positions.dim() != 2:
+        raise ValueError("positions must be [T, top_k]")
+    if weights is not None:
+        _operand(weights, "weights", torch.float32, dev)
+        if weights.shape != positions.shape:
+            raise ValueError("weights must have the shape of positions")
+    T, k = positions.shape
+    return T, k, src.shape[1], dev
+
+
+def _rows_of(t, name, T, H):
+    if t.dim() != 2 or t.shape[1] != H or (T is not None and t.shape[0] != T):
+        raise ValueError(f"{name} must be [{'rows' if T is None else T}, {H}], got {list(t.shape)}")
+
+
+def dispatch_forward(x: torch.Tensor, positions: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                     rows: Optional[torch.Tensor] = None, rows_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """inkling_dispatch_forward: rows[positions[t, i]] = (weights[t, i]) x[t],
+    [T * k, H] (or as many rows as the given `rows` has; positions outside them
+    are dropped).  Rows that no position names are left as they are (in `rows`
+    made here: unset)."""
+    T, k, H, dev = _dispatch_checks("x", x, positions, weights)
+    _rows_of(x, "x", T, H)
+    rdt = _result_dtype("rows", rows, rows_dtype, x.dtype)
+    if rows is None:
+        rows = torch.empty((T * k, H), dtype=rdt, device=dev)
+    else:
+        _operand(rows, "rows", rdt, dev)
+        _rows_of(rows, "rows", None, H)
+    _call(dev, "inkling_dispatch_forward", _dispatch_plan(T, rows.shape[0], k, H, x.dtype, rdt), x.data_ptr(),
+          positions.data_ptr(), _ptr(weights), rows.data_ptr())
+    return rows
+
+
+def dispatch_backward(drows: torch.Tensor, positions: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                      x: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                      dx_dtype: Optional[torch.dtype] = None, dweights: Optional[torch.Tensor] = None) -> dict:
+    """inkling_dispatch_backward: dict(dx [T, H], dweights [T, k]) of
+    dispatch_forward from its rows' gradient; dweights is None unless x is given
+    (the forward's, of dx's dtype)."""
+    T, k, H, dev = _dispatch_checks("drows", drows, positions, weights)
+    tdt = _result_dtype("dx", dx, dx_dtype, drows.dtype if x is None else x.dtype)
+    if x is not None:
+        _operand(x, "x", tdt, dev)
+        _rows_of(x, "x", T, H)
+    elif dweights is not None:
+        raise ValueError("dweights needs x")
+    dx = _result(dx, "dx", (T, H), tdt, dev)
+    if x is not None:
+        dweights = _result(dweights, "dweights", (T, k), torch.float32, dev)
+    _call(dev, "inkling_dispatch_backward", _dispatch_plan(T, drows.shape[0], k, H, tdt, drows.dtype),
+          drows.data_ptr(), positions.data_ptr(), _ptr(weights), _ptr(x), dx.data_ptr(), _ptr(dweights))
+    return {"dx": dx, "dweights": dweights}
+
+
+def combine_forward(rows: torch.Tensor, positions: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                    addend: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """inkling_combine_forward: out[t] = addend[t] + sum_i (weights[t, i])
+    rows[positions[t, i]], [T, H]; the addend (shared experts, a residual) has
+    out's dtype, which is otherwise rows'."""
+    T, k, H, dev = _dispatch_checks("rows", rows, positions, weights)
+    odt = _result_dtype("out", out, out_dtype, rows.dtype if addend is None else addend.dtype)
+    if addend is not None:
+        _operand(addend, "addend", odt, dev)
+        _rows_of(addend, "addend", T, H)
+    out = _result(out, "out", (T, H), odt, dev, like=addend)
+    _call(dev, "inkling_combine_forward", _dispatch_plan(T, rows.shape[0], k, H, odt, rows.dtype), rows.data_ptr(),
+          positions.data_ptr(), _ptr(weights), _ptr(addend), out.data_ptr())
+    return out
+
+
+def combine_backward(dout: torch.Tensor, positions: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                     weights: Optional[torch.Tensor] = None, drows: Optional[torch.Tensor] = None,
+                     rows_dtype: Optional[torch.dtype] = None, dweights: Optional[torch.Tensor] = None) -> dict:
+    """inkling_combine_backward: dict(drows [rows, H], dweights [T, k]) of
+    combine_forward from dout (which is also the addend's gradient); dweights is
+    None unless rows (the forward's) is given.  Rows that no position names are
+    left as they are (in `drows` made here: unset)."""
+    T, k, H, dev = _dispatch_checks("dout", dout, positions, weights)
+    _rows_of(dout, "dout", T, H)
+    rdt = _result_dtype("drows", drows, rows_dtype, dout.dtype if rows is None else rows.dtype)
+    n = T * k
+    if rows is not None:
+        _operand(rows, "rows", rdt, dev)
+        _rows_of(rows, "rows", None, H)
+        n = rows.shape[0]
+    elif dweights is not None:
+        raise ValueError("dweights needs rows")
+    if drows is not None and rows is None:
+        n = drows.shape[0] if drows.dim() == 2 else n
+    drows = _result(drows, "drows", (n, H), rdt, dev, like=rows)
+    if rows is not None:
+        dweights = _result(dweights, "dweights", (T, k), torch.float32, dev)
+    _call(dev, "inkling_combine_backward", _dispatch_plan(T, n, k, H, dout.dtype, rdt), dout.data_ptr(),
+          positions.data_ptr(), _ptr(weights), _ptr(rows), drows.data_ptr(), _ptr(dweights))
+    return {"drows": drows, "dweights": dweights}

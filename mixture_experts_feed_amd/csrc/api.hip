@@ -1083,6 +1083,149 @@ int inkling_norm_backward(const inkling_norm_dims_t* dims, const void* dout, con
     return INKLING_OK;
 }
 
+}  // extern "C"
+
+// ---- tokens sorted by expert, and back ---------------------------------------------
+namespace {
+
+int check_order_dims(const inkling_order_dims_t* d) {
+    if (d == nullptr || d->T < 0 || d->n_routed <= 0 || d->top_k <= 0) return INKLING_ERR_INVALID_ARGUMENT;
+    if (d->n_routed > 512 || d->top_k > 32 || d->T > INT32_MAX || d->T * (int64_t)d->top_k > INT32_MAX - 256)
+        return INKLING_ERR_UNSUPPORTED;
+    return INKLING_OK;
+}
+
+size_t order_workspace(const inkling_order_dims_t* d) {
+    return (size_t)order_hist_ints(d->T * d->top_k, d->n_routed) * 4;
+}
+
+int check_dispatch_dims(const inkling_dispatch_dims_t* d) {
+    if (d == nullptr || d->T < 0 || d->rows < 0 || d->top_k <= 0 || d->hidden <= 0)
+        return INKLING_ERR_INVALID_ARGUMENT;
+    for (const int32_t t : {d->token_dtype, d->rows_dtype})
+        if (t != INKLING_F32 && t != INKLING_BF16) return INKLING_ERR_UNSUPPORTED;
+    if (d->top_k > 32 || d->hidden > (1 << 20) || d->T > INT32_MAX || d->T * (int64_t)d->top_k > INT32_MAX - 256 ||
+        d->rows > INT32_MAX - 256 || !move_fits(d->T, d->hidden))
+        return INKLING_ERR_UNSUPPORTED;
+    return INKLING_OK;
+}
+
+// One of the four row operators.  token_in and rows_in may be NULL where the
+// operator does not need them (checked by the callers).
+int dispatch_call(const inkling_dispatch_dims_t* d, bool spread, const int32_t* positions, const float* weights,
+                  const void* token_in, const void* rows_in, void* token_out, void* rows_out, float* dweights,
+                  void* stream) {
+    if (positions == nullptr || !aligned(positions, 4) || !aligned(weights, 4) || !aligned(dweights, 4) ||
+        !aligned(token_in, 16) || !aligned(rows_in, 16) || !aligned(token_out, 16) || !aligned(rows_out, 16))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    const size_t slots = (size_t)d->T * d->top_k * 4;
+    const size_t tokens = (size_t)d->T * d->hidden * value_bytes(d->token_dtype);
+    const size_t rows = (size_t)d->rows * d->hidden * value_bytes(d->rows_dtype);
+    if (writes_overlap({{token_out, tokens}, {rows_out, rows}, {dweights, slots}},
+                       {{token_in, tokens}, {rows_in, rows}, {positions, slots}, {weights, slots}}))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    RowMoveParams p = {};
+    p.token_dtype = d->token_dtype == INKLING_BF16 ? 1 : 0;
+    p.rows_dtype = d->rows_dtype == INKLING_BF16 ? 1 : 0;
+    p.T = d->T;
+    p.rows = d->rows;
+    p.k = d->top_k;
+    p.H = d->hidden;
+    p.positions = positions;
+    p.weights = weights;
+    p.token_in = token_in;
+    p.rows_in = rows_in;
+    p.token_out = token_out;
+    p.rows_out = rows_out;
+    p.dweights = dweights;
+    HIP_TRY(launch_rows(p, spread, (hipStream_t)stream));
+    return INKLING_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int inkling_expert_order_workspace_size(const inkling_order_dims_t* dims, size_t* bytes) {
+    const int rc = check_order_dims(dims);
+    if (rc != INKLING_OK) return rc;
+    if (bytes == nullptr) return INKLING_ERR_INVALID_ARGUMENT;
+    *bytes = order_workspace(dims);
+    return INKLING_OK;
+}
+
+int inkling_expert_order(const inkling_order_dims_t* dims, const int32_t* topk_indices, const uint8_t* padding_mask,
+                         int32_t* expert_counts, int32_t* expert_offsets, int32_t* sorted_slots, int32_t* positions,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+    const int rc = check_order_dims(dims);
+    if (rc != INKLING_OK) return rc;
+    if (expert_offsets == nullptr || (dims->T > 0 && (topk_indices == nullptr || positions == nullptr)))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (!aligned(topk_indices, 4) || !aligned(expert_counts, 4) || !aligned(expert_offsets, 4) ||
+        !aligned(sorted_slots, 4) || !aligned(positions, 4) || !aligned(workspace, 16))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    const size_t need = order_workspace(dims);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return INKLING_ERR_WORKSPACE;
+    const long long slots = dims->T * dims->top_k;
+    const size_t bytes = (size_t)slots * 4;
+    if (writes_overlap({{expert_counts, (size_t)dims->n_routed * 4},
+                        {expert_offsets, ((size_t)dims->n_routed + 1) * 4},
+                        {sorted_slots, bytes},
+                        {positions, bytes},
+                        {workspace, need}},
+                       {{topk_indices, bytes}, {padding_mask, (size_t)dims->T}}))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    HIP_TRY(launch_expert_order(topk_indices, padding_mask, slots, dims->n_routed, dims->top_k,
+                                static_cast<int32_t*>(workspace), expert_counts, expert_offsets, sorted_slots,
+                                positions, (hipStream_t)stream));
+    return INKLING_OK;
+}
+
+int inkling_dispatch_forward(const inkling_dispatch_dims_t* dims, const void* x, const int32_t* positions,
+                             const float* weights, void* rows, void* stream) {
+    const int rc = check_dispatch_dims(dims);
+    if (rc != INKLING_OK) return rc;
+    if (dims->T == 0 || dims->rows == 0) return INKLING_OK;
+    if (x == nullptr || rows == nullptr) return INKLING_ERR_INVALID_ARGUMENT;
+    return dispatch_call(dims, true, positions, weights, x, nullptr, nullptr, rows, nullptr, stream);
+}
+
+int inkling_dispatch_backward(const inkling_dispatch_dims_t* dims, const void* drows, const int32_t* positions,
+                              const float* weights, const void* x, void* dx, float* dweights, void* stream) {
+    const int rc = check_dispatch_dims(dims);
+    if (rc != INKLING_OK) return rc;
+    if (dims->T == 0) return INKLING_OK;
+    if (dx == nullptr || (dims->rows > 0 && drows == nullptr) || (dweights != nullptr && x == nullptr))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    return dispatch_call(dims, false, positions, weights, dweights != nullptr ? x : nullptr, drows, dx, nullptr,
+                         dweights, stream);
+}
+
+int inkling_combine_forward(const inkling_dispatch_dims_t* dims, const void* rows, const int32_t* positions,
+                            const float* weights, const void* addend, void* out, void* stream) {
+    const int rc = check_dispatch_dims(dims);
+    if (rc != INKLING_OK) return rc;
+    if (dims->T == 0) return INKLING_OK;
+    if (out == nullptr || (dims->rows > 0 && rows == nullptr)) return INKLING_ERR_INVALID_ARGUMENT;
+    return dispatch_call(dims, false, positions, weights, addend, rows, out, nullptr, nullptr, stream);
+}
+
+int inkling_combine_backward(const inkling_dispatch_dims_t* dims, const void* dout, const int32_t* positions,
+                             const float* weights, const void* rows, void* drows, float* dweights, void* stream) {
+    const int rc = check_dispatch_dims(dims);
+    if (rc != INKLING_OK) return rc;
+    if (dims->T == 0 || (dims->rows == 0 && dweights == nullptr)) return INKLING_OK;
+    if (dout == nullptr || (drows == nullptr && dweights == nullptr) ||
+        (dims->rows > 0 && dweights != nullptr && rows == nullptr))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    return dispatch_call(dims, true, positions, weights, dout, dweights != nullptr ? rows : nullptr, nullptr, drows,
+                         dweights, stream);
+}
+
+}  // extern "C"
+
+extern "C" {
+
 const char* inkling_moe_strerror(int code) {
     switch (code) {
         case INKLING_OK: return "success";

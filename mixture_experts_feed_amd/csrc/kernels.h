@@ -241,6 +241,30 @@ int norm_parts(int dtype, int rows, int H);
 hipError_t launch_norm_forward(const NormParams& p, hipStream_t stream);
 hipError_t launch_norm_backward(const NormParams& p, hipStream_t stream);
 
+// ---- tokens sorted by expert, and back (dispatch.hip) ---------------------------
+// ints of `hist` (0: not needed)
+long long order_hist_ints(long long slots, int E);
+// pad, counts and sorted may be NULL; slots = T * k, also 0
+hipError_t launch_expert_order(const int32_t* topk, const uint8_t* pad, long long slots, int E, int k, int32_t* hist,
+                               int32_t* counts, int32_t* offsets, int32_t* sorted, int32_t* positions,
+                               hipStream_t stream);
+struct RowMoveParams {
+    int token_dtype, rows_dtype;   // 0 f32, 1 bf16
+    long long T, rows;
+    int k, H;                      // k at most 32
+    const int32_t* positions;      // [T][k]
+    const float* weights;          // [T][k] or NULL for 1
+    const void* token_in;          // [T][H]; spread and weights' gradient: x; gather without one: added first, or NULL
+    const void* rows_in;           // [rows][H] (gather, weights' gradient)
+    void* token_out;               // gather: [T][H]
+    void* rows_out;                // spread: [rows][H] (NULL: weights' gradient only)
+    float* dweights;               // [T][k] or NULL
+};
+bool move_fits(long long T, int H);
+// spread: rows_out[p] = w token_in[t]; otherwise token_out[t] = token_in[t] + sum w
+// rows_in[p]; dweights = <token_in[t], rows_in[p]> in the same launch
+hipError_t launch_rows(const RowMoveParams& p, bool spread, hipStream_t stream);
+
 // gamma[t] = value for t < T; the GEMM round counters zeroed (the dense MLP's
 // stand-in for the router and the permutation)
 hipError_t launch_dense_prep(float* gamma, int T, float value, int32_t* round_counters, hipStream_t stream);

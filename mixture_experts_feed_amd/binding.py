@@ -36,7 +36,9 @@ EXPORTED = ("inkling_moe_workspace_size", "inkling_moe_route", "inkling_moe_forw
             "inkling_swiglu_checkpoint_size", "inkling_swiglu_forward", "inkling_swiglu_backward",
             "inkling_norm_forward", "inkling_norm_backward_workspace_size", "inkling_norm_backward",
             "inkling_expert_order_workspace_size", "inkling_expert_order", "inkling_dispatch_forward",
-            "inkling_dispatch_backward", "inkling_combine_forward", "inkling_combine_backward")
+            "inkling_dispatch_backward", "inkling_combine_forward", "inkling_combine_backward",
+            "inkling_fp8_quantize_rows", "inkling_fp8_quantize_weight", "inkling_fp8_grouped_linear",
+            "inkling_fp8_grouped_input_grad")
 INKLING_NORM_LAYER = 0
 INKLING_NORM_RMS = 1
 NORM_KINDS = {"layer": INKLING_NORM_LAYER, "rms": INKLING_NORM_RMS}
@@ -83,6 +85,15 @@ class OrderDims(ctypes.Structure):
 class DispatchDims(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("rows", ctypes.c_int64), ("top_k", ctypes.c_int32),
                 ("hidden", ctypes.c_int32), ("token_dtype", ctypes.c_int32), ("rows_dtype", ctypes.c_int32)]
+
+
+class QuantDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class Fp8Dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("x_rows", ctypes.c_int64), ("n_groups", ctypes.c_int32),
+                ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
 class Gate(ctypes.Structure):
@@ -161,8 +172,8 @@ def load() -> ctypes.CDLL:
                                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.inkling_moe_forward_train.restype = ctypes.c_int
     ptr, size = ctypes.c_void_p, ctypes.c_size_t
-    gdims, sdims, ndims, odims, ddims = (ctypes.POINTER(c) for c in (GroupedDims, SwigluDims, NormDims, OrderDims,
-                                                                     DispatchDims))
+    gdims, sdims, ndims, odims, ddims, qdims, fdims = (
+        ctypes.POINTER(c) for c in (GroupedDims, SwigluDims, NormDims, OrderDims, DispatchDims, QuantDims, Fp8Dims))
     for name, args in (
             ("inkling_grouped_workspace_size", [gdims, ctypes.POINTER(size)]),
             ("inkling_grouped_weight_grad_workspace_size", [gdims, ctypes.POINTER(size)]),
@@ -180,7 +191,11 @@ def load() -> ctypes.CDLL:
             ("inkling_dispatch_forward", [ddims, ptr, ptr, ptr, ptr, ptr]),
             ("inkling_dispatch_backward", [ddims, ptr, ptr, ptr, ptr, ptr, ptr, ptr]),
             ("inkling_combine_forward", [ddims, ptr, ptr, ptr, ptr, ptr, ptr]),
-            ("inkling_combine_backward", [ddims, ptr, ptr, ptr, ptr, ptr, ptr, ptr])):
+            ("inkling_combine_backward", [ddims, ptr, ptr, ptr, ptr, ptr, ptr, ptr]),
+            ("inkling_fp8_quantize_rows", [qdims, ptr, ptr, ptr, ptr, ptr]),
+            ("inkling_fp8_quantize_weight", [fdims, ptr, ptr, ptr, ptr]),
+            ("inkling_fp8_grouped_linear", [fdims, ptr, ptr, ptr, ptr, ptr, ptr, ptr, ptr]),
+            ("inkling_fp8_grouped_input_grad", [fdims, ptr, ptr, ptr, ptr, ptr, ptr, ptr])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = ctypes.c_int
     _LIB = lib
@@ -1015,3 +1030,130 @@ def combine_backward(dout: torch.Tensor, positions: torch.Tensor, rows: Optional
     _call(dev, "inkling_combine_backward", _dispatch_plan(T, n, k, H, dout.dtype, rdt), dout.data_ptr(),
           positions.data_ptr(), _ptr(weights), _ptr(rows), drows.data_ptr(), _ptr(dweights))
     return {"drows": drows, "dweights": dweights}
+
+
+# ---- 8-bit floating point with a scale for each block of 128 ----------------------------
+
+E4M3 = torch.float8_e4m3fn
+QBLOCK = 128
+
+
+def _blocks(n: int) -> int:
+    return (n + QBLOCK - 1) // QBLOCK
+
+
+def make_quant_dims(rows, cols, dtype) -> QuantDims:
+    return QuantDims(int(rows), *_ints32(cols), dtype if isinstance(dtype, int) else _dtype_code(dtype))
+
+
+def make_fp8_dims(rows, x_rows, n_groups, in_features, out_features, out_dtype) -> Fp8Dims:
+    return Fp8Dims(int(rows), int(x_rows), *_ints32(n_groups, in_features, out_features),
+                   out_dtype if isinstance(out_dtype, int) else _dtype_code(out_dtype))
+
+
+@functools.lru_cache(maxsize=1024)
+def _quant_plan(*sizes):
+    return ctypes.byref(make_quant_dims(*sizes))
+
+
+@functools.lru_cache(maxsize=1024)
+def _fp8_plan(*sizes):
+    return ctypes.byref(make_fp8_dims(*sizes))
+
+
+def fp8_quantize_rows(x: torch.Tensor, row_count: Optional[torch.Tensor] = None,
+                      values: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+    """inkling_fp8_quantize_rows: (values [rows, cols] float8_e4m3fn, scales
+    [rows, ceil(cols / 128)] fp32, powers of two) of x [rows, cols].  Rows from
+    row_count[0] on are left as they are."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, cols]")
+    dev = x.device
+    _operand(x, "x", x.dtype, dev)
+    R, C = x.shape
+    if row_count is not None:
+        _operand(row_count, "row_count", torch.int32, dev)
+        if row_count.numel() != 1:
+            raise ValueError("row_count must hold one value")
+    dims = _quant_plan(R, C, x.dtype)
+    values = _result(values, "values", (R, C), E4M3, dev)
+    scales = _result(scales, "scales", (R, _blocks(C)), torch.float32, dev)
+    _call(dev, "inkling_fp8_quantize_rows", dims, x.data_ptr(), _ptr(row_count), values.data_ptr(), scales.data_ptr())
+    return values, scales
+
+
+def fp8_quantize_weight(weight: torch.Tensor, values: Optional[torch.Tensor] = None,
+                        scales: Optional[torch.Tensor] = None):
+    """inkling_fp8_quantize_weight: (values [E, N, K] float8_e4m3fn, scales
+    [E, ceil(N / 128), ceil(K / 128)] fp32, powers of two) of weight [E, N, K]."""
+    if weight.dim() != 3:
+        raise ValueError("weight must be [n_groups, out_features, in_features]")
+    dev = weight.device
+    _operand(weight, "weight", weight.dtype, dev)
+    E, N, K = weight.shape
+    dims = _fp8_plan(0, 0, E, K, N, weight.dtype)
+    values = _result(values, "values", (E, N, K), E4M3, dev)
+    scales = _result(scales, "scales", (E, _blocks(N), _blocks(K)), torch.float32, dev)
+    _call(dev, "inkling_fp8_quantize_weight", dims, weight.data_ptr(), values.data_ptr(), scales.data_ptr())
+    return values, scales
+
+
+def _fp8_checks(name, src, src_scales, weight, weight_scales, offsets, axis, row_index):
+    """Checks shared by the two products, whose rows are as wide as weight's
+    `axis`; returns (rows, E, N, K, device)."""
+    if src.dim() != 2 or weight.dim() != 3:
+        raise ValueError(f"{name} must be [rows, features] and weight [n_groups, out_features, in_features]")
+    dev = src.device
+    _operand(src, name, E4M3, dev)
+    _operand(weight, "weight", E4M3, dev)
+    _operand(src_scales, f"{name}_scales", torch.float32, dev)
+    _operand(weight_scales, "weight_scales", torch.float32, dev)
+    E, N, K = weight.shape
+    R, have = src.shape
+    if have != weight.shape[axis]:
+        raise ValueError(f"{name} must have {weight.shape[axis]} columns, got {have}")
+    if src_scales.shape != (R, _blocks(have)):
+        raise ValueError(f"{name}_scales must have shape {(R, _blocks(have))}, got {tuple(src_scales.shape)}")
+    if weight_scales.shape != (E, _blocks(N), _blocks(K)):
+        raise ValueError(f"weight_scales must have shape {(E, _blocks(N), _blocks(K))}, "
+                         f"got {tuple(weight_scales.shape)}")
+    if offsets is not None:
+        _grouped_plan_checks(offsets, E, row_index, dev)
+    elif E != 1:
+        raise ValueError("more than one group needs offsets")
+    elif row_index is not None:
+        _operand(row_index, "row_index", torch.int32, dev)
+        if row_index.dim() != 1:
+            raise ValueError("row_index must be one-dimensional")
+    return (R if row_index is None else row_index.shape[0]), E, N, K, dev
+
+
+def fp8_grouped_linear(x: torch.Tensor, x_scales: torch.Tensor, weight: torch.Tensor, weight_scales: torch.Tensor,
+                       offsets: Optional[torch.Tensor], row_index: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """inkling_fp8_grouped_linear: grouped_linear on float8_e4m3fn x [rows, K]
+    and weight [E, N, K] with fp32 scales [rows, ceil(K / 128)] and [E, ceil(N /
+    128), ceil(K / 128)]; out [rows, N] in bf16 (default) or fp32.  offsets may be
+    None for one group (a dense product of all rows)."""
+    R, E, N, K, dev = _fp8_checks("x", x, x_scales, weight, weight_scales, offsets, 2, row_index)
+    odt = _result_dtype("out", out, out_dtype, torch.bfloat16)
+    dims = _fp8_plan(R, x.shape[0], E, K, N, odt)
+    out = _result(out, "out", (R, N), odt, dev)
+    _call(dev, "inkling_fp8_grouped_linear", dims, x.data_ptr(), x_scales.data_ptr(), _ptr(row_index),
+          weight.data_ptr(), weight_scales.data_ptr(), _ptr(offsets), out.data_ptr())
+    return out
+
+
+def fp8_grouped_input_grad(dout: torch.Tensor, dout_scales: torch.Tensor, weight: torch.Tensor,
+                           weight_scales: torch.Tensor, offsets: Optional[torch.Tensor],
+                           dx: Optional[torch.Tensor] = None, dx_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """inkling_fp8_grouped_input_grad: dx [rows, K] in bf16 (default) or fp32 from
+    float8_e4m3fn dout [rows, N] with scales [rows, ceil(N / 128)] and the weights
+    and scales of fp8_grouped_linear."""
+    R, E, N, K, dev = _fp8_checks("dout", dout, dout_scales, weight, weight_scales, offsets, 1, None)
+    odt = _result_dtype("dx", dx, dx_dtype, torch.bfloat16)
+    dims = _fp8_plan(R, R, E, K, N, odt)
+    dx = _result(dx, "dx", (R, K), odt, dev)
+    _call(dev, "inkling_fp8_grouped_input_grad", dims, dout.data_ptr(), dout_scales.data_ptr(), weight.data_ptr(),
+          weight_scales.data_ptr(), _ptr(offsets), dx.data_ptr())
+    return dx

@@ -1224,6 +1224,123 @@ int inkling_combine_backward(const inkling_dispatch_dims_t* dims, const void* do
 
 }  // extern "C"
 
+// ---- 8-bit floating point with a scale for each block of 128 -------------------------
+namespace {
+
+long long blocks128(long long n) { return (n + 127) / 128; }
+
+int check_fp8_dims(const inkling_fp8_dims_t* d, bool products) {
+    if (d == nullptr || d->n_groups <= 0 || d->in_features <= 0 || d->out_features <= 0)
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (products && (d->rows < 0 || d->x_rows < 0)) return INKLING_ERR_INVALID_ARGUMENT;
+    if (d->out_dtype != INKLING_F32 && d->out_dtype != INKLING_BF16) return INKLING_ERR_UNSUPPORTED;
+    if (d->in_features % 16 != 0 || d->out_features % 16 != 0 || d->in_features > (1 << 20) ||
+        d->out_features > (1 << 20) || d->n_groups > 512)
+        return INKLING_ERR_UNSUPPORTED;
+    if (products && (d->rows > INT32_MAX - 256 || d->x_rows > INT32_MAX - 256)) return INKLING_ERR_UNSUPPORTED;
+    return INKLING_OK;
+}
+
+size_t weight_scale_bytes(const inkling_fp8_dims_t* d) {
+    return (size_t)d->n_groups * blocks128(d->out_features) * blocks128(d->in_features) * 4;
+}
+
+int fp8_product(const inkling_fp8_dims_t* d, bool input_grad, const void* x, const float* x_scales,
+                const int32_t* row_index, const void* weight, const float* weight_scales, const int32_t* offsets,
+                void* out, void* stream) {
+    const int rc = check_fp8_dims(d, true);
+    if (rc != INKLING_OK) return rc;
+    if (d->rows == 0) return INKLING_OK;
+    if (x == nullptr || x_scales == nullptr || weight == nullptr || weight_scales == nullptr || out == nullptr ||
+        (offsets == nullptr && d->n_groups != 1))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (!input_grad && (row_index == nullptr ? d->x_rows != d->rows : d->x_rows == 0))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(out, 16) || !aligned(x_scales, 4) ||
+        !aligned(weight_scales, 4) || !aligned(offsets, 4) || !aligned(row_index, 4))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    const int len = input_grad ? d->out_features : d->in_features, cols = input_grad ? d->in_features : d->out_features;
+    Fp8Params p = {};
+    p.weight = weight;
+    p.weight_scale = weight_scales;
+    p.x = x;
+    p.x_scale = x_scales;
+    p.row_index = row_index;
+    p.offsets = offsets;
+    p.out = out;
+    p.rows = (int)d->rows;
+    p.x_rows = input_grad ? (int)d->rows : (int)d->x_rows;
+    p.E = d->n_groups;
+    p.N = d->out_features;
+    p.K = d->in_features;
+    p.out_bf16 = d->out_dtype == INKLING_BF16 ? 1 : 0;
+    p.input_grad = input_grad;
+    if (!fp8_product_fits(p)) return INKLING_ERR_UNSUPPORTED;
+    const size_t rows = (size_t)d->rows, x_rows = (size_t)p.x_rows;
+    if (writes_overlap({{out, rows * cols * value_bytes(d->out_dtype)}},
+                       {{x, x_rows * len},
+                        {x_scales, x_rows * blocks128(len) * 4},
+                        {weight, (size_t)d->n_groups * d->out_features * d->in_features},
+                        {weight_scales, weight_scale_bytes(d)},
+                        {offsets, ((size_t)d->n_groups + 1) * 4},
+                        {row_index, rows * 4}}))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    HIP_TRY(launch_fp8_product(p, (hipStream_t)stream));
+    return INKLING_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int inkling_fp8_quantize_rows(const inkling_quant_dims_t* dims, const void* x, const int32_t* row_count,
+                              void* values, float* scales, void* stream) {
+    if (dims == nullptr || dims->rows < 0 || dims->cols <= 0) return INKLING_ERR_INVALID_ARGUMENT;
+    if (dims->dtype != INKLING_F32 && dims->dtype != INKLING_BF16) return INKLING_ERR_UNSUPPORTED;
+    if (dims->cols % 16 != 0 || dims->cols > (1 << 20) || dims->rows > INT32_MAX - 256 ||
+        dims->rows * blocks128(dims->cols) > INT32_MAX)
+        return INKLING_ERR_UNSUPPORTED;
+    if (dims->rows == 0) return INKLING_OK;
+    if (x == nullptr || values == nullptr || scales == nullptr) return INKLING_ERR_INVALID_ARGUMENT;
+    if (!aligned(x, 16) || !aligned(values, 16) || !aligned(scales, 4) || !aligned(row_count, 4))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    const size_t n = (size_t)dims->rows * dims->cols;
+    if (writes_overlap({{values, n}, {scales, (size_t)dims->rows * blocks128(dims->cols) * 4}},
+                       {{x, n * value_bytes(dims->dtype)}, {row_count, 4}}))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    HIP_TRY(launch_quantize_rows(dims->dtype == INKLING_BF16 ? 1 : 0, x, row_count, (int)dims->rows, dims->cols, values,
+                                 scales, (hipStream_t)stream));
+    return INKLING_OK;
+}
+
+int inkling_fp8_quantize_weight(const inkling_fp8_dims_t* dims, const void* weight, void* values, float* scales,
+                                void* stream) {
+    const int rc = check_fp8_dims(dims, false);
+    if (rc != INKLING_OK) return rc;
+    if (weight == nullptr || values == nullptr || scales == nullptr) return INKLING_ERR_INVALID_ARGUMENT;
+    if (!aligned(weight, 16) || !aligned(values, 16) || !aligned(scales, 4)) return INKLING_ERR_INVALID_ARGUMENT;
+    const size_t n = (size_t)dims->n_groups * dims->out_features * dims->in_features;
+    if (writes_overlap({{values, n}, {scales, weight_scale_bytes(dims)}}, {{weight, n * value_bytes(dims->out_dtype)}}))
+        return INKLING_ERR_INVALID_ARGUMENT;
+    HIP_TRY(launch_quantize_weight(dims->out_dtype == INKLING_BF16 ? 1 : 0, weight, dims->n_groups, dims->out_features,
+                                   dims->in_features, values, scales, (hipStream_t)stream));
+    return INKLING_OK;
+}
+
+int inkling_fp8_grouped_linear(const inkling_fp8_dims_t* dims, const void* x, const float* x_scales,
+                               const int32_t* row_index, const void* weight, const float* weight_scales,
+                               const int32_t* offsets, void* out, void* stream) {
+    return fp8_product(dims, false, x, x_scales, row_index, weight, weight_scales, offsets, out, stream);
+}
+
+int inkling_fp8_grouped_input_grad(const inkling_fp8_dims_t* dims, const void* dout, const float* dout_scales,
+                                   const void* weight, const float* weight_scales, const int32_t* offsets, void* dx,
+                                   void* stream) {
+    return fp8_product(dims, true, dout, dout_scales, nullptr, weight, weight_scales, offsets, dx, stream);
+}
+
+}  // extern "C"
+
 extern "C" {
 
 const char* inkling_moe_strerror(int code) {

@@ -1,0 +1,247 @@
+// 8-bit floating point (e4m3) with a scale for each block of 128: rows and weights
+// turned into it, and products grouped by expert.
+//
+// Quantising: the scale of a block (128 columns of a row; 128 x 128 of a weight) is the
+// smallest power of two 2^e, e >= -126, with max|block| <= 448 2^e, so v / 2^e is exact
+// and each value is rounded once, to nearest even (v_cvt_pk_fp8_f32; its results for
+// |v| <= 448 are tested one by one).  Half a step is 2^-4 of a value from 2^-6 2^e on, and
+// 2^-10 2^e below.  A block with an infinity or a NaN gets a NaN scale and zeros, so that
+// every product with it is NaN.  One read and one write: HBM bounds both kernels.
+#include <algorithm>
+#include <type_traits>
+
+#include "common.h"
+#include "fp8_common.h"
+#include "fp8_stream.h"
+#include "fp8_tiles.h"
+#include "kernels.h"
+#include "vec.h"
+
+namespace inkling {
+
+namespace {
+
+// Eight values of TE as they lie in memory, and widened
+template <typename TE>
+struct Eight {
+    Raw<TE, 16 / (int)sizeof(TE)> r[8 * sizeof(TE) / 16];
+    __device__ __forceinline__ void load(const TE* p) {
+        constexpr int V = 16 / (int)sizeof(TE);
+#pragma unroll
+        for (int i = 0; i < 8 / V; ++i) r[i] = *reinterpret_cast<const Raw<TE, V>*>(p + i * V);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (size_t i = 0; i < sizeof(r) / sizeof(r[0]); ++i) r[i] = {};
+    }
+    __device__ __forceinline__ void get(float* v) const {
+        constexpr int V = 16 / (int)sizeof(TE);
+#pragma unroll
+        for (int i = 0; i < 8 / V; ++i) widen<TE, V>(r[i], v + i * V);
+    }
+    // largest |v|, in integer order (NaN above infinity)
+    __device__ __forceinline__ uint32_t top() const {
+        float v[8];
+        get(v);
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t = max(t, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        return t;
+    }
+};
+
+// Scale of a block whose largest |v| has these bits, and its inverse (0: every value
+// becomes 0).  448 = 1.75 2^8: adding 0x1FFFFF carries into the exponent exactly when the
+// significand passes 1.75.
+__device__ __forceinline__ float block_scale(uint32_t top, float& inv) {
+    if (top >= 0x7F800000u) {
+        inv = 0.0f;
+        return __uint_as_float(0x7FC00000u);
+    }
+    const int e = max((int)((top + 0x1FFFFFu) >> 23) - 8, 1);
+    inv = __uint_as_float((uint32_t)(254 - e) << 23);
+    return __uint_as_float((uint32_t)e << 23);
+}
+
+__device__ __forceinline__ uint2 to_fp8(const float* v, float inv) {
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = inv == 0.0f ? 0.0f : v[i] * inv;
+    int a = __builtin_amdgcn_cvt_pk_fp8_f32(s[0], s[1], 0, false);
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(s[2], s[3], a, true);
+    int b = __builtin_amdgcn_cvt_pk_fp8_f32(s[4], s[5], 0, false);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(s[6], s[7], b, true);
+    return make_uint2((uint32_t)a, (uint32_t)b);
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
+}
+// largest over 16 neighbouring lanes
+__device__ __forceinline__ uint32_t lanes16_max(uint32_t v) {
+    v = dpp_max<0xB1>(v);
+    v = dpp_max<0x4E>(v);
+    v = dpp_max<0x141>(v);
+    return dpp_max<0x140>(v);
+}
+
+// 16 lanes a block of a row, eight values each
+template <typename TE>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(const TE* __restrict__ x, const int32_t* __restrict__ row_count,
+                                                            int rows, int cols, uint8_t* __restrict__ out,
+                                                            float* __restrict__ scales) {
+    const uint32_t nb = (uint32_t)(cols + kQBlock - 1) / kQBlock;
+    const int end = row_count != nullptr ? max(0, min(rows, *row_count)) : rows;
+    const uint32_t total = (uint32_t)end * nb;   // < 2^31 (host)
+    const int sub = threadIdx.x & 15;
+    for (uint32_t u = blockIdx.x * 16u + (threadIdx.x >> 4); u < total; u += gridDim.x * 16u) {
+        const uint32_t row = u / nb, col = (u - row * nb) * kQBlock + sub * 8;
+        const size_t at = (size_t)row * cols + col;
+        Eight<TE> v;
+        v.zero();
+        const bool in = (int)col < cols;   // cols is a multiple of 16
+        if (in) v.load(x + at);
+        float inv, w[8];
+        const float s = block_scale(lanes16_max(v.top()), inv);
+        v.get(w);
+        if (in) *reinterpret_cast<uint2*>(out + at) = to_fp8(w, inv);
+        if (sub == 0) scales[u] = s;
+    }
+}
+
+// A workgroup a block of 128 x 128: 16 lanes a row, 16 rows at a time
+template <typename TE>
+__global__ __launch_bounds__(256) void quantize_weight_kernel(const TE* __restrict__ w, int E, int N, int K,
+                                                              uint8_t* __restrict__ out, float* __restrict__ scales) {
+    __shared__ uint32_t tops[2][4];
+    const int nb = (N + kQBlock - 1) / kQBlock, kb = (K + kQBlock - 1) / kQBlock;
+    const long long total = (long long)E * nb * kb;
+    const int sub = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+    int turn = 0;
+    for (long long u = blockIdx.x; u < total; u += gridDim.x, turn ^= 1) {
+        const long long rest = u / kb;
+        const int b = (int)(u - rest * kb), n = (int)(rest % nb), e = (int)(rest / nb);
+        const int col = b * kQBlock + sub * 8;
+        Eight<TE> v[8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = n * kQBlock + i * 16 + r0;
+            v[i].zero();
+            if (row < N && col < K) v[i].load(w + ((size_t)e * N + row) * K + col);
+            top = max(top, v[i].top());
+        }
+        top = lanes16_max(top);
+        top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+        if (lane_id() == 0) tops[turn][threadIdx.x >> 6] = top;   // two in turn: one barrier a block
+        __syncthreads();
+        top = max(max(tops[turn][0], tops[turn][1]), max(tops[turn][2], tops[turn][3]));
+        float inv;
+        const float s = block_scale(top, inv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = n * kQBlock + i * 16 + r0;
+            float f[8];
+            v[i].get(f);
+            if (row < N && col < K) *reinterpret_cast<uint2*>(out + ((size_t)e * N + row) * K + col) = to_fp8(f, inv);
+        }
+        if (threadIdx.x == 0) scales[u] = s;
+    }
+}
+
+Fp8Args fp8_args(const Fp8Params& p) {
+    Fp8Args a = {};
+    a.weight = static_cast<const uint8_t*>(p.weight);
+    a.weight_scale = p.weight_scale;
+    a.x = static_cast<const uint8_t*>(p.x);
+    a.x_scale = p.x_scale;
+    a.row_index = p.row_index;
+    a.offsets = p.offsets;
+    a.out = p.out;
+    a.rows = p.rows;
+    a.x_rows = p.x_rows;
+    a.E = p.E;
+    a.N = p.N;
+    a.K = p.K;
+    a.out_bf16 = p.out_bf16;
+    return a;
+}
+
+// Few rows an expert: the weights are streamed.
+bool fp8_streams(const Fp8Params& p) { return !p.input_grad && (long long)p.rows <= 48LL * p.E; }
+
+int stream_cols(const Fp8Params& p) { return (long long)p.E * ((p.N + 63) / 64) >= 512 ? 64 : 16; }
+
+template <bool KN, bool EXACT>
+void launch_tiles(const Fp8Args& a, int grid, hipStream_t stream) {
+    hipLaunchKernelGGL((fp8_tile_kernel<KN, EXACT>), dim3(grid), dim3(kTileThreads), 0, stream, a);
+}
+
+template <int BN, int NW>
+void launch_stream(const Fp8Args& a, hipStream_t stream) {
+    const dim3 grid((unsigned)(a.E * ((a.N + BN - 1) / BN))), block(NW * 64);
+    if (a.out_bf16) hipLaunchKernelGGL((fp8_stream_kernel<BN, NW, false>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((fp8_stream_kernel<BN, NW, true>), grid, block, 0, stream, a);
+}
+
+// tiles of 256 x 256, at most
+long long max_tiles(const Fp8Params& p) {
+    return (((long long)p.rows + 255) / 256 + p.E) * (((p.input_grad ? p.K : p.N) + 255) / 256);
+}
+
+}  // namespace
+
+// Tiles count in 31 bits; a launch has fewer than 2^32 threads (512 a workgroup of 16
+// streamed columns; 64 columns take 256).
+bool fp8_product_fits(const Fp8Params& p) {
+    return (long long)p.E * ((p.N + 63) / 64) < (1LL << 23) && max_tiles(p) <= INT32_MAX - 4096;
+}
+
+hipError_t launch_quantize_rows(int dtype, const void* x, const int32_t* row_count, int rows, int cols, void* values,
+                                float* scales, hipStream_t stream) {
+    const long long units = (long long)rows * ((cols + kQBlock - 1) / kQBlock);
+    const dim3 grid((unsigned)std::min<long long>((units + 15) / 16, 1 << 18)), block(256);
+    if (dtype == 1)
+        hipLaunchKernelGGL(quantize_rows_kernel<bf16_t>, grid, block, 0, stream, static_cast<const bf16_t*>(x), row_count,
+                           rows, cols, static_cast<uint8_t*>(values), scales);
+    else
+        hipLaunchKernelGGL(quantize_rows_kernel<float>, grid, block, 0, stream, static_cast<const float*>(x), row_count,
+                           rows, cols, static_cast<uint8_t*>(values), scales);
+    return hipGetLastError();
+}
+
+hipError_t launch_quantize_weight(int dtype, const void* w, int E, int N, int K, void* values, float* scales,
+                                  hipStream_t stream) {
+    const long long blocks = (long long)E * ((N + kQBlock - 1) / kQBlock) * ((K + kQBlock - 1) / kQBlock);
+    const dim3 grid((unsigned)std::min<long long>(blocks, 1 << 20)), block(256);
+    if (dtype == 1)
+        hipLaunchKernelGGL(quantize_weight_kernel<bf16_t>, grid, block, 0, stream, static_cast<const bf16_t*>(w), E, N, K,
+                           static_cast<uint8_t*>(values), scales);
+    else
+        hipLaunchKernelGGL(quantize_weight_kernel<float>, grid, block, 0, stream, static_cast<const float*>(w), E, N, K,
+                           static_cast<uint8_t*>(values), scales);
+    return hipGetLastError();
+}
+
+hipError_t launch_fp8_product(const Fp8Params& p, hipStream_t stream) {
+    const Fp8Args a = fp8_args(p);
+    if (fp8_streams(p)) {
+        if (stream_cols(p) == 64) launch_stream<64, 4>(a, stream);
+        else launch_stream<16, 8>(a, stream);
+        return hipGetLastError();
+    }
+    const long long tiles = max_tiles(p);
+    const int grid = ((int)std::min<long long>(tiles, device_cu_count()) + 7) / 8 * 8;
+    if (p.input_grad) {
+        if (p.out_bf16) launch_tiles<true, false>(a, grid, stream);
+        else launch_tiles<true, true>(a, grid, stream);
+    } else {
+        if (p.out_bf16) launch_tiles<false, false>(a, grid, stream);
+        else launch_tiles<false, true>(a, grid, stream);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace inkling

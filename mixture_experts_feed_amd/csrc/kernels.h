@@ -265,6 +265,26 @@ bool move_fits(long long T, int H);
 // rows_in[p]; dweights = <token_in[t], rows_in[p]> in the same launch
 hipError_t launch_rows(const RowMoveParams& p, bool spread, hipStream_t stream);
 
+// ---- 8-bit floating point with a scale for each block of 128 (fp8.hip) ----------
+hipError_t launch_quantize_rows(int dtype, const void* x, const int32_t* row_count, int rows, int cols, void* values,
+                                float* scales, hipStream_t stream);
+hipError_t launch_quantize_weight(int dtype, const void* w, int E, int N, int K, void* values, float* scales,
+                                  hipStream_t stream);
+struct Fp8Params {
+    const void* weight;            // [E][N][K] e4m3
+    const float* weight_scale;     // [E][ceil(N/128)][ceil(K/128)]
+    const void* x;                 // rows: [x_rows][K] (input gradient: [rows][N])
+    const float* x_scale;          // [x_rows][ceil(K/128)] (input gradient: [rows][ceil(N/128)])
+    const int32_t* row_index;      // or NULL; not the input gradient
+    const int32_t* offsets;        // [E + 1] (NULL with E == 1: all rows)
+    void* out;
+    int rows, x_rows, E, N, K;     // rows > 0
+    int out_bf16;
+    bool input_grad;
+};
+bool fp8_product_fits(const Fp8Params& p);   // tiles and launch sizes
+hipError_t launch_fp8_product(const Fp8Params& p, hipStream_t stream);
+
 // gamma[t] = value for t < T; the GEMM round counters zeroed (the dense MLP's
 // stand-in for the router and the permutation)
 hipError_t launch_dense_prep(float* gamma, int T, float value, int32_t* round_counters, hipStream_t stream);

@@ -170,7 +170,10 @@ Fp8Args fp8_args(const Fp8Params& p) {
 }
 
 // Few rows an expert: the weights are streamed.
-bool fp8_streams(const Fp8Params& p) { return !p.input_grad && (long long)p.rows <= 48LL * p.E; }
+#ifndef SMAX
+#define SMAX 48LL
+#endif
+bool fp8_streams(const Fp8Params& p) { return !p.input_grad && (long long)p.rows <= SMAX * p.E; }
 
 int stream_cols(const Fp8Params& p) { return (long long)p.E * ((p.N + 63) / 64) >= 512 ? 64 : 16; }
 
@@ -179,11 +182,25 @@ void launch_tiles(const Fp8Args& a, int grid, hipStream_t stream) {
     hipLaunchKernelGGL((fp8_tile_kernel<KN, EXACT>), dim3(grid), dim3(kTileThreads), 0, stream, a);
 }
 
-template <int BN, int NW>
-void launch_stream(const Fp8Args& a, hipStream_t stream) {
-    const dim3 grid((unsigned)(a.E * ((a.N + BN - 1) / BN))), block(NW * 64);
-    if (a.out_bf16) hipLaunchKernelGGL((fp8_stream_kernel<BN, NW, false>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((fp8_stream_kernel<BN, NW, true>), grid, block, 0, stream, a);
+template <int BN, int NW, int DEPTH, int FM>
+void launch_stream_as(const Fp8Args& a, hipStream_t stream) {
+    const long long tasks = ((long long)(a.rows + 16 * FM - 1) / (16 * FM) + a.E) * ((a.N + BN - 1) / BN);
+    const dim3 grid((unsigned)std::min<long long>(tasks, device_cu_count())), block(NW * 64);
+    if (a.out_bf16) hipLaunchKernelGGL((fp8_stream_kernel<BN, NW, DEPTH, FM, false>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((fp8_stream_kernel<BN, NW, DEPTH, FM, true>), grid, block, 0, stream, a);
+}
+
+void launch_stream(const Fp8Args& a, int cols, hipStream_t stream) {
+    const double mean = (double)a.rows / a.E;
+    if (cols == 64) {
+        if (mean <= 8.0) launch_stream_as<64, 4, 4, 1>(a, stream);
+        else if (mean <= 20.0) launch_stream_as<64, 4, 4, 2>(a, stream);
+        else launch_stream_as<64, 4, 4, 4>(a, stream);
+    } else {
+        if (mean <= (a.E == 1 ? 16.0 : 8.0)) launch_stream_as<16, 8, 6, 1>(a, stream);
+        else if (mean <= (a.E == 1 ? 32.0 : 20.0)) launch_stream_as<16, 8, 6, 2>(a, stream);
+        else launch_stream_as<16, 8, 4, 4>(a, stream);
+    }
 }
 
 // tiles of 256 x 256, at most
@@ -228,8 +245,7 @@ hipError_t launch_quantize_weight(int dtype, const void* w, int E, int N, int K,
 hipError_t launch_fp8_product(const Fp8Params& p, hipStream_t stream) {
     const Fp8Args a = fp8_args(p);
     if (fp8_streams(p)) {
-        if (stream_cols(p) == 64) launch_stream<64, 4>(a, stream);
-        else launch_stream<16, 8>(a, stream);
+        launch_stream(a, stream_cols(p), stream);
         return hipGetLastError();
     }
     const long long tiles = max_tiles(p);

@@ -2,6 +2,8 @@
 // block of 128): fragments, the product of one block, the caller's offsets made safe.
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 #include "vec.h"
 
@@ -79,6 +81,122 @@ struct Fp8Args {
     int rows, x_rows, E, N, K;
     int out_bf16;
 };
+
+constexpr int kMaxFp8Groups = 512;
+
+// The experts' rows and row tiles of BM, found from the caller's offsets by the whole
+// workgroup: offs[0 .. E] clamped to [0, rows], each at least the largest before it;
+// first[e] = row tiles of the experts before e.  Ends with a barrier.
+template <int THREADS, int BM>
+__device__ __forceinline__ void plan_experts(const Fp8Args& a, int32_t* offs, int32_t* first) {
+    constexpr int PER = kMaxFp8Groups / THREADS, NW = THREADS / kWave;
+    static_assert(PER >= 1 && PER * THREADS == kMaxFp8Groups, "a thread takes PER experts");
+    __shared__ int32_t wave_max[NW], wave_sum[NW];
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    if (a.offsets == nullptr) {
+        if (tid == 0) {
+            offs[0] = first[0] = 0;
+            offs[1] = a.rows;
+            first[1] = (a.rows + BM - 1) / BM;
+        }
+        __syncthreads();
+        return;
+    }
+    const int start = max(0, min(a.offsets[0], a.rows));
+    int end[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = tid * PER + i;
+        end[i] = e < a.E ? max(0, min(a.offsets[e + 1], a.rows)) : 0;
+    }
+    end[0] = max(end[0], start);
+#pragma unroll
+    for (int i = 1; i < PER; ++i) end[i] = max(end[i], end[i - 1]);
+    int top = end[PER - 1];   // running maximum over the threads
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int o = __shfl_up(top, d);
+        if (lane >= d) top = max(top, o);
+    }
+    if (lane == kWave - 1) wave_max[wv] = top;
+    __syncthreads();
+    int before = start;
+    for (int w = 0; w < wv; ++w) before = max(before, wave_max[w]);
+    const int prev = __shfl_up(top, 1);
+    if (lane > 0) before = max(before, prev);
+    int tiles[PER], sum = 0, begin = before;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        end[i] = max(end[i], before);
+        tiles[i] = tid * PER + i < a.E ? (end[i] - begin + BM - 1) / BM : 0;
+        begin = end[i];
+        sum += tiles[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int o = __shfl_up(incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == kWave - 1) wave_sum[wv] = incl;
+    __syncthreads();
+    int at = incl - sum;
+    for (int w = 0; w < wv; ++w) at += wave_sum[w];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = tid * PER + i;
+        at += tiles[i];
+        if (e < a.E) {
+            offs[e + 1] = end[i];
+            first[e + 1] = at;
+        }
+    }
+    if (tid == 0) {
+        offs[0] = start;
+        first[0] = 0;
+    }
+    __syncthreads();
+}
+
+// The last expert whose first row tile is not after rt.  Whole waves.
+__device__ __forceinline__ int expert_of(const int32_t* first, int E, int rt) {
+    int count = 0;
+    for (int c = 0; c < E; c += kWave) {
+        const int e = c + lane_id();
+        count += __popcll(__ballot(e < E && first[min(e, E)] <= rt));
+    }
+    return __builtin_amdgcn_readfirstlane(count - 1);
+}
+
+typedef __attribute__((address_space(3))) void fp8_lds_t;
+typedef const __attribute__((address_space(1))) void fp8_glb_t;
+typedef __attribute__((address_space(3))) i32x2_t fp8_lds_i32x2_t;
+
+// what lanes past an end load
+__device__ uint4 fp8_zero_chunk = {0u, 0u, 0u, 0u};
+
+constexpr int kLoadOnce = 2;   // cache policy of loads that nothing reads again (non-temporal)
+template <int POLICY>
+__device__ __forceinline__ void copy16_to_lds(const void* src, uint8_t* dst) {
+    __builtin_amdgcn_global_load_lds((fp8_glb_t*)src, (fp8_lds_t*)dst, 16, 0, POLICY);
+}
+
+// s_waitcnt vmcnt(N) and lgkmcnt(0), each alone
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4)); }
+__device__ __forceinline__ void barrier_only() { __asm__ volatile("s_barrier" ::: "memory"); }
+
+template <int B, int E, typename F>
+__device__ __forceinline__ void static_for8(F&& f) {
+    if constexpr (B < E) {
+        f(std::integral_constant<int, B>{});
+        static_for8<B + 1, E>(f);
+    }
+}
 
 }  // namespace
 

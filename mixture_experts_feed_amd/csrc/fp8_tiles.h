@@ -18,8 +18,6 @@
 // workgroups that run side by side share weights and rows through its L2.
 #pragma once
 
-#include <type_traits>
-
 #include "fp8_common.h"
 
 namespace inkling {
@@ -27,31 +25,6 @@ namespace inkling {
 namespace {
 
 constexpr int kTileThreads = 512;
-constexpr int kMaxFp8Groups = 512;
-
-typedef __attribute__((address_space(3))) void fp8_lds_t;
-typedef const __attribute__((address_space(1))) void fp8_glb_t;
-typedef __attribute__((address_space(3))) i32x2_t fp8_lds_i32x2_t;
-
-// what lanes past a tail load
-__device__ uint4 fp8_zero_chunk = {0u, 0u, 0u, 0u};
-
-__device__ __forceinline__ void copy16_to_lds(const void* src, uint8_t* dst) {
-    __builtin_amdgcn_global_load_lds((fp8_glb_t*)src, (fp8_lds_t*)dst, 16, 0, 0);
-}
-
-// all of this wave's loads done; LDS reads done
-__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xF << 8)); }
-__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4)); }
-__device__ __forceinline__ void barrier_only() { __asm__ volatile("s_barrier" ::: "memory"); }
-
-template <int B, int E, typename F>
-__device__ __forceinline__ void static_for8(F&& f) {
-    if constexpr (B < E) {
-        f(std::integral_constant<int, B>{});
-        static_for8<B + 1, E>(f);
-    }
-}
 
 struct Fp8Tile {
     int e, row0, valid, n0;   // expert; first row and rows of the tile; first output column
@@ -73,7 +46,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
     constexpr int kEpRow = 144;   // 128 bytes of a result row and 16 of padding
     __shared__ __attribute__((aligned(16))) uint8_t ep_lds[NW * 16 * kEpRow];
     __shared__ int32_t offs[kMaxFp8Groups + 1], first[kMaxFp8Groups + 1];
-    __shared__ int32_t wave_max[NW], wave_sum[NW];
 
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn0 = (wv % WN) * 64, wm = wv / WN;
@@ -84,48 +56,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
     const int ntn = (cols + BN - 1) / BN;
 
     // ---- the experts' rows and row tiles -----------------------------------------
-    if (a.offsets == nullptr) {
-        if (tid == 0) {
-            offs[0] = first[0] = 0;
-            offs[1] = a.rows;
-            first[1] = (a.rows + BM - 1) / BM;
-        }
-    } else {
-        // clamped to [0, rows], each at least the largest before it
-        const int start = max(0, min(a.offsets[0], a.rows));
-        int end = tid < a.E ? max(0, min(a.offsets[tid + 1], a.rows)) : 0;
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) {
-            const int o = __shfl_up(end, d);
-            if (lane >= d) end = max(end, o);
-        }
-        if (lane == kWave - 1) wave_max[wv] = end;
-        __syncthreads();
-        end = max(end, start);
-        int begin = start;
-        for (int w = 0; w < wv; ++w) begin = max(begin, wave_max[w]);
-        end = max(end, begin);
-        const int prev = __shfl_up(end, 1);
-        if (lane > 0) begin = prev;
-        int incl = tid < a.E ? (end - begin + BM - 1) / BM : 0;
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) {
-            const int o = __shfl_up(incl, d);
-            if (lane >= d) incl += o;
-        }
-        if (lane == kWave - 1) wave_sum[wv] = incl;
-        __syncthreads();
-        for (int w = 0; w < wv; ++w) incl += wave_sum[w];
-        if (tid < a.E) {
-            offs[tid + 1] = end;
-            first[tid + 1] = incl;
-        }
-        if (tid == 0) {
-            offs[0] = start;
-            first[0] = 0;
-        }
-    }
-    __syncthreads();
+    plan_experts<kTileThreads, BM>(a, offs, first);
     const long long total = (long long)first[a.E] * ntn;
     const int xcd = blockIdx.x & 7, nloc = gridDim.x >> 3;
     const int L_end = (int)(total * (xcd + 1) / 8);
@@ -135,13 +66,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
     auto decode = [&](int l) {
         Fp8Tile t;
         const int rt = l / ntn;
-        // the last expert whose first row tile is not after rt
-        int count = 0;
-        for (int c = 0; c < a.E; c += kWave) {
-            const int e = c + lane;
-            count += __popcll(__ballot(e < a.E && first[min(e, a.E)] <= rt));
-        }
-        t.e = __builtin_amdgcn_readfirstlane(count - 1);
+        t.e = expert_of(first, a.E, rt);
         const int f = first[t.e], c = first[t.e + 1] - f;
         const int in = l - f * ntn, nt = in / c, mt = in - nt * c;
         t.row0 = __builtin_amdgcn_readfirstlane(offs[t.e] + mt * BM);
@@ -196,9 +121,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
         if (k0 + kQBlock <= len) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                if (8 * (wv + NW * q) < ld_valid) copy16_to_lds(b_src[q] + k0, db + (wv + NW * q) * 1024);
+                if (8 * (wv + NW * q) < ld_valid) copy16_to_lds<0>(b_src[q] + k0, db + (wv + NW * q) * 1024);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) copy16_to_lds(ab + a_off[q], da + (wv + NW * q) * 1024);
+            for (int q = 0; q < 4; ++q) copy16_to_lds<0>(ab + a_off[q], da + (wv + NW * q) * 1024);
         } else {
             // the stage of the tail: what lies past it reads zeros
             const uint8_t* zero = reinterpret_cast<const uint8_t*>(&fp8_zero_chunk);
@@ -206,11 +131,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 if (8 * (wv + NW * q) < ld_valid)
-                    copy16_to_lds(in ? b_src[q] + k0 : zero, db + (wv + NW * q) * 1024);
+                    copy16_to_lds<0>(in ? b_src[q] + k0 : zero, db + (wv + NW * q) * 1024);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const bool there = KN ? 4 * (wv + NW * q) + (lane >> 4) < len - k0 : in;
-                copy16_to_lds(there ? ab + a_off[q] : zero, da + (wv + NW * q) * 1024);
+                copy16_to_lds<0>(there ? ab + a_off[q] : zero, da + (wv + NW * q) * 1024);
             }
         }
         ++ld_block;
@@ -279,7 +204,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
                 __asm__("" : "+v"(acc[i][j]));   // here, not where the sum is next read
             }
         };
-        wait_loads();
+        wait_loads<0>();
         barrier_only();
         if (nb > 1) issue(sa1, sb1, ss1);
 #pragma unroll
@@ -305,7 +230,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
                 } else {
                     if (more) {
                         wait_lds();
-                        wait_loads();
+                        wait_loads<0>();
                         barrier_only();
                         if (b + 2 < nb) issue(wa, wb, wsc);
                     }

@@ -177,9 +177,15 @@ bool fp8_streams(const Fp8Params& p) { return !p.input_grad && (long long)p.rows
 
 int stream_cols(const Fp8Params& p) { return (long long)p.E * ((p.N + 63) / 64) >= 512 ? 64 : 16; }
 
-template <bool KN, bool EXACT>
+// fp32 results take tiles of 128 rows: the conversions need the registers.
+int tile_rows(const Fp8Params& p) { return p.out_bf16 ? 256 : 128; }
+
+template <int FM, bool KN, bool EXACT>
 void launch_tiles(const Fp8Args& a, int grid, hipStream_t stream) {
-    hipLaunchKernelGGL((fp8_tile_kernel<KN, EXACT>), dim3(grid), dim3(kTileThreads), 0, stream, a);
+    // offsets into the rows: 32 bits, or not
+    if ((uint64_t)a.x_rows * (KN ? a.N : a.K) < (1ull << 32))
+        hipLaunchKernelGGL((fp8_tile_kernel<FM, KN, EXACT, false>), dim3(grid), dim3(kTileThreads), 0, stream, a);
+    else hipLaunchKernelGGL((fp8_tile_kernel<FM, KN, EXACT, true>), dim3(grid), dim3(kTileThreads), 0, stream, a);
 }
 
 template <int BN, int NW, int DEPTH, int FM>
@@ -203,9 +209,9 @@ void launch_stream(const Fp8Args& a, int cols, hipStream_t stream) {
     }
 }
 
-// tiles of 256 x 256, at most
+// tiles of a launch, at most
 long long max_tiles(const Fp8Params& p) {
-    return (((long long)p.rows + 255) / 256 + p.E) * (((p.input_grad ? p.K : p.N) + 255) / 256);
+    return (((long long)p.rows + tile_rows(p) - 1) / tile_rows(p) + p.E) * (((p.input_grad ? p.K : p.N) + 255) / 256);
 }
 
 }  // namespace
@@ -251,11 +257,11 @@ hipError_t launch_fp8_product(const Fp8Params& p, hipStream_t stream) {
     const long long tiles = max_tiles(p);
     const int grid = ((int)std::min<long long>(tiles, device_cu_count()) + 7) / 8 * 8;
     if (p.input_grad) {
-        if (p.out_bf16) launch_tiles<true, false>(a, grid, stream);
-        else launch_tiles<true, true>(a, grid, stream);
+        if (p.out_bf16) launch_tiles<8, true, false>(a, grid, stream);
+        else launch_tiles<4, true, true>(a, grid, stream);
     } else {
-        if (p.out_bf16) launch_tiles<false, false>(a, grid, stream);
-        else launch_tiles<false, true>(a, grid, stream);
+        if (p.out_bf16) launch_tiles<8, false, false>(a, grid, stream);
+        else launch_tiles<4, false, true>(a, grid, stream);
     }
     return hipGetLastError();
 }

@@ -31,18 +31,23 @@ struct Fp8Tile {
 };
 
 // KN: the input gradient (weights read as [reduction][column])
-template <bool KN, bool EXACT>
+// FM: 16-row blocks of a wave's tile; the workgroup's tile has BM = 32 FM rows.
+// FAR: x is larger than 32 bits reach.
+template <int FM, bool KN, bool EXACT, bool FAR>
 __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args a) {
-    constexpr int BN = 256, BM = 256, WN = 4, NW = 8, FN = 4, FM = 8;
-    constexpr int STAGE = 256 * kQBlock;
+    constexpr int BN = 256, BM = 32 * FM, WN = 4, NW = 8, FN = 4;
+    constexpr int BH = FM / 4;                     // wave loads of half a stage's rows
+    static_assert(FM == 4 || FM == 8, "128 or 256 rows");
+    constexpr int STAGE = BN * kQBlock, STAGE_B = BM * kQBlock;
     // each stage its own object: the compiler then needs no wait for the loads into one
     // before reads of the other
     __shared__ __attribute__((aligned(16))) uint8_t sa0[STAGE];
     __shared__ __attribute__((aligned(16))) uint8_t sa1[STAGE];
-    __shared__ __attribute__((aligned(16))) uint8_t sb0[STAGE];
-    __shared__ __attribute__((aligned(16))) uint8_t sb1[STAGE];
-    __shared__ __attribute__((aligned(16))) float ss0[BM];
-    __shared__ __attribute__((aligned(16))) float ss1[BM];
+    __shared__ __attribute__((aligned(16))) uint8_t sb0[STAGE_B];
+    __shared__ __attribute__((aligned(16))) uint8_t sb1[STAGE_B];
+    // scales of a stage: of 256 rows, then those of each column group's weights (64 times)
+    __shared__ __attribute__((aligned(16))) float ss0[kTileThreads];
+    __shared__ __attribute__((aligned(16))) float ss1[kTileThreads];
     constexpr int kEpRow = 144;   // 128 bytes of a result row and 16 of padding
     __shared__ __attribute__((aligned(16))) uint8_t ep_lds[NW * 16 * kEpRow];
     __shared__ int32_t offs[kMaxFp8Groups + 1], first[kMaxFp8Groups + 1];
@@ -79,70 +84,109 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
     // 128-byte rows (token rows; weights of the forward): the 16-byte chunk c of row r
     // sits at chunk place c ^ (r & 7); 256-byte rows (weights of the input gradient, a
     // row of the reduction each): at c ^ swk(r).  Both keep the reads below spread over
-    // the banks.
+    // the banks.  A wave load is 1 KB: eight 128-byte rows (lane / 8 of them; chunk place
+    // lane % 8) or four 256-byte rows.
     auto swk = [](int r) { return (r & 7) | ((r >> 1) & 8); };
-    // a wave load is 1 KB: eight 128-byte rows (lane / 8 of them; chunk place lane % 8)
-    // or four 256-byte rows
     const int c16 = 16 * ((lane & 7) ^ (lane >> 3));   // the lane's chunk of its 128-byte rows
-    const uint8_t* a_base = nullptr;    // this expert's weights, from the tile's first row
-    uint32_t a_off[4];                  // the lane's four chunks of a stage, from a_base
-    const uint8_t* b_src[4];
-    const float* s_src = nullptr;
-    int ld_block = 0, ld_valid = 1;
+    // A load adds a lane's 32-bit offset to a scalar base.  Weights: from the expert's,
+    // the tile's first row (input gradient: the reduction's first); rows: from a.x (FAR:
+    // the row's number, and 64-bit arithmetic for every load).
+    const uint8_t* a_base = nullptr;
+    const float* ws_base = nullptr;     // weight scale of block 0 of this wave's columns
+    uint32_t a_off[4], b_off[2 * BH], s_off = 0;
     auto setup = [&](const Fp8Tile& t) __attribute__((always_inline)) {
+        const int kb = (a.K + kQBlock - 1) / kQBlock, c = min((t.n0 + wn0) / kQBlock, cb - 1);
         a_base = a.weight + (size_t)t.e * a.N * a.K + (KN ? 0 : (size_t)t.n0 * a.K);
+        ws_base = a.weight_scale + (size_t)t.e * cb * nb + (KN ? c : c * kb);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             if constexpr (KN) {
                 const int r = 4 * (wv + NW * q) + (lane >> 4);
-                const int c = (lane & 15) ^ swk(r);
-                a_off[q] = (uint32_t)r * a.K + min(t.n0 + 16 * c, a.K - 16);   // columns past the end: the last chunk
+                const int ch = (lane & 15) ^ swk(r);
+                a_off[q] = (uint32_t)r * a.K + min(t.n0 + 16 * ch, a.K - 16);   // columns past the end: the last chunk
             } else {
                 const int r = 8 * (wv + NW * q) + (lane >> 3);
-                a_off[q] = (uint32_t)min(r, a.N - 1 - t.n0) * a.K + c16;       // rows past the end: the last row
+                a_off[q] = (uint32_t)min(r, a.N - 1 - t.n0) * a.K + c16;        // rows past the end: the last row
             }
-            int row = t.row0 + min(8 * (wv + NW * q) + (lane >> 3), t.valid - 1);
-            if (!KN && a.row_index != nullptr) row = max(0, min(a.row_index[row], a.x_rows - 1));
-            b_src[q] = a.x + (size_t)row * len + c16;
         }
-        if (wv < 4) {
-            int row = t.row0 + min(64 * wv + lane, t.valid - 1);
+        auto source = [&](int m) {   // x row of the tile's row m (past the end: the last one)
+            int row = t.row0 + min(m, t.valid - 1);
             if (!KN && a.row_index != nullptr) row = max(0, min(a.row_index[row], a.x_rows - 1));
-            s_src = a.x_scale + (size_t)row * nb;
+            return (uint32_t)row;
+        };
+#pragma unroll
+        for (int q = 0; q < 2 * BH; ++q) {
+            const uint32_t row = source(8 * (wv + NW * q) + (lane >> 3));
+            b_off[q] = FAR ? row : row * (uint32_t)len + c16;
         }
-        ld_block = 0;
-        ld_valid = t.valid;
+        const uint32_t row = source(64 * (wv & 3) + lane);
+        s_off = FAR ? row : row * (uint32_t)nb;
     };
-    auto issue = [&](uint8_t* da, uint8_t* db, float* ds) __attribute__((always_inline)) {
-        const int k0 = ld_block * kQBlock;
-        if (wv < 4)
-            __builtin_amdgcn_global_load_lds((fp8_glb_t*)(s_src + ld_block), (fp8_lds_t*)(ds + 64 * wv), 4, 0, 0);
-        const uint8_t* ab = a_base + (KN ? (size_t)k0 * a.K : (size_t)k0);
-        if (k0 + kQBlock <= len) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (8 * (wv + NW * q) < ld_valid) copy16_to_lds<0>(b_src[q] + k0, db + (wv + NW * q) * 1024);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) copy16_to_lds<0>(ab + a_off[q], da + (wv + NW * q) * 1024);
+    // (Offsets pass through an empty asm so that no address is kept over the K loop, which
+    // needs the registers: a spilled one's reload would wait for all loads.)
+    auto fresh = [](uint32_t v) __attribute__((always_inline)) {
+        __asm__ volatile("" : "+v"(v));
+        return v;
+    };
+    // The loads of a block, in two parts (see the schedule below): weights and the first
+    // half of the rows; the scales and the second half.  Always the same number, which
+    // the waits count.  Chunks past the end of the reduction read the row's last chunk
+    // (input gradient, weights: earlier rows) and are made zeros as fragments of the rows;
+    // the other operand's numbers do not matter there, since one that is NaN also stands
+    // in the sums of the same row or column before.
+    constexpr int FIRST = 4 + BH, SECOND = 1 + BH;
+    auto past = [&](int b) __attribute__((always_inline)) {   // bytes that the lane's chunk starts past the last one
+        return (uint32_t)max(0, c16 + 16 + b * kQBlock - len);
+    };
+    auto load_a = [&](int q, uint8_t* da, int b) __attribute__((always_inline)) {
+        uint8_t* dst = da + (wv + NW * q) * 1024;
+        if constexpr (KN) {
+            // (four rows of the reduction, all before its end or all past it)
+            const int r = 4 * (wv + NW * q);
+            const uint8_t* base = a_base + ((size_t)b * kQBlock - (b * kQBlock + r < len ? 0 : r)) * a.K;
+            copy16_to_lds<0>(base + fresh(a_off[q]), dst);
         } else {
-            // the stage of the tail: what lies past it reads zeros
-            const uint8_t* zero = reinterpret_cast<const uint8_t*>(&fp8_zero_chunk);
-            const bool in = c16 < len - k0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (8 * (wv + NW * q) < ld_valid)
-                    copy16_to_lds<0>(in ? b_src[q] + k0 : zero, db + (wv + NW * q) * 1024);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const bool there = KN ? 4 * (wv + NW * q) + (lane >> 4) < len - k0 : in;
-                copy16_to_lds<0>(there ? ab + a_off[q] : zero, da + (wv + NW * q) * 1024);
-            }
+            copy16_to_lds<0>(a_base + b * kQBlock + (fresh(a_off[q]) - past(b)), dst);
         }
-        ++ld_block;
+    };
+    auto load_b = [&](int q, uint8_t* db, int b) __attribute__((always_inline)) {
+        uint8_t* dst = db + (wv + NW * q) * 1024;
+        const uint32_t off = fresh(b_off[q]);
+        if constexpr (FAR) copy16_to_lds<0>(a.x + b * kQBlock + ((uint64_t)off * (uint32_t)len + (c16 - past(b))), dst);
+        else copy16_to_lds<0>(a.x + b * kQBlock + (off - past(b)), dst);
+    };
+    auto load_s = [&](float* ds, int b) __attribute__((always_inline)) {
+        const uint32_t off = fresh(s_off);
+        if (wv < 4) {
+            const float* p = FAR ? a.x_scale + b + (uint64_t)off * (uint32_t)nb : a.x_scale + b + off;
+            __builtin_amdgcn_global_load_lds((fp8_glb_t*)p, (fp8_lds_t*)(ds + 64 * wv), 4, 0, 0);
+        } else {
+            const float* p = ws_base + (size_t)b * (KN ? cb : 1);
+            __builtin_amdgcn_global_load_lds((fp8_glb_t*)p, (fp8_lds_t*)(ds + 64 * wv), 4, 0, 0);
+        }
+    };
+    // load number i of each part
+    auto first_part = [&](int i, uint8_t* da, uint8_t* db, int b) __attribute__((always_inline)) {
+        if (i < 4) load_a(i, da, b);
+        else load_b(i - 4, db, b);
+    };
+    auto second_part = [&](int i, uint8_t* db, float* ds, int b) __attribute__((always_inline)) {
+        if (i == 0) load_s(ds, b);
+        else load_b(BH + i - 1, db, b);
+    };
+    // what a tile's K loop finds on its way
+    auto issue_tile = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < FIRST; ++i) first_part(i, sa0, sb0, 0);
+#pragma unroll
+        for (int i = 0; i < SECOND; ++i) second_part(i, sb0, ss0, 0);
+        if (nb > 1)
+#pragma unroll
+            for (int i = 0; i < FIRST; ++i) first_part(i, sa1, sb1, 1);
     };
 
     // ---- fragments -----------------------------------------------------------------
-    const int p0 = (g ^ (rl & 7)) << 4, p1 = ((4 + g) ^ (rl & 7)) << 4;   // places of chunks g and 4 + g
+    const int at0 = (g ^ (rl & 7)) << 4, at1 = ((4 + g) ^ (rl & 7)) << 4;   // places of chunks g and 4 + g
     const int a_row = (wn0 + rl) * kQBlock, b_row = (16 * wm + rl) * kQBlock;
     // input gradient: lane 2 j + h of 16 addresses half h of the 16 columns' chunk in
     // reduction row j of eight; the transposing read hands lane c the eight rows of column c
@@ -151,125 +195,150 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
     auto read_a = [&](const uint8_t* __restrict__ st, int i) __attribute__((always_inline)) {
         Frag f;
         if constexpr (KN) {
-            const uint8_t* p = st + (tr_at ^ (i << 4));
+            const uint8_t* p = st + ((int)fresh((uint32_t)tr_at) ^ (i << 4));
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 f.quarter[q] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
                     (fp8_lds_i32x2_t*)(p + ((q & 1) * 8 + (q >> 1) * 64) * 256));
         } else {
-            f.half[0] = *reinterpret_cast<const i32x4_t*>(st + a_row + i * 16 * kQBlock + p0);
-            f.half[1] = *reinterpret_cast<const i32x4_t*>(st + a_row + i * 16 * kQBlock + p1);
+            f.half[0] = *reinterpret_cast<const i32x4_t*>(st + a_row + i * 16 * kQBlock + at0);
+            f.half[1] = *reinterpret_cast<const i32x4_t*>(st + a_row + i * 16 * kQBlock + at1);
         }
         return f;
     };
     auto read_b = [&](const uint8_t* __restrict__ st, int j) __attribute__((always_inline)) {
         Frag f;
-        f.half[0] = *reinterpret_cast<const i32x4_t*>(st + b_row + j * 32 * kQBlock + p0);
-        f.half[1] = *reinterpret_cast<const i32x4_t*>(st + b_row + j * 32 * kQBlock + p1);
+        f.half[0] = *reinterpret_cast<const i32x4_t*>(st + b_row + j * 32 * kQBlock + at0);
+        f.half[1] = *reinterpret_cast<const i32x4_t*>(st + b_row + j * 32 * kQBlock + at1);
         return f;
     };
 
     f32x4_t acc[FN][FM];
-    // weight scale of block b for this wave's columns
-    auto weight_scale = [&](const Fp8Tile& t, int b) __attribute__((always_inline)) {
-        const int c = min((t.n0 + wn0) / kQBlock, cb - 1);
-        const int kb = (a.K + kQBlock - 1) / kQBlock;
-        const int at = KN ? b * kb + c : c * kb + b;
-        return scalar_load(a.weight_scale + (size_t)t.e * cb * nb + at);
-    };
 
     // NJ: 16-row blocks of the wave that are multiplied (the others hold no rows).
     //
-    // A stage takes a step a row block: its four products, the sums of the step before,
-    // and the LDS reads of the next step.  Before the last step, all of whose reads are
-    // done: wait for the next stage's loads, meet, load the stage after it into the
-    // buffers just read; the next stage's first reads run beside the last products.
+    // A stage takes a step a row block: the LDS reads of the next step, the block's four
+    // products, and their sums (by the time the last product is issued the first is done).  All waves meet twice a stage:
+    //   P0(b), before the last step of stage b - 1 (all its reads done): the weights, the
+    //     first half of the rows and the scales of b are there; the second half and the
+    //     scales of b + 1 may be loaded where b - 1 had them;
+    //   P1(b), once the weights (read into registers at once) and the first half of b are
+    //     read: its second half is there; the weights and the first half of b + 2 may be
+    //     loaded in their place.
+    // So everything is on its way for a stage and a half, in two stages' buffers.  The
+    // loads are spread over the steps after each meeting: all at once they would hold up
+    // every wave.
     auto kloop = [&](auto NJ_, const Fp8Tile& t) __attribute__((always_inline)) {
         constexpr int NJ = decltype(NJ_)::value;
+        constexpr int HALF = FM / 2, MEET = NJ > HALF ? HALF - 1 : NJ - 2;   // step of P1
+        constexpr int PER2 = MEET > 0 ? (SECOND + MEET - 1) / MEET : SECOND;
+        constexpr int PER1 = (FIRST + NJ - 2 - MEET) / (NJ - 1 - MEET);
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
             for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         Frag fa[FN], fb[2];
-        f32x4_t p[2][FN];      // products of a step
-        float f[2], sc[2];     // their factor; row scales
-        float ws = weight_scale(t, 0);
-        // add the products of step (row block) j
-        auto add = [&](auto J_, int turn) __attribute__((always_inline)) {
-            constexpr int j = decltype(J_)::value;
-#pragma unroll
-            for (int i = 0; i < FN; ++i) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[turn][i][r], f[turn], acc[i][j][r]);
-                __asm__("" : "+v"(acc[i][j]));   // here, not where the sum is next read
-            }
+        float sc[2], ws;       // row scales, the weights' scale
+        auto meet0 = [&](int b) __attribute__((always_inline)) {
+            if (b + 1 < nb) wait_loads<BH + FIRST>();   // after the scales of b: its second half, the first part of b + 1
+            else wait_loads<0>();
+            barrier_only();
         };
-        wait_loads<0>();
-        barrier_only();
-        if (nb > 1) issue(sa1, sb1, ss1);
+        auto meet1 = [&](int b) __attribute__((always_inline)) {
+            if (b + 1 < nb) wait_loads<FIRST + SECOND>();   // both parts of b + 1
+            else wait_loads<0>();
+            barrier_only();
+        };
+        auto first_reads = [&](const uint8_t* __restrict__ na, const uint8_t* __restrict__ nbuf,
+                               const float* __restrict__ ns) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < FN; ++i) fa[i] = read_a(sa0, i);
-        fb[0] = read_b(sb0, 0);
-        sc[0] = ss0[16 * wm + rl];
+            for (int i = 0; i < FN; ++i) fa[i] = read_a(na, i);
+            fb[0] = read_b(nbuf, 0);
+            sc[0] = ns[16 * wm + rl];
+            ws = ns[256 + 64 * (wv % WN) + lane];
+        };
+        meet0(0);
+        first_reads(sa0, sb0, ss0);
         // (turns of the double buffers: NJ is even)
-        auto stage = [&](const uint8_t* __restrict__ ca, const uint8_t* __restrict__ cbuf, const float* __restrict__ cs,
-                         const uint8_t* __restrict__ na, const uint8_t* __restrict__ nbuf,
-                         const float* __restrict__ ns, uint8_t* wa, uint8_t* wb, float* wsc,
+        auto stage = [&](uint8_t* __restrict__ ca, uint8_t* __restrict__ cbuf, float* __restrict__ cs,
+                         uint8_t* __restrict__ na, uint8_t* __restrict__ nbuf, float* __restrict__ ns,
                          int b) __attribute__((always_inline)) {
             const bool more = b + 1 < nb;
+            const int rest = len - b * kQBlock;   // of the reduction
             const float w = ws;
-            if (more) ws = weight_scale(t, b + 1);
             static_for8<0, NJ>([&](auto J_) __attribute__((always_inline)) {
                 constexpr int j = decltype(J_)::value, cur = j & 1;
-                if constexpr (j + 1 < NJ) {
+                auto next_reads = [&]() __attribute__((always_inline)) {
                     fb[cur ^ 1] = read_b(cbuf, j + 1);
                     sc[cur ^ 1] = cs[16 * (2 * (j + 1) + wm) + rl];
-                    __builtin_amdgcn_sched_barrier(0);
+                };
+                if constexpr (j == MEET) {
+                    // (reads of the rows that the loads take the place of come before)
+                    if constexpr (j + 1 < HALF) next_reads();
+                    if constexpr (MEET == 0) {
+                        if (more)
 #pragma unroll
-                    for (int i = 0; i < FN; ++i) p[cur][i] = block_product<EXACT>(fa[i], fb[cur]);
-                } else {
-                    if (more) {
-                        wait_lds();
-                        wait_loads<0>();
-                        barrier_only();
-                        if (b + 2 < nb) issue(wa, wb, wsc);
+                            for (int i = 0; i < SECOND; ++i) second_part(i, nbuf, ns, b + 1);
                     }
-                    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                    for (int i = 0; i < FN; ++i) p[cur][i] = block_product<EXACT>(fa[i], fb[cur]);
+                    wait_lds();
+                    meet1(b);
+                    if constexpr (j + 1 >= HALF) next_reads();
+                } else if constexpr (j + 1 < NJ) {
+                    next_reads();
+                } else if (more) {
+                    wait_lds();
+                    meet0(b + 1);
                 }
-                f[cur] = sc[cur] * w;
-                if constexpr (j > 0) add(std::integral_constant<int, j - 1>{}, cur ^ 1);
-                else if (b > 0) add(std::integral_constant<int, NJ - 1>{}, cur ^ 1);
+                if constexpr (j < MEET) {
+                    if (more)
+#pragma unroll
+                        for (int i = j * PER2; i < SECOND && i < (j + 1) * PER2; ++i) second_part(i, nbuf, ns, b + 1);
+                }
+                if constexpr (j >= MEET && j + 1 < NJ) {
+                    if (b + 2 < nb)
+#pragma unroll
+                        for (int i = (j - MEET) * PER1; i < FIRST && i < (j - MEET + 1) * PER1; ++i)
+                            first_part(i, ca, cbuf, b + 2);
+                }
+                if (rest < kQBlock) {   // chunks past the end
+                    const i32x4_t none = {0, 0, 0, 0};
+                    if (16 * g >= rest) fb[cur].half[0] = none;
+                    if (64 + 16 * g >= rest) fb[cur].half[1] = none;
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                f32x4_t p[FN];
+#pragma unroll
+                for (int i = 0; i < FN; ++i) p[i] = block_product<EXACT>(fa[i], fb[cur]);
+                const float f = sc[cur] * w;
+#pragma unroll
+                for (int i = 0; i < FN; ++i) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[i][r], f, acc[i][j][r]);
+                    __asm__("" : "+v"(acc[i][j]));   // here, not where the sum is next read
+                }
                 __builtin_amdgcn_sched_barrier(0);
                 if constexpr (j + 1 == NJ) {
-                    if (more) {
-#pragma unroll
-                        for (int i = 0; i < FN; ++i) fa[i] = read_a(na, i);
-                        fb[0] = read_b(nbuf, 0);
-                        sc[0] = ns[16 * wm + rl];
-                    }
+                    if (more) first_reads(na, nbuf, ns);
                 }
             });
         };
         for (int b = 0; b < nb; b += 2) {
-            stage(sa0, sb0, ss0, sa1, sb1, ss1, sa0, sb0, ss0, b);
-            if (b + 1 < nb) stage(sa1, sb1, ss1, sa0, sb0, ss0, sa1, sb1, ss1, b + 1);
+            stage(sa0, sb0, ss0, sa1, sb1, ss1, b);
+            if (b + 1 < nb) stage(sa1, sb1, ss1, sa0, sb0, ss0, b + 1);
         }
-        add(std::integral_constant<int, NJ - 1>{}, 1);
     };
 
     Fp8Tile cur = decode(L);
     setup(cur);
-    issue(sa0, sb0, ss0);
+    issue_tile();
     while (true) {
         // 16-row blocks wm, wm + 2, .. of the tile that hold rows
         const int blocks = (cur.valid + 15) >> 4, mine = max(0, (blocks - wm + 1) / 2);
         // a wave without rows still takes part in the loads and barriers
-        if (mine > 6) kloop(std::integral_constant<int, 8>{}, cur);
-        else if (mine > 4) kloop(std::integral_constant<int, 6>{}, cur);
-        else if (mine > 2) kloop(std::integral_constant<int, 4>{}, cur);
-        else kloop(std::integral_constant<int, 2>{}, cur);
+        static_for8<1, FM / 2 + 1>([&](auto H_) __attribute__((always_inline)) {
+            constexpr int h = decltype(H_)::value;
+            if (max(1, (mine + 1) / 2) == h) kloop(std::integral_constant<int, 2 * h>{}, cur);
+        });
 
         L += nloc;
         const bool has_next = L < L_end;
@@ -279,10 +348,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
         if (has_next) {
             nxt = decode(L);
             setup(nxt);
-            issue(sa0, sb0, ss0);
+            issue_tile();
         }
         // ---- results: 16 rows of 64 columns at a time through the wave's LDS, so that a
         // store covers whole runs of a row.  A wave's LDS operations complete in order.
+        // (places from the lane number are made anew for every tile: kept over the K loop,
+        // they would take registers that it needs)
+        int ln = lane;
+        __asm__ volatile("" : "+v"(ln));
+        const int el = ln & 15, eg = ln >> 4;
         uint8_t* __restrict__ ep = ep_lds + wv * 16 * kEpRow;
         const int n0 = cur.n0 + wn0;
 #pragma unroll
@@ -293,11 +367,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
             if (a.out_bf16) {
 #pragma unroll
                 for (int i = 0; i < FN; ++i)
-                    *reinterpret_cast<uint2*>(ep + rl * kEpRow + (16 * i + 4 * g) * 2) =
+                    *reinterpret_cast<uint2*>(ep + el * kEpRow + (16 * i + 4 * eg) * 2) =
                         make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    const int c = lane + 64 * s, r = c >> 3, q = c & 7;
+                    const int c = ln + 64 * s, r = c >> 3, q = c & 7;
                     const i32x4_t d = *reinterpret_cast<const i32x4_t*>(ep + r * kEpRow + q * 16);
                     if (mb + r < cur.valid && n0 + 8 * q < cols)
                         __builtin_nontemporal_store(
@@ -308,10 +382,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
                 for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
                     for (int i = 2 * hh; i < 2 * hh + 2; ++i)
-                        *reinterpret_cast<f32x4_t*>(ep + rl * kEpRow + ((i - 2 * hh) * 16 + 4 * g) * 4) = acc[i][j];
+                        *reinterpret_cast<f32x4_t*>(ep + el * kEpRow + ((i - 2 * hh) * 16 + 4 * eg) * 4) = acc[i][j];
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        const int c = lane + 64 * s, r = c >> 3, q = c & 7, n = n0 + 32 * hh + 4 * q;
+                        const int c = ln + 64 * s, r = c >> 3, q = c & 7, n = n0 + 32 * hh + 4 * q;
                         const f32x4_t d = *reinterpret_cast<const f32x4_t*>(ep + r * kEpRow + q * 16);
                         if (mb + r < cur.valid && n < cols)
                             __builtin_nontemporal_store(

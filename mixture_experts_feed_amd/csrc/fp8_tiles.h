@@ -219,9 +219,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
     //
     // A stage takes a step a row block: the LDS reads of the next step, the block's four
     // products, and their sums (by the time the last product is issued the first is done).  All waves meet twice a stage:
-    //   P0(b), before the last step of stage b - 1 (all its reads done): the weights, the
-    //     first half of the rows and the scales of b are there; the second half and the
-    //     scales of b + 1 may be loaded where b - 1 had them;
+    //   P0(b), before the products of the last two steps of stage b - 1 (all its reads
+    //     done): the weights, the first half of the rows and the scales of b are there; the
+    //     second half and the scales of b + 1 may be loaded where b - 1 had them;
     //   P1(b), once the weights (read into registers at once) and the first half of b are
     //     read: its second half is there; the weights and the first half of b + 2 may be
     //     loaded in their place.
@@ -230,9 +230,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
     // every wave.
     auto kloop = [&](auto NJ_, const Fp8Tile& t) __attribute__((always_inline)) {
         constexpr int NJ = decltype(NJ_)::value;
-        constexpr int HALF = FM / 2, MEET = NJ > HALF ? HALF - 1 : NJ - 2;   // step of P1
+        // steps before the last two; the one of them that P1 is in (none: it is with P0)
+        constexpr int HALF = FM / 2, EARLY = NJ - 2, MEET = NJ > HALF ? HALF - 1 : EARLY;
         constexpr int PER2 = MEET > 0 ? (SECOND + MEET - 1) / MEET : SECOND;
-        constexpr int PER1 = (FIRST + NJ - 2 - MEET) / (NJ - 1 - MEET);
+        constexpr int PER1 = MEET < EARLY ? (FIRST + EARLY - MEET - 1) / (EARLY - MEET) : FIRST;
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -249,16 +250,12 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
             else wait_loads<0>();
             barrier_only();
         };
-        auto first_reads = [&](const uint8_t* __restrict__ na, const uint8_t* __restrict__ nbuf,
-                               const float* __restrict__ ns) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < FN; ++i) fa[i] = read_a(na, i);
-            fb[0] = read_b(nbuf, 0);
-            sc[0] = ns[16 * wm + rl];
-            ws = ns[256 + 64 * (wv % WN) + lane];
-        };
         meet0(0);
-        first_reads(sa0, sb0, ss0);
+#pragma unroll
+        for (int i = 0; i < FN; ++i) fa[i] = read_a(sa0, i);
+        fb[0] = read_b(sb0, 0);
+        sc[0] = ss0[16 * wm + rl];
+        ws = ss0[256 + 64 * (wv % WN) + lane];
         // (turns of the double buffers: NJ is even)
         auto stage = [&](uint8_t* __restrict__ ca, uint8_t* __restrict__ cbuf, float* __restrict__ cs,
                          uint8_t* __restrict__ na, uint8_t* __restrict__ nbuf, float* __restrict__ ns,
@@ -266,61 +263,87 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
             const bool more = b + 1 < nb;
             const int rest = len - b * kQBlock;   // of the reduction
             const float w = ws;
-            static_for8<0, NJ>([&](auto J_) __attribute__((always_inline)) {
-                constexpr int j = decltype(J_)::value, cur = j & 1;
-                auto next_reads = [&]() __attribute__((always_inline)) {
-                    fb[cur ^ 1] = read_b(cbuf, j + 1);
-                    sc[cur ^ 1] = cs[16 * (2 * (j + 1) + wm) + rl];
-                };
-                if constexpr (j == MEET) {
-                    // (reads of the rows that the loads take the place of come before)
-                    if constexpr (j + 1 < HALF) next_reads();
-                    if constexpr (MEET == 0) {
-                        if (more)
+            auto next_reads = [&](int j) __attribute__((always_inline)) {
+                fb[j & 1] = read_b(cbuf, j);
+                sc[j & 1] = cs[16 * (2 * j + wm) + rl];
+            };
+            auto cut = [&](Frag& v) __attribute__((always_inline)) {   // chunks past the end
+                const i32x4_t none = {0, 0, 0, 0};
+                if (16 * g >= rest) v.half[0] = none;
+                if (64 + 16 * g >= rest) v.half[1] = none;
+            };
+            auto add = [&](f32x4_t& sum, const f32x4_t& v, float f) __attribute__((always_inline)) {
 #pragma unroll
-                            for (int i = 0; i < SECOND; ++i) second_part(i, nbuf, ns, b + 1);
-                    }
+                for (int r = 0; r < 4; ++r) sum[r] = __builtin_fmaf(v[r], f, sum[r]);
+                __asm__("" : "+v"(sum));   // here, not where the sum is next read
+            };
+            auto loads_second = [&](int from, int to) __attribute__((always_inline)) {
+                if (more)
+#pragma unroll
+                    for (int i = from; i < SECOND && i < to; ++i) second_part(i, nbuf, ns, b + 1);
+            };
+            auto loads_first = [&](int from, int to) __attribute__((always_inline)) {
+                if (b + 2 < nb)
+#pragma unroll
+                    for (int i = from; i < FIRST && i < to; ++i) first_part(i, ca, cbuf, b + 2);
+            };
+            static_for8<0, EARLY>([&](auto J_) __attribute__((always_inline)) {
+                constexpr int j = decltype(J_)::value, cur = j & 1;
+                if constexpr (j == MEET) {
+                    // (the next rows are the first of the second half)
+                    if constexpr (MEET == 0) loads_second(0, SECOND);
                     wait_lds();
                     meet1(b);
-                    if constexpr (j + 1 >= HALF) next_reads();
-                } else if constexpr (j + 1 < NJ) {
-                    next_reads();
-                } else if (more) {
-                    wait_lds();
-                    meet0(b + 1);
                 }
-                if constexpr (j < MEET) {
-                    if (more)
-#pragma unroll
-                        for (int i = j * PER2; i < SECOND && i < (j + 1) * PER2; ++i) second_part(i, nbuf, ns, b + 1);
-                }
-                if constexpr (j >= MEET && j + 1 < NJ) {
-                    if (b + 2 < nb)
-#pragma unroll
-                        for (int i = (j - MEET) * PER1; i < FIRST && i < (j - MEET + 1) * PER1; ++i)
-                            first_part(i, ca, cbuf, b + 2);
-                }
-                if (rest < kQBlock) {   // chunks past the end
-                    const i32x4_t none = {0, 0, 0, 0};
-                    if (16 * g >= rest) fb[cur].half[0] = none;
-                    if (64 + 16 * g >= rest) fb[cur].half[1] = none;
-                }
+                next_reads(j + 1);
+                if constexpr (j < MEET) loads_second(j * PER2, (j + 1) * PER2);
+                else loads_first((j - MEET) * PER1, (j - MEET + 1) * PER1);
+                if (rest < kQBlock) cut(fb[cur]);
                 __builtin_amdgcn_sched_barrier(0);
                 f32x4_t p[FN];
 #pragma unroll
                 for (int i = 0; i < FN; ++i) p[i] = block_product<EXACT>(fa[i], fb[cur]);
                 const float f = sc[cur] * w;
 #pragma unroll
-                for (int i = 0; i < FN; ++i) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[i][r], f, acc[i][j][r]);
-                    __asm__("" : "+v"(acc[i][j]));   // here, not where the sum is next read
-                }
+                for (int i = 0; i < FN; ++i) add(acc[i][j], p[i], f);
                 __builtin_amdgcn_sched_barrier(0);
-                if constexpr (j + 1 == NJ) {
-                    if (more) first_reads(na, nbuf, ns);
-                }
             });
+            // The last two steps together, by weight rows: as soon as a fragment of the
+            // weights has met both, the next stage's is read in its place, beside the
+            // products that follow.
+            next_reads(NJ - 1);
+            if constexpr (MEET == EARLY && MEET == 0) loads_second(0, SECOND);
+            wait_lds();
+            if constexpr (MEET == EARLY) {
+                meet1(b);
+                loads_first(0, FIRST);
+            }
+            if (more) meet0(b + 1);
+            if (rest < kQBlock) {
+                cut(fb[0]);
+                cut(fb[1]);
+            }
+            const float f0 = sc[0] * w, f1 = sc[1] * w;
+            f32x4_t p[2][2];
+#pragma unroll
+            for (int i = 0; i <= FN; ++i) {
+                if (i < FN) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    p[i & 1][0] = block_product<EXACT>(fa[i], fb[0]);
+                    p[i & 1][1] = block_product<EXACT>(fa[i], fb[1]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (more) fa[i] = read_a(na, i);
+                }
+                if (i > 0) {
+                    add(acc[i - 1][NJ - 2], p[(i - 1) & 1][0], f0);
+                    add(acc[i - 1][NJ - 1], p[(i - 1) & 1][1], f1);
+                }
+            }
+            if (more) {
+                fb[0] = read_b(nbuf, 0);
+                sc[0] = ns[16 * wm + rl];
+                ws = ns[256 + 64 * (wv % WN) + lane];
+            }
         };
         for (int b = 0; b < nb; b += 2) {
             stage(sa0, sb0, ss0, sa1, sb1, ss1, b);

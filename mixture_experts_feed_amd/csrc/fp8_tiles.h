@@ -130,12 +130,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
     };
     // The loads of a block, in two parts (see the schedule below): weights and the first
     // half of the rows; the scales and the second half.  Always the same number, which
-    // the waits count.  Chunks past the end of the reduction read the row's last chunk
-    // (input gradient, weights: earlier rows) and are made zeros as fragments of the rows;
-    // the other operand's numbers do not matter there, since one that is NaN also stands
-    // in the sums of the same row or column before.
+    // the waits count.  Past the end of the reduction the rows' chunks read zeros; the
+    // weights read their row's last chunk (input gradient: earlier rows), whose numbers do
+    // not matter, since one that is NaN also stands in the sums of the same column before.
     constexpr int FIRST = 4 + BH, SECOND = 1 + BH;
-    auto past = [&](int b) __attribute__((always_inline)) {   // bytes that the lane's chunk starts past the last one
+    auto past = [&](int b) __attribute__((always_inline)) {   // bytes of the lane's chunk past the end
         return (uint32_t)max(0, c16 + 16 + b * kQBlock - len);
     };
     auto load_a = [&](int q, uint8_t* da, int b) __attribute__((always_inline)) {
@@ -152,8 +151,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
     auto load_b = [&](int q, uint8_t* db, int b) __attribute__((always_inline)) {
         uint8_t* dst = db + (wv + NW * q) * 1024;
         const uint32_t off = fresh(b_off[q]);
-        if constexpr (FAR) copy16_to_lds<0>(a.x + b * kQBlock + ((uint64_t)off * (uint32_t)len + (c16 - past(b))), dst);
-        else copy16_to_lds<0>(a.x + b * kQBlock + (off - past(b)), dst);
+        const int k0 = b * kQBlock;
+        if (k0 + kQBlock <= len) {
+            copy16_to_lds<0>(a.x + k0 + (FAR ? (uint64_t)off * (uint32_t)len + c16 : (uint64_t)off), dst);
+        } else {
+            uint64_t p = reinterpret_cast<uint64_t>(a.x + k0 + (FAR ? (uint64_t)off * (uint32_t)len + c16 : (uint64_t)off));
+            p = k0 + c16 < len ? p : reinterpret_cast<uint64_t>(&fp8_zero_chunk);
+            __asm__ volatile("" : "+v"(p));   // not computed where the tail is not
+            copy16_to_lds<0>((const void*)p, dst);
+        }
     };
     auto load_s = [&](float* ds, int b) __attribute__((always_inline)) {
         const uint32_t off = fresh(s_off);
@@ -240,6 +246,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
             for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         Frag fa[FN], fb[2];
         float sc[2], ws;       // row scales, the weights' scale
+        // Products whose sums are not taken yet, two and two: while two are multiplied, the
+        // two before are added, so that neither waits for the other.  p[2] and p[3] are
+        // left over at the end of a step, with their factors g0 and g1.
+        f32x4_t p[4] = {};
+        float g0 = 0.f, g1 = 0.f;
         auto meet0 = [&](int b) __attribute__((always_inline)) {
             if (b + 1 < nb) wait_loads<BH + FIRST>();   // after the scales of b: its second half, the first part of b + 1
             else wait_loads<0>();
@@ -261,16 +272,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
                          uint8_t* __restrict__ na, uint8_t* __restrict__ nbuf, float* __restrict__ ns,
                          int b) __attribute__((always_inline)) {
             const bool more = b + 1 < nb;
-            const int rest = len - b * kQBlock;   // of the reduction
             const float w = ws;
             auto next_reads = [&](int j) __attribute__((always_inline)) {
                 fb[j & 1] = read_b(cbuf, j);
                 sc[j & 1] = cs[16 * (2 * j + wm) + rl];
-            };
-            auto cut = [&](Frag& v) __attribute__((always_inline)) {   // chunks past the end
-                const i32x4_t none = {0, 0, 0, 0};
-                if (16 * g >= rest) v.half[0] = none;
-                if (64 + 16 * g >= rest) v.half[1] = none;
             };
             auto add = [&](f32x4_t& sum, const f32x4_t& v, float f) __attribute__((always_inline)) {
 #pragma unroll
@@ -289,29 +294,43 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
             };
             static_for8<0, EARLY>([&](auto J_) __attribute__((always_inline)) {
                 constexpr int j = decltype(J_)::value, cur = j & 1;
+                // this step's reads, issued a step ago (waited for by themselves: with loads
+                // into LDS in between, the compiler would wait for the next ones too)
+                wait_lds();
                 if constexpr (j == MEET) {
-                    // (the next rows are the first of the second half)
                     if constexpr (MEET == 0) loads_second(0, SECOND);
-                    wait_lds();
                     meet1(b);
                 }
+                __builtin_amdgcn_sched_barrier(0);
                 next_reads(j + 1);
                 if constexpr (j < MEET) loads_second(j * PER2, (j + 1) * PER2);
                 else loads_first((j - MEET) * PER1, (j - MEET + 1) * PER1);
-                if (rest < kQBlock) cut(fb[cur]);
-                __builtin_amdgcn_sched_barrier(0);
-                f32x4_t p[FN];
-#pragma unroll
-                for (int i = 0; i < FN; ++i) p[i] = block_product<EXACT>(fa[i], fb[cur]);
                 const float f = sc[cur] * w;
-#pragma unroll
-                for (int i = 0; i < FN; ++i) add(acc[i][j], p[i], f);
+                __builtin_amdgcn_sched_barrier(0);
+                p[0] = block_product<EXACT>(fa[0], fb[cur]);
+                p[1] = block_product<EXACT>(fa[1], fb[cur]);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (j == 0) {
+                    add(acc[3][NJ - 2], p[2], g0);
+                    add(acc[3][NJ - 1], p[3], g1);
+                } else {
+                    add(acc[2][j - 1], p[2], g0);
+                    add(acc[3][j - 1], p[3], g0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                p[2] = block_product<EXACT>(fa[2], fb[cur]);
+                p[3] = block_product<EXACT>(fa[3], fb[cur]);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (j + 1 == EARLY) next_reads(NJ - 1);
+                add(acc[0][j], p[0], f);
+                add(acc[1][j], p[1], f);
+                g0 = f;
                 __builtin_amdgcn_sched_barrier(0);
             });
             // The last two steps together, by weight rows: as soon as a fragment of the
             // weights has met both, the next stage's is read in its place, beside the
             // products that follow.
-            next_reads(NJ - 1);
+            if constexpr (EARLY == 0) next_reads(NJ - 1);
             if constexpr (MEET == EARLY && MEET == 0) loads_second(0, SECOND);
             wait_lds();
             if constexpr (MEET == EARLY) {
@@ -319,26 +338,28 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
                 loads_first(0, FIRST);
             }
             if (more) meet0(b + 1);
-            if (rest < kQBlock) {
-                cut(fb[0]);
-                cut(fb[1]);
-            }
             const float f0 = sc[0] * w, f1 = sc[1] * w;
-            f32x4_t p[2][2];
 #pragma unroll
-            for (int i = 0; i <= FN; ++i) {
-                if (i < FN) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    p[i & 1][0] = block_product<EXACT>(fa[i], fb[0]);
-                    p[i & 1][1] = block_product<EXACT>(fa[i], fb[1]);
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (more) fa[i] = read_a(na, i);
-                }
+            for (int i = 0; i < FN; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                p[2 * (i & 1)] = block_product<EXACT>(fa[i], fb[0]);
+                p[2 * (i & 1) + 1] = block_product<EXACT>(fa[i], fb[1]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (more) fa[i] = read_a(na, i);
                 if (i > 0) {
-                    add(acc[i - 1][NJ - 2], p[(i - 1) & 1][0], f0);
-                    add(acc[i - 1][NJ - 1], p[(i - 1) & 1][1], f1);
+                    add(acc[i - 1][NJ - 2], p[2 * (1 - (i & 1))], f0);
+                    add(acc[i - 1][NJ - 1], p[2 * (1 - (i & 1)) + 1], f1);
+                } else if constexpr (EARLY > 0) {
+                    add(acc[2][EARLY - 1], p[2], g0);
+                    add(acc[3][EARLY - 1], p[3], g0);
+                } else {
+                    add(acc[3][NJ - 2], p[2], g0);
+                    add(acc[3][NJ - 1], p[3], g1);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
+            g0 = f0;
+            g1 = f1;
             if (more) {
                 fb[0] = read_b(nbuf, 0);
                 sc[0] = ns[16 * wm + rl];
@@ -348,6 +369,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
         for (int b = 0; b < nb; b += 2) {
             stage(sa0, sb0, ss0, sa1, sb1, ss1, b);
             if (b + 1 < nb) stage(sa1, sb1, ss1, sa0, sb0, ss0, b + 1);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            acc[3][NJ - 2][r] = __builtin_fmaf(p[2][r], g0, acc[3][NJ - 2][r]);
+            acc[3][NJ - 1][r] = __builtin_fmaf(p[3][r], g1, acc[3][NJ - 1][r]);
         }
     };
 

@@ -169,13 +169,24 @@ Fp8Args fp8_args(const Fp8Params& p) {
     return a;
 }
 
-// Few rows an expert: the weights are streamed.
-#ifndef SMAX
-#define SMAX 48LL
-#endif
-bool fp8_streams(const Fp8Params& p) { return !p.input_grad && (long long)p.rows <= SMAX * p.E; }
-
-int stream_cols(const Fp8Params& p) { return (long long)p.E * ((p.N + 63) / 64) >= 512 ? 64 : 16; }
+// The forward streams the weights (fp8_stream.h) where experts have few rows; 256-row
+// tiles otherwise, whose stages without rows cost little: 5.5 TB/s of weights at 2 to 48
+// rows an expert.  us, streamed against tiles (E experts of r rows, K x N):
+// - up to 8 rows and K from 2048 on: 387 / 465 at 128 x 2 (6144 x 4096), 79 / 98 at 128 x
+//   2 and 100 / 106 at 128 x 8 (2048 x 2048), 75 / 110 at 64 x 2 (4096 x 2048), 36 / 39 at
+//   64 x 2 (2048 x 1536); 22 / 14 at 64 x 2 (1024 x 1024);
+// - up to 16 rows and K from 4096 on: 547 / 574 at 128 x 16 (6144 x 4096), 104 / 135 at 16
+//   x 16 (6144 x 6144); 121 / 106 at 128 x 16 (2048 x 2048), 655 / 581 at 128 x 24 (6144 x
+//   4096);
+// - up to 48 rows where fewer than 64 tiles would run, K from 1024 on: 12 / 43 at one
+//   expert of 1 row and 21 / 43 of 40 (6144 x 4096), 9 / 18 of 1 (2048 x 2048), 9 / 11 of 1
+//   (1024 x 1024); 9 / 8 at 512 x 512, and 39 / 32 at 4 x 40 (4096 x 4096, 64 tiles).
+bool fp8_streams(const Fp8Params& p) {
+    if (p.input_grad) return false;
+    const long long rows = p.rows, E = p.E;
+    if (E * ((p.N + 255) / 256) < 64) return p.K >= 1024 && rows <= 48 * E;
+    return rows <= (p.K >= 4096 ? 16 : p.K >= 2048 ? 8 : 0) * E;
+}
 
 // fp32 results take tiles of 128 rows: the conversions need the registers.
 int tile_rows(const Fp8Params& p) { return p.out_bf16 ? 256 : 128; }
@@ -189,23 +200,32 @@ void launch_tiles(const Fp8Args& a, int grid, hipStream_t stream) {
 }
 
 template <int BN, int NW, int DEPTH, int FM>
-void launch_stream_as(const Fp8Args& a, hipStream_t stream) {
+void launch_stream_as(const Fp8Args& a, int per_cu, hipStream_t stream) {
     const long long tasks = ((long long)(a.rows + 16 * FM - 1) / (16 * FM) + a.E) * ((a.N + BN - 1) / BN);
-    const dim3 grid((unsigned)std::min<long long>(tasks, device_cu_count())), block(NW * 64);
+    const dim3 grid((unsigned)std::min<long long>(tasks, (long long)device_cu_count() * per_cu)), block(NW * 64);
     if (a.out_bf16) hipLaunchKernelGGL((fp8_stream_kernel<BN, NW, DEPTH, FM, false>), grid, block, 0, stream, a);
     else hipLaunchKernelGGL((fp8_stream_kernel<BN, NW, DEPTH, FM, true>), grid, block, 0, stream, a);
 }
 
-void launch_stream(const Fp8Args& a, int cols, hipStream_t stream) {
+// Columns of a task: 64 where that gives every CU two, else 16, for which eight waves
+// share out a long reduction where every CU has a task or two, otherwise four (four
+// workgroups a CU).  Rows of a task: 16, 32 or 64, so that few experts have more (their
+// weights are read again).
+void launch_stream(const Fp8Args& a, hipStream_t stream) {
     const double mean = (double)a.rows / a.E;
-    if (cols == 64) {
-        if (mean <= 8.0) launch_stream_as<64, 4, 4, 1>(a, stream);
-        else if (mean <= 20.0) launch_stream_as<64, 4, 4, 2>(a, stream);
-        else launch_stream_as<64, 4, 4, 4>(a, stream);
+    const int fm = mean <= (a.E == 1 ? 16.0 : 8.0) ? 1 : mean <= (a.E == 1 ? 32.0 : 20.0) ? 2 : 4;
+    if ((long long)a.E * ((a.N + 63) / 64) >= 2LL * device_cu_count()) {
+        // (at least 64 tiles of 256 columns then, so at most 16 rows)
+        if (fm == 1) launch_stream_as<64, 4, 4, 1>(a, 1, stream);
+        else launch_stream_as<64, 4, 4, 2>(a, 1, stream);
+    } else if (a.K > 24 * kQBlock && (long long)a.E * ((a.N + 15) / 16) < 2LL * device_cu_count()) {
+        if (fm == 1) launch_stream_as<16, 8, 6, 1>(a, 1, stream);
+        else if (fm == 2) launch_stream_as<16, 8, 6, 2>(a, 1, stream);
+        else launch_stream_as<16, 8, 4, 4>(a, 1, stream);
     } else {
-        if (mean <= (a.E == 1 ? 16.0 : 8.0)) launch_stream_as<16, 8, 6, 1>(a, stream);
-        else if (mean <= (a.E == 1 ? 32.0 : 20.0)) launch_stream_as<16, 8, 6, 2>(a, stream);
-        else launch_stream_as<16, 8, 4, 4>(a, stream);
+        if (fm == 1) launch_stream_as<16, 4, 4, 1>(a, 4, stream);
+        else if (fm == 2) launch_stream_as<16, 4, 4, 2>(a, 4, stream);
+        else launch_stream_as<16, 4, 4, 4>(a, 4, stream);
     }
 }
 
@@ -251,7 +271,7 @@ hipError_t launch_quantize_weight(int dtype, const void* w, int E, int N, int K,
 hipError_t launch_fp8_product(const Fp8Params& p, hipStream_t stream) {
     const Fp8Args a = fp8_args(p);
     if (fp8_streams(p)) {
-        launch_stream(a, stream_cols(p), stream);
+        launch_stream(a, stream);
         return hipGetLastError();
     }
     const long long tiles = max_tiles(p);

@@ -294,6 +294,49 @@ def test_dense(R, out_dtype):
            _reference("linear", x, xs, w, ws, [0, R + 3], out_dtype, idx), [0, R + 3])
 
 
+@pytest.mark.parametrize("E,N,K,mean", [
+    (512, 64, 2064, 2), (512, 64, 2064, 8), (512, 64, 4112, 12), (512, 80, 4096, 16),   # 64 columns a task
+    (3, 208, 4112, 1), (3, 208, 4112, 7), (3, 208, 4112, 15), (2, 1040, 5136, 45),      # 16, eight waves
+    (40, 256, 4112, 5), (5, 640, 1040, 3), (5, 640, 1040, 18), (5, 640, 1040, 40),      # 16, four waves
+    (1, 64, 1024, 16), (1, 64, 1024, 17), (1, 64, 1024, 33), (1, 64, 4096, 48),
+])
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+def test_streamed(E, N, K, mean, out_dtype):
+    """Few rows an expert: uneven, some without rows, some with more than a task takes."""
+    _say(f"streamed E={E} N={N} K={K} mean {mean} {out_dtype}")
+    rng = np.random.default_rng(E + K + mean)
+    p = rng.random(E) ** 3 + 1e-3
+    p[0] = 0.0 if E > 1 else 1.0
+    counts = rng.multinomial(mean * E, p / p.sum())
+    ends, R = _rows(counts.tolist(), 0, 0)
+    w, ws = _weight(E, N, K)
+    X = max(1, R // 2)
+    x, xs = _fp8((X, K), 5), _scales((X, -(-K // 128)), 6)
+    index = torch.randint(0, X, (R,), dtype=torch.int32, device=DEV)
+    off = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    out = torch.full((R + 2, N), MARK, dtype=out_dtype, device=DEV)
+    B.fp8_grouped_linear(x, xs, w, ws, off, row_index=torch.cat([index, index[:1], index[:1]]), out=out)
+    keep = sorted({0, 1, 2, E // 2, E - 1, int(np.argmax(counts))} & set(range(E)))   # the others are alike
+    for e in keep:
+        part = _reference("linear", x, xs, w[e:e + 1], ws[e:e + 1], ends[e:e + 2], out_dtype, index)
+        for (a, b), want, bound in part:
+            assert bool(((out[a:b].double() - want).abs() <= bound).all()), (e, counts[e])
+    assert bool((out[R:] == MARK).all())
+    again = torch.full_like(out, MARK)
+    B.fp8_grouped_linear(x, xs, w, ws, off, row_index=torch.cat([index, index[:1], index[:1]]), out=again)
+    assert torch.equal(out, again)
+    # every expert against the same rows one by one
+    some = rng.integers(0, R, 20)
+    one = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    for r in some:
+        e = int(np.searchsorted(ends, r, side="right")) - 1
+        one.zero_()
+        one[e + 1:] = 1
+        single = B.fp8_grouped_linear(x, xs, w, ws, one, row_index=index[r:r + 1].contiguous(), out_dtype=F32)
+        scale = float(single.abs().max())
+        assert float((single[0] - out[r].float()).abs().max()) <= 2.0 ** -7 * scale, (r, e)
+
+
 @pytest.mark.parametrize("rows", [40, 1200])
 def test_many_groups(rows):
     """512 groups, most of them empty."""

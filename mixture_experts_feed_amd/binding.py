@@ -905,6 +905,10 @@ def expert_order(topk_indices: torch.Tensor, n_routed: int, padding_mask: Option
             raise ValueError("padding_mask must hold a value for each token")
     dims, need = _order_plan(T, n_routed, k)
     i32 = torch.int32
+    if expert_counts is None and expert_offsets is None and sorted_slots is None:
+        # one buffer for the three (cheaper than three)
+        expert_counts, expert_offsets, sorted_slots = topk_indices.new_empty(
+            (2 * n_routed + 1 + T * k,)).split_with_sizes((n_routed, n_routed + 1, T * k))
     res = {"expert_counts": _result(expert_counts, "expert_counts", (n_routed,), i32, dev),
            "expert_offsets": _result(expert_offsets, "expert_offsets", (n_routed + 1,), i32, dev),
            "sorted_slots": _result(sorted_slots, "sorted_slots", (T * k,), i32, dev),

@@ -301,10 +301,11 @@ __global__ __launch_bounds__(256) void gather_kernel(const MoveArgs a) {
 // With the weights' gradient: a whole token by G lanes, or (G == 256) by a
 // workgroup.  SPREAD: also rows_out[p] = w x (where rows_out is given); otherwise
 // also token_out = sum w rows.  Sums over the lanes in a fixed order.
-template <typename TT, typename TR, int V, int G, bool SPREAD>
+// kMaxSlots: 8 or 32 (with 32 running sums a lane the fp32 gradients of 1001 x 1237,
+// top-2, took 27 us for both operators' kernels instead of 10).
+template <typename TT, typename TR, int V, int G, int kMaxSlots, bool SPREAD>
 __global__ __launch_bounds__(256) void dweights_kernel(const MoveArgs a) {
-    __shared__ float part[4][32];
-    constexpr int kMaxSlots = 32;
+    __shared__ float part[4][kMaxSlots];
     const int sub = threadIdx.x % G;
     long long t = (long long)blockIdx.x * (256 / G) + threadIdx.x / G;
     if constexpr (G == kWave) t = (long long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -351,6 +352,7 @@ __global__ __launch_bounds__(256) void dweights_kernel(const MoveArgs a) {
                     }
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);   // the next slots' rows in these ones' registers
         }
         if constexpr (!SPREAD) store_row<TT, V, false>(static_cast<TT*>(a.token_out) + (size_t)t * a.H + col, acc);
     }
@@ -375,22 +377,28 @@ __global__ __launch_bounds__(256) void dweights_kernel(const MoveArgs a) {
 template <typename TT, typename TR>
 constexpr int move_cols() { return sizeof(TT) == 2 && sizeof(TR) == 2 ? 8 : 4; }
 
+template <typename TT, typename TR, int V, int G, int SLOTS>
+void launch_dweights(const MoveArgs& a, bool spread, hipStream_t stream) {
+    const long long per = 256 / G;
+    const dim3 grid((unsigned)((a.T + per - 1) / per)), block(256);
+    if (spread) hipLaunchKernelGGL((dweights_kernel<TT, TR, V, G, SLOTS, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((dweights_kernel<TT, TR, V, G, SLOTS, false>), grid, block, 0, stream, a);
+}
+
 template <typename TT, typename TR, int V, int G>
 hipError_t launch_move_as(MoveArgs a, bool spread, hipStream_t stream) {
     a.nv = (a.H + V - 1) / V;
     if (a.dweights != nullptr) {
-        const long long per = 256 / G;
-        const bool wide = G == kWave && a.nv > kWave;   // more than a vector a lane: a workgroup a token
-        const dim3 grid((unsigned)(wide ? a.T : (a.T + per - 1) / per)), block(256);
-        if constexpr (G == kWave) {
-            if (wide) {
-                if (spread) hipLaunchKernelGGL((dweights_kernel<TT, TR, V, 256, true>), grid, block, 0, stream, a);
-                else hipLaunchKernelGGL((dweights_kernel<TT, TR, V, 256, false>), grid, block, 0, stream, a);
-                return hipGetLastError();
-            }
+        // more than a vector a lane of a wave: a workgroup a token
+        constexpr int WIDE = G == kWave ? 256 : G;
+        const bool wide = a.nv > G;
+        if (a.k <= 8) {
+            if (wide) launch_dweights<TT, TR, V, WIDE, 8>(a, spread, stream);
+            else launch_dweights<TT, TR, V, G, 8>(a, spread, stream);
+        } else {
+            if (wide) launch_dweights<TT, TR, V, WIDE, 32>(a, spread, stream);
+            else launch_dweights<TT, TR, V, G, 32>(a, spread, stream);
         }
-        if (spread) hipLaunchKernelGGL((dweights_kernel<TT, TR, V, G, true>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((dweights_kernel<TT, TR, V, G, false>), grid, block, 0, stream, a);
         return hipGetLastError();
     }
     const long long units = a.T * ((a.nv + G - 1) / G), per = 256 / G;

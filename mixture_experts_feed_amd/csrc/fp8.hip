@@ -8,7 +8,9 @@
 // 2^-10 2^e below.  A block with an infinity or a NaN gets a NaN scale and zeros, so that
 // every product with it is NaN.  One read and one write: HBM bounds both kernels.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
+#include <utility>
 
 #include "common.h"
 #include "fp8_common.h"
@@ -180,16 +182,47 @@ Fp8Args fp8_args(const Fp8Params& p) {
 //   4096);
 // - up to 48 rows where fewer than 64 tiles would run, K from 1024 on: 12 / 43 at one
 //   expert of 1 row and 21 / 43 of 40 (6144 x 4096), 9 / 18 of 1 (2048 x 2048), 9 / 11 of 1
-//   (1024 x 1024); 9 / 8 at 512 x 512, and 39 / 32 at 4 x 40 (4096 x 4096, 64 tiles).
+//   (1024 x 1024); 9 / 8 at 512 x 512, and 39 / 32 at 4 x 40 (4096 x 4096, 64 tiles);
+// - any number where 64 x 64 tasks give a CU two at most (a tile's stages wait for their
+//   loads, and few CUs have one), K from 2048 on: 29 / 58 at one expert of 128 rows and 51 /
+//   77 of 512 (6144 x 4096), 17 / 31 of 512 (2048 x 2048), 26 / 31 at 4 x 200 (2048 x 2048),
+//   24 / 32 at 16 x 30 (4096 x 1024); 96 / 79 at one of 1024 (6144 x 4096), 16 / 15 at 8 x
+//   100 (1024 x 1024), 27 / 23 at 16 x 64 (2048 x 1024).
+long long tasks64(const Fp8Params& p) { return (((long long)p.rows + 63) / 64 + p.E - 1) * ((p.N + 63) / 64); }
+
 bool fp8_streams(const Fp8Params& p) {
     if (p.input_grad) return false;
     const long long rows = p.rows, E = p.E;
+    if (p.K >= 2048 && E <= (p.K >= 4096 ? 16 : 8) && tasks64(p) <= 2LL * device_cu_count()) return true;
     if (E * ((p.N + 255) / 256) < 64) return p.K >= 1024 && rows <= 48 * E;
     return rows <= (p.K >= 4096 ? 16 : p.K >= 2048 ? 8 : 0) * E;
 }
 
-// fp32 results take tiles of 128 rows: the conversions need the registers.
-int tile_rows(const Fp8Params& p) { return p.out_bf16 ? 256 : 128; }
+// Rows of a tile.  fp32 results take 128: the conversions need the registers.  Otherwise
+// 256, or less where that leaves the last of few rounds of the grid nearly empty: of 256,
+// 192, 128 and 64 what takes least by rounds times a stage's time (8192 x 8192 x 8192:
+// 2.07, 1.64, 1.30, 0.91 us).  The experts' last tiles are half full on average.  us,
+// against 256 rows: 150 / 167 for 16 experts of 8192 uneven rows (input gradient, 2048
+// columns from 6144), 38 / 58 for one of 512 (6144 from 4096), 99 / 113 for 4 of 1000 (4096 x
+// 4096); 73 / 64 for 32 of 300 (2048 x 2048), whose rounds come out differently.
+int tile_rows(const Fp8Params& p) {
+    if (!p.out_bf16) return 128;
+    const double cus = device_cu_count(), ntn = ((p.input_grad ? p.K : p.N) + 255) / 256;
+    int best = 256;
+    double least = 0.0;
+    for (const auto& c : {std::pair<int, double>{256, 2.07}, {192, 1.64}, {128, 1.30}, {64, 0.91}}) {
+        const double tiles = p.E == 1 ? (p.rows + c.first - 1) / c.first : (double)p.rows / c.first + 0.5 * p.E;
+        const double rounds = std::ceil(tiles * ntn / cus);
+        if (c.first == 256) {
+            least = rounds * c.second;
+            if (rounds > 2.0) break;   // more rounds even out
+        } else if (rounds * c.second < least) {
+            least = rounds * c.second;
+            best = c.first;
+        }
+    }
+    return best;
+}
 
 template <int FM, bool KN, bool EXACT>
 void launch_tiles(const Fp8Args& a, int grid, hipStream_t stream) {
@@ -207,21 +240,21 @@ void launch_stream_as(const Fp8Args& a, int per_cu, hipStream_t stream) {
     else hipLaunchKernelGGL((fp8_stream_kernel<BN, NW, DEPTH, FM, true>), grid, block, 0, stream, a);
 }
 
-// Columns of a task: 64 where that gives every CU two, else 16, for which eight waves
-// share out a long reduction where every CU has a task or two, otherwise four (four
-// workgroups a CU).  Rows of a task: 16, 32 or 64, so that few experts have more (their
-// weights are read again).
-void launch_stream(const Fp8Args& a, hipStream_t stream) {
+// Rows of a task: 16, 32 or 64, so that few experts have more (their weights are read
+// again).  Columns: 64 where that gives every CU two tasks (with 64 rows: every second CU
+// one), else 16, for which eight waves share out a long reduction where every CU has a
+// task or two, otherwise four (four workgroups a CU).
+void launch_stream(const Fp8Params& p, const Fp8Args& a, hipStream_t stream) {
     const double mean = (double)a.rows / a.E;
+    const long long cus = device_cu_count(), E = a.E;
     const int fm = mean <= (a.E == 1 ? 16.0 : 8.0) ? 1 : mean <= (a.E == 1 ? 32.0 : 20.0) ? 2 : 4;
-    if ((long long)a.E * ((a.N + 63) / 64) >= 2LL * device_cu_count()) {
-        // (at least 64 tiles of 256 columns then, so at most 16 rows)
+    if (fm < 4 ? E * ((a.N + 63) / 64) >= 2 * cus : 2 * tasks64(p) >= cus) {
         if (fm == 1) launch_stream_as<64, 4, 4, 1>(a, 1, stream);
-        else launch_stream_as<64, 4, 4, 2>(a, 1, stream);
-    } else if (a.K > 24 * kQBlock && (long long)a.E * ((a.N + 15) / 16) < 2LL * device_cu_count()) {
+        else if (fm == 2) launch_stream_as<64, 4, 4, 2>(a, 1, stream);
+        else launch_stream_as<64, 4, 4, 4>(a, 1, stream);
+    } else if (a.K > 24 * kQBlock && fm < 4 && E * ((a.N + 15) / 16) < 2 * cus) {
         if (fm == 1) launch_stream_as<16, 8, 6, 1>(a, 1, stream);
-        else if (fm == 2) launch_stream_as<16, 8, 6, 2>(a, 1, stream);
-        else launch_stream_as<16, 8, 4, 4>(a, 1, stream);
+        else launch_stream_as<16, 8, 6, 2>(a, 1, stream);
     } else {
         if (fm == 1) launch_stream_as<16, 4, 4, 1>(a, 4, stream);
         else if (fm == 2) launch_stream_as<16, 4, 4, 2>(a, 4, stream);
@@ -231,7 +264,8 @@ void launch_stream(const Fp8Args& a, hipStream_t stream) {
 
 // tiles of a launch, at most
 long long max_tiles(const Fp8Params& p) {
-    return (((long long)p.rows + tile_rows(p) - 1) / tile_rows(p) + p.E) * (((p.input_grad ? p.K : p.N) + 255) / 256);
+    const int rows = tile_rows(p);
+    return (((long long)p.rows + rows - 1) / rows + p.E) * (((p.input_grad ? p.K : p.N) + 255) / 256);
 }
 
 }  // namespace
@@ -269,11 +303,12 @@ hipError_t launch_quantize_weight(int dtype, const void* w, int E, int N, int K,
 }
 
 hipError_t launch_fp8_product(const Fp8Params& p, hipStream_t stream) {
-    const Fp8Args a = fp8_args(p);
+    Fp8Args a = fp8_args(p);
     if (fp8_streams(p)) {
-        launch_stream(a, stream);
+        launch_stream(p, a, stream);
         return hipGetLastError();
     }
+    a.tile_rows = tile_rows(p);
     const long long tiles = max_tiles(p);
     const int grid = ((int)std::min<long long>(tiles, device_cu_count()) + 7) / 8 * 8;
     if (p.input_grad) {

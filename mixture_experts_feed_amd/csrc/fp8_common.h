@@ -80,15 +80,16 @@ struct Fp8Args {
     void* out;                    // [rows][cols], cols = N or K
     int rows, x_rows, E, N, K;
     int out_bf16;
+    int tile_rows;                // rows of a tile (fp8_tiles.h), a multiple of 64
 };
 
 constexpr int kMaxFp8Groups = 512;
 
-// The experts' rows and row tiles of BM, found from the caller's offsets by the whole
+// The experts' rows and row tiles of bm, found from the caller's offsets by the whole
 // workgroup: offs[0 .. E] clamped to [0, rows], each at least the largest before it;
 // first[e] = row tiles of the experts before e.  Ends with a barrier.
-template <int THREADS, int BM>
-__device__ __forceinline__ void plan_experts(const Fp8Args& a, int32_t* offs, int32_t* first) {
+template <int THREADS>
+__device__ __forceinline__ void plan_experts(const Fp8Args& a, int bm, int32_t* offs, int32_t* first) {
     constexpr int PER = kMaxFp8Groups / THREADS, NW = THREADS / kWave;
     static_assert(PER >= 1 && PER * THREADS == kMaxFp8Groups, "a thread takes PER experts");
     __shared__ int32_t wave_max[NW], wave_sum[NW];
@@ -97,7 +98,7 @@ __device__ __forceinline__ void plan_experts(const Fp8Args& a, int32_t* offs, in
         if (tid == 0) {
             offs[0] = first[0] = 0;
             offs[1] = a.rows;
-            first[1] = (a.rows + BM - 1) / BM;
+            first[1] = (a.rows + bm - 1) / bm;
         }
         __syncthreads();
         return;
@@ -128,7 +129,7 @@ __device__ __forceinline__ void plan_experts(const Fp8Args& a, int32_t* offs, in
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         end[i] = max(end[i], before);
-        tiles[i] = tid * PER + i < a.E ? (end[i] - begin + BM - 1) / BM : 0;
+        tiles[i] = tid * PER + i < a.E ? (end[i] - begin + bm - 1) / bm : 0;
         begin = end[i];
         sum += tiles[i];
     }

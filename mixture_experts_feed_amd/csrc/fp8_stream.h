@@ -88,7 +88,7 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void fp8_stream_kernel(const Fp8Ar
     const int kb = (a.K + kQBlock - 1) / kQBlock;
     // blocks of a task for each wave, the missing ones as zeros
     const int steps = ((kb + NW - 1) / NW + DEPTH - 1) / DEPTH * DEPTH;
-    plan_experts<THREADS, BM>(a, offs, first);
+    plan_experts<THREADS>(a, BM, offs, first);
     const int total = first[a.E] * ntn;
     if ((int)blockIdx.x >= total) return;
 

@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
     const int ntn = (cols + BN - 1) / BN;
 
     // ---- the experts' rows and row tiles -----------------------------------------
-    plan_experts<kTileThreads, BM>(a, offs, first);
+    plan_experts<kTileThreads>(a, a.tile_rows, offs, first);
     const long long total = (long long)first[a.E] * ntn;
     const int xcd = blockIdx.x & 7, nloc = gridDim.x >> 3;
     const int L_end = (int)(total * (xcd + 1) / 8);
@@ -74,8 +74,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Fp8Args
         t.e = expert_of(first, a.E, rt);
         const int f = first[t.e], c = first[t.e + 1] - f;
         const int in = l - f * ntn, nt = in / c, mt = in - nt * c;
-        t.row0 = __builtin_amdgcn_readfirstlane(offs[t.e] + mt * BM);
-        t.valid = __builtin_amdgcn_readfirstlane(min(BM, offs[t.e + 1] - t.row0));
+        // the expert's row tiles share its rows evenly, by 64
+        const int rows = offs[t.e + 1] - offs[t.e], per = ((rows + 63) / 64 + c - 1) / c * 64;
+        t.row0 = __builtin_amdgcn_readfirstlane(offs[t.e] + mt * per);
+        t.valid = __builtin_amdgcn_readfirstlane(min(per, rows - mt * per));
         t.n0 = __builtin_amdgcn_readfirstlane(nt * BN);
         return t;
     };

@@ -337,6 +337,50 @@ def test_streamed(E, N, K, mean, out_dtype):
         assert float((single[0] - out[r].float()).abs().max()) <= 2.0 ** -7 * scale, (r, e)
 
 
+def _sampled(counts, seed, each):
+    """Rows of each group, a few of them, its first and last among them; (group, rows)."""
+    rng = np.random.default_rng(seed)
+    a = 0
+    for e, c in enumerate(counts):
+        if c:
+            yield e, torch.from_numpy(np.unique(np.concatenate([[a, a + c - 1], rng.integers(a, a + c, each)]))).to(DEV)
+        a += c
+
+
+@pytest.mark.parametrize("counts,N,K", [
+    ([2000], 1040, 272), ([5120], 1040, 272), ([15360], 1040, 272), ([30001], 1040, 272),   # 64 to 256 rows a tile
+    ([5000, 1, 0, 12345, 12000, 770], 1040, 272), ([1000, 0, 3, 900], 1040, 272), ([8191, 8193], 528, 1040),
+    ([512], 1040, 2064), ([1, 300, 99], 1040, 2064), ([200, 0, 513], 2064, 4112),           # streamed, 64 by 64
+])
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+def test_tall(counts, N, K, out_dtype):
+    """Many rows an expert, against sampled rows; all of them written, none behind them."""
+    _say(f"tall {counts} N={N} K={K} {out_dtype}")
+    E, R = len(counts), sum(counts)
+    ends, _ = _rows(counts, 0, 0)
+    w, ws = _weight(E, N, K)
+    off = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    n_at, k_at = torch.arange(N, device=DEV) // 128, torch.arange(K, device=DEV) // 128
+    X = R // 2 + 1
+    x, xs = _fp8((X, K), 5), _scales((X, -(-K // 128)), 6)
+    index = torch.randint(0, X, (R,), dtype=torch.int32, device=DEV)
+    d, ds = _fp8((R, N), 7), _scales((R, -(-N // 128)), 8)
+    out = torch.full((R + 2, N), MARK, dtype=out_dtype, device=DEV)
+    dx = torch.full((R + 2, K), MARK, dtype=out_dtype, device=DEV)
+    B.fp8_grouped_linear(x, xs, w, ws, off, row_index=torch.cat([index, index[:1], index[:1]]), out=out)
+    B.fp8_grouped_input_grad(torch.cat([d.view(torch.uint8), d[:2].view(torch.uint8)]).view(E4M3),
+                             torch.cat([ds, ds[:2]]), w, ws, off, dx=dx)
+    for e, rows in _sampled(counts, N + K, 60):
+        at = index[rows].long()
+        want, bound = _product(x[at].double(), xs[at].double(), w[e].double(), ws[e].double()[n_at], out_dtype)
+        assert bool(((out[rows].double() - want).abs() <= bound).all()), ("linear", e)
+        want, bound = _product(d[rows].double(), ds[rows].double(), w[e].double().t().contiguous(),
+                               ws[e].double().t()[k_at], out_dtype)
+        assert bool(((dx[rows].double() - want).abs() <= bound).all()), ("input_grad", e)
+    for t in (out, dx):
+        assert bool((t[R:] == MARK).all()) and not bool((t[:R] == MARK).all(1).any())
+
+
 @pytest.mark.parametrize("rows", [40, 1200])
 def test_many_groups(rows):
     """512 groups, most of them empty."""
@@ -481,6 +525,38 @@ def test_past_32_bits():
     want, bound = _product(d.double(), ds.double(), w[E - 1].double().t().contiguous(),
                            ws[E - 1].double().t()[torch.arange(K, device=DEV) // 128], F32)
     assert bool(((dx.double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+def test_rows_past_32_bits(out_dtype):
+    """Read rows past 2^32 bytes, and results past 2^32 values, in many tiles."""
+    _say(f"rows past 32 bits {out_dtype}")
+    R, L, E = 4200000, 1040, 3
+    counts = [1900003, 0, R - 1900003]
+    ends, _ = _rows(counts, 0, 0)
+    off = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    tall = torch.randint(0, 0x70, (R, L), dtype=torch.uint8, device=DEV).view(E4M3)
+    ts = _scales((R, 9), 3)
+    wide = torch.arange(L, device=DEV) // 128
+    w, ws = _weight(E, L, 16)
+    dx = B.fp8_grouped_input_grad(tall, ts, w, ws, off, dx_dtype=out_dtype)
+    w2, w2s = _weight(E, 16, L, 4)
+    index = torch.randint(0, R, (R,), dtype=torch.int32, device=DEV)
+    out = B.fp8_grouped_linear(tall, ts, w2, w2s, off, row_index=index, out_dtype=out_dtype)
+    for e, rows in _sampled(counts, 1, 300):
+        want, bound = _product(tall[rows].double(), ts[rows].double(), w[e].double().t().contiguous(),
+                               ws[e].double().t().expand(16, 9), out_dtype)
+        assert bool(((dx[rows].double() - want).abs() <= bound).all()), ("input_grad", e)
+        at = index[rows].long()
+        want, bound = _product(tall[at].double(), ts[at].double(), w2[e].double(), w2s[e].double().expand(16, 9),
+                               out_dtype)
+        assert bool(((out[rows].double() - want).abs() <= bound).all()), ("linear", e)
+    del dx, out
+    x, xs = _fp8((R, 16), 11), _scales((R, 1), 12)
+    out = B.fp8_grouped_linear(x, xs, w, ws, off, out_dtype=out_dtype)
+    for e, rows in _sampled(counts, 2, 300):
+        want, bound = _product(x[rows].double(), xs[rows].double(), w[e].double(), ws[e].double()[wide], out_dtype)
+        assert bool(((out[rows].double() - want).abs() <= bound).all()), ("results", e)
 
 
 @pytest.mark.parametrize("R", [48, 1500])

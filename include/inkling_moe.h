@@ -509,7 +509,7 @@ int inkling_combine_backward(const inkling_dispatch_dims_t* dims, const void* do
  * Limits (INKLING_ERR_UNSUPPORTED): cols, in_features and out_features multiples of
  * 16 up to 2^20, 1 <= n_groups <= 512, rows and x_rows at most 2^31 - 257, rows *
  * ceil(cols/128) < 2^31 for quantize_rows, fewer than 2^31 - 4096 output tiles of 256
- * x 256, n_groups * ceil(out_features/64) < 2^23.
+ * x 256 (fp32: 128 rows x 256), n_groups * ceil(out_features/64) < 2^23.
  * Tensor pointers 16-byte aligned (scales, row_count, offsets and row_index 4-byte);
  * outputs must not overlap each other or an operand (INKLING_ERR_INVALID_ARGUMENT).
  * No workspace.  rows == 0 is a no-op.

@@ -8,8 +8,8 @@
 // row is that plus its rank among the equal experts of the 64 lanes, from one
 // ballot for each bit of the expert's number.  Integers throughout, so the order
 // depends on nothing but the input.  Up to kOrderOne slots one workgroup does it
-// all in one launch; more take a launch of counts before (two launches: 65536 slots
-// of 128 experts in 64 chunks).
+// all in one launch; more take a launch of counts before (65536 slots of 128 experts in
+// 64 chunks: 4.8 + 6.7 us; 256 slots, one launch: 3.6).  Latency bounds it.
 //
 // Rows and tokens: positions [T][k] hold the row of each slot (-1: none), so both
 // directions go by token, and nothing is summed by atomics:
@@ -17,7 +17,10 @@
 //   gather (combine forward, dispatch backward)  out[t] = add[t] + sum_i w(t,i) rows[p(t,i)]
 //   and where wanted the weights' gradient       dw(t,i) = <x[t], rows[p(t,i)]>.
 // HBM bounds all of them: a token's row is read (or written) once, beside its k
-// rows.  Arithmetic in fp32 in the order of the slots, rounded once.
+// rows.  Arithmetic in fp32 in the order of the slots, rounded once.  A wave takes 64
+// vectors of one token's row, so that up to eight rows' loads are on their way together.
+// 8192 tokens of 6144 bf16, top-8: spread of 7168 tokens 135 us (6.0 TB/s), gather of
+// 65536 rows 159 (5.7), weights' gradient with the rows written 325 (5.3).
 #include <algorithm>
 
 #include "common.h"

@@ -9,6 +9,8 @@
 // anybody until the waves' sums are added in LDS at the end of a task, in the order of
 // the waves.  The loads run ahead over the end of a task, so that the next one's weights
 // are on their way while the sums are added and stored.
+// 128 experts of 2 rows, 6144 x 4096: 385 us (7.2 TB/s of the weights of the experts that
+// have rows); one expert of one row: 11 us, whose 25 MB lie in the last cache.
 #pragma once
 
 #include "fp8_common.h"

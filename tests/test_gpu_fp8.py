@@ -651,6 +651,60 @@ def test_the_run_of_an_expert_block():
     assert float((dx.double() - ref).abs().max()) <= 2e-5 * float(ref.abs().max())
 
 
+def test_a_padded_step_captured():
+    """The run with padded tokens, rows counted on the device, captured once and replayed on other tokens and
+    choices, eager work in between: each replay is the eager result."""
+    T, E, k, H, I = 200, 5, 3, 400, 272
+    g = torch.Generator().manual_seed(8)
+    wu = B.fp8_quantize_weight((torch.randn((E, 2 * I, H), generator=g) * 0.1).to(BF16).to(DEV))
+    wd = B.fp8_quantize_weight((torch.randn((E, H, I), generator=g) * 0.1).to(BF16).to(DEV))
+    held = {"x": torch.zeros((T, H), dtype=BF16, device=DEV), "topk": torch.zeros((T, k), dtype=torch.int32, device=DEV),
+            "pad": torch.zeros(T, dtype=torch.uint8, device=DEV), "w": torch.zeros((T, k), device=DEV)}
+    space = [torch.zeros((T * k, n), dtype=BF16, device=DEV) for n in (H, 2 * I, H, H, I, H)]
+
+    def fill(seed):
+        r = torch.Generator().manual_seed(seed)
+        held["x"].copy_(torch.randn((T, H), generator=r))
+        held["topk"].copy_(torch.randint(-1, E + 1, (T, k), generator=r))     # out of range, twice the same
+        held["pad"].copy_((torch.rand(T, generator=r) < 0.3 * seed).to(torch.uint8))
+        held["w"].copy_(torch.rand((T, k), generator=r))
+
+    def step():
+        o = B.expert_order(held["topk"], E, held["pad"])
+        off, pos = o["expert_offsets"], o["positions"]
+        used = off[-1:]
+        rows, h, y, dy, dact, dr = space
+        B.dispatch_forward(held["x"], pos, rows=rows)
+        B.fp8_grouped_linear(*B.fp8_quantize_rows(rows, row_count=used), *wu, off, out=h)
+        act, kept = B.swiglu_forward(h)
+        B.fp8_grouped_linear(*B.fp8_quantize_rows(act, row_count=used), *wd, off, out=y)
+        out = B.combine_forward(y, pos, held["w"], addend=held["x"])
+        b = B.combine_backward(out, pos, rows=y, weights=held["w"], drows=dy)
+        B.fp8_grouped_input_grad(*B.fp8_quantize_rows(dy, row_count=used), *wd, off, dx=dact)
+        dh = B.swiglu_backward(dact, kept)["dh"]
+        B.fp8_grouped_input_grad(*B.fp8_quantize_rows(dh, row_count=used), *wu, off, dx=dr)
+        return out, b["dweights"], B.dispatch_backward(dr, pos)["dx"]
+
+    fill(0)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = step()
+    for seed in (1, 0, 2, 4, 1):       # 4: every token padded
+        fill(seed)
+        eager = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        for t in res:
+            t.fill_(MARK)
+        graph.replay()
+        for a, b in zip(res, eager):
+            assert torch.equal(a, b), seed
+            assert bool(torch.isfinite(a.float()).all())
+        if seed == 4:
+            assert torch.equal(res[0], held["x"]) and not bool(res[1].any()) and not bool(res[2].any())
+
+
 def test_binding_refusals():
     w, ws = _weight(2, 32, 48)
     x, xs = _fp8((5, 48), 5), _scales((5, 1), 6)

@@ -89,6 +89,33 @@ def test_order(T, E, k, kind, masked):
     _check_order(got, _ref_order(topk, E, mask))
 
 
+def test_order_of_the_most_slots():
+    """Nearly 2^31 slots: every slot in its row, rows by expert, then by slot."""
+    T, E, k = 71582000, 5, 30
+    n = T * k
+    _say(f"order of {n} slots")
+    topk = torch.randint(0, E + 1, (T, k), dtype=torch.int32, device=DEV)     # E: no row
+    got = B.expert_order(topk, E)
+    flat, pos, slots = topk.view(-1), got["positions"].view(-1), got["sorted_slots"]
+    ends = got["expert_offsets"].tolist()
+    assert ends[0] == 0 and np.diff(ends).tolist() == got["expert_counts"].tolist()
+    used, step, rows = ends[-1], 1 << 26, 0
+    for a in range(0, n, step):
+        p, e = pos[a:a + step], flat[a:a + step]
+        has = e < E
+        assert torch.equal(p >= 0, has)
+        at = has.nonzero().view(-1)
+        rows += at.numel()
+        assert torch.equal(slots[p[at].long()].long(), at + a)
+    assert rows == used and bool((slots[used:used + (1 << 20)] == -1).all()) and int(slots[n - 1]) == -1
+    for a in range(0, used - 1, step):
+        c = slots[a:min(a + step + 1, used)].long()
+        key = flat[c].long() * n + c
+        assert bool((key[1:] > key[:-1]).all())
+    for e in range(E):
+        assert int(flat[slots[ends[e]].long()]) == e and int(flat[slots[ends[e + 1] - 1].long()]) == e
+
+
 def test_order_of_nothing():
     got = B.expert_order(torch.empty((0, 4), dtype=torch.int32, device=DEV), 7)
     assert got["expert_offsets"].tolist() == [0] * 8 and got["expert_counts"].tolist() == [0] * 7

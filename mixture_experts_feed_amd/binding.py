@@ -903,6 +903,7 @@ def expert_order(topk_indices: torch.Tensor, n_routed: int, padding_mask: Option
         _operand(padding_mask, "padding_mask", torch.uint8, dev)
         if padding_mask.dim() != 1 or padding_mask.shape[0] != T:
             raise ValueError("padding_mask must hold a value for each token")
+    n_routed = int(n_routed)   # (a tensor would be its identity to the kept sizes)
     dims, need = _order_plan(T, n_routed, k)
     i32 = torch.int32
     if expert_counts is None and expert_offsets is None and sorted_slots is None:

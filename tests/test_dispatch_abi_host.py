@@ -149,3 +149,20 @@ def test_binding_refuses_host_tensors_and_shapes():
         B.combine_forward(x, pos, addend=torch.zeros((4, 9)))
     with pytest.raises(ValueError):
         B.combine_forward(torch.zeros((2, 4, 8)), pos)
+
+
+def test_a_number_of_experts_changed_in_place_is_read_anew(monkeypatch):
+    """A tensor as n_routed is its value at the call: sizes kept by the object would write past the results."""
+    seen = []
+    monkeypatch.setattr(B, "_operand", lambda *a: None)
+    monkeypatch.setattr(B, "_call", lambda dev, name, dims, *a: seen.append(dims._obj.n_routed))
+    topk, n = torch.zeros((4, 2), dtype=torch.int32), torch.tensor(200)
+    for value in (200, 7, 300):
+        n.fill_(value)
+        o = B.expert_order(topk, n)
+        assert seen[-1] == value and o["expert_counts"].shape == (value,) and o["expert_offsets"].shape == (value + 1,)
+    for same in (8, 8.0, torch.tensor(8)):
+        o = B.expert_order(topk, same)
+        assert seen[-1] == 8 and o["expert_counts"].shape == (8,)
+    with pytest.raises(TypeError):
+        B.expert_order(topk, None)

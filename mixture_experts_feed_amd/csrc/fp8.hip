@@ -234,9 +234,10 @@ void launch_tiles(const Fp8Args& a, int grid, hipStream_t stream) {
 }
 
 template <int BN, int NW, int DEPTH, int FM>
-void launch_stream_as(const Fp8Args& a, int per_cu, hipStream_t stream) {
+void launch_stream_as(const Fp8Args& a, hipStream_t stream) {
     const long long tasks = ((long long)(a.rows + 16 * FM - 1) / (16 * FM) + a.E) * ((a.N + BN - 1) / BN);
-    const dim3 grid((unsigned)std::min<long long>(tasks, (long long)device_cu_count() * per_cu)), block(NW * 64);
+    const long long most = (long long)device_cu_count() * stream_per_cu<BN, NW, DEPTH, FM>();
+    const dim3 grid((unsigned)std::min<long long>(tasks, most)), block(NW * 64);
     if (a.out_bf16) hipLaunchKernelGGL((fp8_stream_kernel<BN, NW, DEPTH, FM, false>), grid, block, 0, stream, a);
     else hipLaunchKernelGGL((fp8_stream_kernel<BN, NW, DEPTH, FM, true>), grid, block, 0, stream, a);
 }
@@ -244,22 +245,22 @@ void launch_stream_as(const Fp8Args& a, int per_cu, hipStream_t stream) {
 // Rows of a task: 16, 32 or 64, so that few experts have more (their weights are read
 // again).  Columns: 64 where that gives every CU two tasks (with 64 rows: every second CU
 // one), else 16, for which eight waves share out a long reduction where every CU has a
-// task or two, otherwise four (four workgroups a CU).
+// task or two, otherwise four (three workgroups a CU, two with 64 rows).
 void launch_stream(const Fp8Params& p, const Fp8Args& a, hipStream_t stream) {
     const double mean = (double)a.rows / a.E;
     const long long cus = device_cu_count(), E = a.E;
     const int fm = mean <= (a.E == 1 ? 16.0 : 8.0) ? 1 : mean <= (a.E == 1 ? 32.0 : 20.0) ? 2 : 4;
     if (fm < 4 ? E * ((a.N + 63) / 64) >= 2 * cus : 2 * tasks64(p) >= cus) {
-        if (fm == 1) launch_stream_as<64, 4, 4, 1>(a, 1, stream);
-        else if (fm == 2) launch_stream_as<64, 4, 4, 2>(a, 1, stream);
-        else launch_stream_as<64, 4, 4, 4>(a, 1, stream);
+        if (fm == 1) launch_stream_as<64, 4, 4, 1>(a, stream);
+        else if (fm == 2) launch_stream_as<64, 4, 4, 2>(a, stream);
+        else launch_stream_as<64, 4, 4, 4>(a, stream);
     } else if (a.K > 24 * kQBlock && fm < 4 && E * ((a.N + 15) / 16) < 2 * cus) {
-        if (fm == 1) launch_stream_as<16, 8, 6, 1>(a, 1, stream);
-        else launch_stream_as<16, 8, 6, 2>(a, 1, stream);
+        if (fm == 1) launch_stream_as<16, 8, 6, 1>(a, stream);
+        else launch_stream_as<16, 8, 6, 2>(a, stream);
     } else {
-        if (fm == 1) launch_stream_as<16, 4, 4, 1>(a, 4, stream);
-        else if (fm == 2) launch_stream_as<16, 4, 4, 2>(a, 4, stream);
-        else launch_stream_as<16, 4, 4, 4>(a, 4, stream);
+        if (fm == 1) launch_stream_as<16, 4, 4, 1>(a, stream);
+        else if (fm == 2) launch_stream_as<16, 4, 4, 2>(a, stream);
+        else launch_stream_as<16, 4, 4, 4>(a, stream);
     }
 }
 

@@ -2,13 +2,13 @@
 // read once: HBM bounds it, so the aim is to keep enough of W on its way.
 //
 // A task is BN output columns of one expert for up to 16 FM of its rows.  Persistent
-// workgroups of NW waves, one a CU, walk the tasks with stride.  The waves share out the
-// reduction by blocks of 128 (wave w takes blocks w, w + NW, ...).  Each wave loads its
-// weights straight into LDS rings of its own, DEPTH blocks of BN x 128 deep and whole
-// 128-byte lines at a time, and its rows into registers as far ahead; nobody waits for
-// anybody until the waves' sums are added in LDS at the end of a task, in the order of
-// the waves.  The loads run ahead over the end of a task, so that the next one's weights
-// are on their way while the sums are added and stored.
+// workgroups of NW waves, as many a CU as its LDS holds (stream_per_cu), walk the tasks
+// with stride.  The waves share out the reduction by blocks of 128 (wave w takes blocks w,
+// w + NW, ...).  Each wave loads its weights straight into LDS rings of its own, DEPTH
+// blocks of BN x 128 deep and whole 128-byte lines at a time, and its rows into registers
+// as far ahead; nobody waits for anybody until the waves' sums are added in LDS at the end
+// of a task, in the order of the waves.  The loads run ahead over the end of a task, so
+// that the next one's weights are on their way while the sums are added and stored.
 // 128 experts of 2 rows, 6144 x 4096: 385 us (7.2 TB/s of the weights of the experts that
 // have rows); one expert of one row: 11 us, whose 25 MB lie in the last cache.
 #pragma once
@@ -52,17 +52,45 @@ __device__ __forceinline__ void lds_blocks(Frag (&f)[4], uint32_t p0, uint32_t p
         : "memory");
 }
 
+// A ring place of a wave: BN rows of 128 bytes of weights, then the row scales (lane m: of
+// row m).
+template <int BN>
+constexpr int stream_slot() { return BN * kQBlock + kWave * 4; }
+// blocks of 16 columns whose sums the waves join at a time
+template <int BN, int FM>
+constexpr int stream_joined() { return BN / 16 / FM > 0 ? BN / 16 / FM : 1; }
+
+// LDS of a workgroup: rings, row numbers, the waves' sums, the plan and its scan; given out
+// by 1280 bytes
+template <int BN, int NW, int DEPTH, int FM>
+constexpr int stream_lds() {
+    constexpr int ring = DEPTH * NW * stream_slot<BN>(), index = NW * kWave * 4,
+                  part = NW * 16 * FM * (16 * stream_joined<BN, FM>() + 4) * 4,
+                  plan = 2 * (kMaxFp8Groups + 1) * 4 + 2 * NW * 4;
+    return (ring + index + part + plan + 1279) / 1280 * 1280;
+}
+// Workgroups that a CU's LDS holds: one of 64 columns or of eight waves, three of 16 columns
+// (two with 64 rows).  No more are launched: the others would start when these have ended,
+// with a scan and empty rings of their own (us, four workgroups a CU of 16 columns against
+// three: 14.9 / 10.9 for 50 experts of 6 rows, 2048 x 256, and 20.8 / 16.3 for 100; 19.8 /
+// 15.7 for 7 of 2048 x 4096).
+constexpr int kLdsBytes = 160 * 1024;
+template <int BN, int NW, int DEPTH, int FM>
+constexpr int stream_per_cu() {
+    static_assert(stream_lds<BN, NW, DEPTH, FM>() <= kLdsBytes, "a workgroup's LDS");
+    return kLdsBytes / stream_lds<BN, NW, DEPTH, FM>();
+}
+
 template <int BN, int NW, int DEPTH, int FM, bool EXACT>
-__global__ __launch_bounds__(NW * 64, NW / 4) void fp8_stream_kernel(const Fp8Args a) {
+__global__ __launch_bounds__(NW * 64, (NW / 4 * stream_per_cu<BN, NW, DEPTH, FM>())) void fp8_stream_kernel(const Fp8Args a) {
     constexpr int THREADS = NW * 64, BM = 16 * FM, FN = BN / 16;
     constexpr int LW = BN / 8;                    // wave loads of a block's weights (8 rows of 128 bytes each)
     constexpr int PER = LW + 2 * FM + 1;          // loads of a block: weights, rows, the rows' scales
     static_assert((DEPTH - 1) * PER < 64, "loads in flight are counted in six bits");
     static_assert(DEPTH >= 4 && DEPTH <= 8, "ring depth");
-    // A ring place of a wave: BN rows of 128 bytes of weights, then the row scales (lane
-    // m: of row m).  One object for both: the compiler tells few apart, and waits for
-    // every load on its way where it cannot.
-    constexpr int SLOT = BN * kQBlock + kWave * 4, RING = NW * SLOT, NONE = 16;
+    // Weights and row scales of a place in one object: the compiler tells few apart, and
+    // waits for every load on its way where it cannot.
+    constexpr int SLOT = stream_slot<BN>(), RING = NW * SLOT, NONE = 16;
     __shared__ __attribute__((aligned(16))) uint8_t r0[RING], r1[RING], r2[RING], r3[RING];
     __shared__ __attribute__((aligned(16))) uint8_t r4[DEPTH > 4 ? RING : NONE], r5[DEPTH > 5 ? RING : NONE],
         r6[DEPTH > 6 ? RING : NONE], r7[DEPTH > 7 ? RING : NONE];
@@ -80,9 +108,11 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void fp8_stream_kernel(const Fp8Ar
     // the next task's row_index entries (lane m: of row m)
     __shared__ __attribute__((aligned(16))) int32_t index[NW][kWave];
     // sums of the waves, RI blocks of 16 columns at a time
-    constexpr int RI = FN >= FM ? (FN / FM > 0 ? FN / FM : 1) : 1, RC = 16 * RI;
+    constexpr int RI = stream_joined<BN, FM>(), RC = 16 * RI;
     __shared__ __attribute__((aligned(16))) float part[NW][BM][RC + 4];
     __shared__ int32_t offs[kMaxFp8Groups + 1], first[kMaxFp8Groups + 1];
+    static_assert(DEPTH * RING + sizeof(index) + sizeof(part) + sizeof(offs) + sizeof(first) + 2 * NW * 4 <=
+                      stream_lds<BN, NW, DEPTH, FM>(), "the LDS that the launch counts on");
 
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int rl = lane & 15, g = lane >> 4;

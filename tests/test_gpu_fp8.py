@@ -337,6 +337,34 @@ def test_streamed(E, N, K, mean, out_dtype):
         assert float((single[0] - out[r].float()).abs().max()) <= 2.0 ** -7 * scale, (r, e)
 
 
+@pytest.mark.parametrize("E,N,K,mean", [
+    (50, 256, 2064, 6), (70, 256, 2064, 6), (110, 272, 2064, 7),   # 800 to 1870 tasks of 16 columns and 16 rows
+    (50, 272, 4112, 12), (4, 4096, 4112, 12), (7, 4112, 2064, 4),  # ... and 32 rows, of a few experts
+])
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+def test_streamed_tasks_in_turn(E, N, K, mean, out_dtype):
+    """More tasks of 16 columns than the card holds workgroups: each takes several, the loads running ahead from one
+    to the next; uneven rows, experts without any."""
+    _say(f"streamed in turn E={E} N={N} K={K} mean {mean} {out_dtype}")
+    rng = np.random.default_rng(E + N + mean)
+    p = rng.random(E) + 1e-3
+    p[E // 3] = 0.0
+    counts = rng.multinomial(mean * E, p / p.sum()).tolist()
+    ends, R = _rows(counts, 0, 0)
+    w, ws = _weight(E, N, K)
+    X = max(1, R // 2)
+    x, xs = _fp8((X, K), 5), _scales((X, -(-K // 128)), 6)
+    index = torch.randint(0, X, (R,), dtype=torch.int32, device=DEV)
+    off = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    out = torch.full((R + 2, N), MARK, dtype=out_dtype, device=DEV)
+    B.fp8_grouped_linear(x, xs, w, ws, off, row_index=torch.cat([index, index[:2]]), out=out)
+    for e in sorted({0, 1, E // 3, E // 2, E - 2, E - 1, int(np.argmax(counts))}):
+        part = _reference("linear", x, xs, w[e:e + 1], ws[e:e + 1], ends[e:e + 2], out_dtype, index)
+        for (a, b), want, bound in part:
+            assert bool(((out[a:b].double() - want).abs() <= bound).all()), (e, counts[e])
+    assert bool((out[R:] == MARK).all())
+
+
 def _sampled(counts, seed, each):
     """Rows of each group, a few of them, its first and last among them; (group, rows)."""
     rng = np.random.default_rng(seed)

@@ -243,23 +243,31 @@ void launch_stream_as(const Fp8Args& a, hipStream_t stream) {
 }
 
 // Rows of a task: 16, 32 or 64, so that few experts have more (their weights are read
-// again).  Columns: 64 where that gives every CU two tasks (with 64 rows: every second CU
-// one), else 16, for which eight waves share out a long reduction where every CU has a
-// task or two, otherwise four (three workgroups a CU, two with 64 rows).
+// again).  Columns: 64 where that gives every CU two tasks (with 32 rows: three of four
+// CUs one, with 64 rows: every second one), else 16, of which a CU holds three workgroups
+// (two with 64 rows).  us, 64 columns against 16 (E experts of r rows, K x N):
+// - 16 rows: 16.1 / 13.2 at 64 x 6 (2048 x 320, 320 tasks of 64 columns), 18.1 / 17.7 at 120 x
+//   6 (2048 x 256, 480), 18.4 / 18.7 at 128 x 6 (512), 22.7 / 23.8 at 64 x 6
+//   (2048 x 768, 768);
+// - 32 rows: 15.8 / 13.1 at 2 x 12 (4096 x 4096, 128), 17.3 / 24.0 at 40 x 12 (4096 x 320, 200),
+//   19.2 / 21.9 at 4 x 12 (4096 x 4096, 256), 27.6 / 33.7 at 7 x 12 (448);
+// - 64 rows: 16.5 / 12.6 at 1 x 64 (2048 x 4096, 64), 28.1 / 35.5 at 1 x 128 (6144 x 4096, 128),
+//   16.8 / 26.9 at 1 x 512 (2048 x 2048, 256).
+// 16 columns and rows: eight waves share out a reduction from 16384 on where few CUs have
+// more than a task (eight against four: 12.2 / 10.0 at 1 x 1 (8192 x 4096), 17.8 / 18.2
+// (16384 x 4096), 16.9 / 21.4 (32768 x 512), 27 / 36 (65536 x 256)).
 void launch_stream(const Fp8Params& p, const Fp8Args& a, hipStream_t stream) {
     const double mean = (double)a.rows / a.E;
-    const long long cus = device_cu_count(), E = a.E;
-    const int fm = mean <= (a.E == 1 ? 16.0 : 8.0) ? 1 : mean <= (a.E == 1 ? 32.0 : 20.0) ? 2 : 4;
-    if (fm < 4 ? E * ((a.N + 63) / 64) >= 2 * cus : 2 * tasks64(p) >= cus) {
-        if (fm == 1) launch_stream_as<64, 4, 4, 1>(a, stream);
-        else if (fm == 2) launch_stream_as<64, 4, 4, 2>(a, stream);
-        else launch_stream_as<64, 4, 4, 4>(a, stream);
-    } else if (a.K > 24 * kQBlock && fm < 4 && E * ((a.N + 15) / 16) < 2 * cus) {
-        if (fm == 1) launch_stream_as<16, 8, 6, 1>(a, stream);
-        else launch_stream_as<16, 8, 6, 2>(a, stream);
+    const long long cus = device_cu_count(), E = a.E, tasks = E * ((a.N + 63) / 64);
+    if (mean <= (E == 1 ? 16.0 : 8.0)) {
+        if (tasks >= 2 * cus) launch_stream_as<64, 4, 4, 1>(a, stream);
+        else if (a.K >= 128 * kQBlock && E * ((a.N + 15) / 16) < 2 * cus) launch_stream_as<16, 8, 6, 1>(a, stream);
+        else launch_stream_as<16, 4, 4, 1>(a, stream);
+    } else if (mean <= (E == 1 ? 32.0 : 20.0)) {
+        if (4 * tasks >= 3 * cus) launch_stream_as<64, 4, 4, 2>(a, stream);
+        else launch_stream_as<16, 4, 4, 2>(a, stream);
     } else {
-        if (fm == 1) launch_stream_as<16, 4, 4, 1>(a, stream);
-        else if (fm == 2) launch_stream_as<16, 4, 4, 2>(a, stream);
+        if (2 * tasks64(p) >= cus) launch_stream_as<64, 4, 4, 4>(a, stream);
         else launch_stream_as<16, 4, 4, 4>(a, stream);
     }
 }

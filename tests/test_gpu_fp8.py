@@ -365,6 +365,22 @@ def test_streamed_tasks_in_turn(E, N, K, mean, out_dtype):
     assert bool((out[R:] == MARK).all())
 
 
+@pytest.mark.parametrize("E,N,K,R", [(1, 64, 24592, 1), (1, 208, 16384, 16), (3, 80, 20496, 9), (2, 272, 16400, 5)])
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+def test_streamed_long_rows(E, N, K, R, out_dtype):
+    """Reductions that eight waves share out."""
+    _say(f"streamed long rows E={E} N={N} K={K} R={R} {out_dtype}")
+    ends = [0, R // 2, R // 2, R][4 - E - 1:] if E > 1 else [0, R]
+    w, ws = _weight(E, N, K)
+    x, xs = _fp8((R, K), 5), _scales((R, -(-K // 128)), 6)
+    off = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    out = torch.full((R, N), MARK, dtype=out_dtype, device=DEV)
+    B.fp8_grouped_linear(x, xs, w, ws, off, out=out)
+    for (a, b), want, bound in _reference("linear", x, xs, w, ws, ends, out_dtype):
+        assert bool(((out[a:b].double() - want).abs() <= bound).all())
+    assert bool((out[:ends[0]] == MARK).all())
+
+
 def _sampled(counts, seed, each):
     """Rows of each group, a few of them, its first and last among them; (group, rows)."""
     rng = np.random.default_rng(seed)

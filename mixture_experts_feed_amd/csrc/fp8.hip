@@ -172,30 +172,40 @@ Fp8Args fp8_args(const Fp8Params& p) {
     return a;
 }
 
+// 64 x 64 tasks of the forward, at most, and as rows spread over a few experts make them
+long long tasks64(const Fp8Params& p) { return (((long long)p.rows + 63) / 64 + p.E - 1) * ((p.N + 63) / 64); }
+double expected64(const Fp8Params& p) {
+    const double tiles = p.E == 1 ? (p.rows + 63LL) / 64 : std::max<double>(p.E, p.rows / 64.0 + p.E / 4.0);
+    return tiles * ((p.N + 63) / 64);
+}
+
 // The forward streams the weights (fp8_stream.h) where experts have few rows; 256-row
 // tiles otherwise, whose stages without rows cost little: 5.5 TB/s of weights at 2 to 48
 // rows an expert.  us, streamed against tiles (E experts of r rows, K x N):
-// - up to 8 rows and K from 2048 on: 387 / 465 at 128 x 2 (6144 x 4096), 79 / 98 at 128 x
-//   2 and 100 / 106 at 128 x 8 (2048 x 2048), 75 / 110 at 64 x 2 (4096 x 2048), 36 / 39 at
+// - up to 8 rows and K from 2048 on: 387 / 465 at 128 x 2 (6144 x 4096), 78 / 98 at 128 x
+//   2 and 101 / 106 at 128 x 8 (2048 x 2048), 77 / 114 at 64 x 2 (4096 x 2048), 36 / 38 at
 //   64 x 2 (2048 x 1536); 22 / 14 at 64 x 2 (1024 x 1024);
-// - up to 16 rows and K from 4096 on: 547 / 574 at 128 x 16 (6144 x 4096), 104 / 135 at 16
-//   x 16 (6144 x 6144); 121 / 106 at 128 x 16 (2048 x 2048), 655 / 581 at 128 x 24 (6144 x
+// - up to 16 rows and K from 4096 on: 532 / 563 at 128 x 16 (6144 x 4096), 104 / 136 at 16
+//   x 16 (6144 x 6144); 121 / 109 at 128 x 16 (2048 x 2048), 655 / 566 at 128 x 24 (6144 x
 //   4096);
-// - up to 48 rows where fewer than 64 tiles would run, K from 1024 on: 12 / 43 at one
-//   expert of 1 row and 21 / 43 of 40 (6144 x 4096), 9 / 18 of 1 (2048 x 2048), 9 / 11 of 1
-//   (1024 x 1024); 9 / 8 at 512 x 512, and 39 / 32 at 4 x 40 (4096 x 4096, 64 tiles);
-// - any number where 64 x 64 tasks give a CU two at most (a tile's stages wait for their
-//   loads, and few CUs have one), K from 2048 on: 29 / 58 at one expert of 128 rows and 51 /
-//   77 of 512 (6144 x 4096), 17 / 31 of 512 (2048 x 2048), 26 / 31 at 4 x 200 (2048 x 2048),
-//   24 / 32 at 16 x 30 (4096 x 1024); 96 / 79 at one of 1024 (6144 x 4096), 16 / 15 at 8 x
-//   100 (1024 x 1024), 27 / 23 at 16 x 64 (2048 x 1024).
-long long tasks64(const Fp8Params& p) { return (((long long)p.rows + 63) / 64 + p.E - 1) * ((p.N + 63) / 64); }
-
+// - up to 48 rows where fewer than 64 tiles would run, K from 2048 on: 9.8 / 44 at one
+//   expert of 1 row and 17 / 44 of 40 (6144 x 4096), 7.3 / 18 of 1 (2048 x 2048), 28 / 32 at 30
+//   x 48 (4096 x 512), 18.6 / 19.4 at 60 x 40 (2048 x 256); from 1024 on with 16 tiles at most:
+//   11.1 / 12.0 at 1 x 48 (1024 x 4096), 11.2 / 12.1 at 4 x 40 (1024 x 1024), otherwise up to 20
+//   rows: 13.2 / 15.3 at 15 x 20 (1536 x 1024), 10.9 / 11.8 at 15 x 8 and 15.8 / 12.3 at 15 x 40
+//   (1024 x 1024); 8.8 / 8.7 at 1 x 48 (512 x 4096);
+// - any number where few experts' 64 x 64 tasks give a CU one at most (of several experts: a
+//   tenth more by their average), since a tile's stages wait for their loads, and few CUs
+//   have one, K from 2048 on: 29.5 / 48 at one expert of 256 rows and 51 / 48 of 320 (6144 x
+//   4096), 16.6 / 18.8 of 512 and 24 / 19 of 768 (2048 x 2048), 24 / 33 at 2 x 100 and 39 / 33
+//   at 4 x 64 (4096 x 4096), 22 / 32 at 2 x 256 (4096 x 2048), 27 / 32 at 16 x 48 and 39 / 33 at
+//   16 x 60 (4096 x 1024), 17.9 / 18.9 at 8 x 100 (2048 x 1024), 26 / 19 at 4 x 150 (2048 x 2048).
 bool fp8_streams(const Fp8Params& p) {
     if (p.input_grad) return false;
-    const long long rows = p.rows, E = p.E;
-    if (p.K >= 2048 && E <= (p.K >= 4096 ? 16 : 8) && tasks64(p) <= 2LL * device_cu_count()) return true;
-    if (E * ((p.N + 255) / 256) < 64) return p.K >= 1024 && rows <= 48 * E;
+    const long long rows = p.rows, E = p.E, tiles = E * ((p.N + 255) / 256);
+    if (p.K >= 2048 && E <= (p.K >= 4096 ? 16 : 8) && expected64(p) <= (E == 1 ? 1.0 : 1.1) * device_cu_count())
+        return true;
+    if (tiles < 64) return p.K >= 1024 && rows <= (p.K >= 2048 || tiles <= 16 ? 48 : 20) * E;
     return rows <= (p.K >= 4096 ? 16 : p.K >= 2048 ? 8 : 0) * E;
 }
 

@@ -3,9 +3,9 @@
 //
 // Quantising: the scale of a block (128 columns of a row; 128 x 128 of a weight) is the
 // smallest power of two 2^e, e >= -126, with max|block| <= 448 2^e, so v / 2^e is exact
-// and each value is rounded once, to nearest even (v_cvt_pk_fp8_f32; its results for
-// |v| <= 448 are tested one by one).  Half a step is 2^-4 of a value from 2^-6 2^e on, and
-// 2^-10 2^e below.  A block with an infinity or a NaN gets a NaN scale and zeros, so that
+// and each value is rounded once, to nearest even (v_cvt_pk_fp8_f32; tested on every e4m3
+// value, every midpoint of two and the numbers next to each of them, of both signs).  Half a
+// step is 2^-4 of a value from 2^-6 2^e on, and 2^-10 2^e below.  A block with an infinity or a NaN gets a NaN scale and zeros, so that
 // every product with it is NaN.  One read and one write: HBM bounds both kernels (8192
 // rows of 6144 bf16: 28 us, 5.4 TB/s).
 #include <algorithm>

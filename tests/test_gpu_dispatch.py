@@ -468,3 +468,45 @@ def test_binding_refusals():
     with pytest.raises(B.InklingError) as e:
         B.combine_forward(r, p, addend=x, out=x)
     assert e.value.code == B.INKLING_ERR_INVALID_ARGUMENT
+
+
+# ---- results that a C caller does not want -------------------------------------------------
+
+
+@pytest.mark.parametrize("T,E,k", [(50, 7, 3), (1024, 128, 8), (9000, 128, 8), (3000, 512, 32), (0, 5, 2)])
+@pytest.mark.parametrize("without", [("expert_counts",), ("sorted_slots",), ("expert_counts", "sorted_slots")])
+def test_order_without_some_results(T, E, k, without):
+    """expert_counts and sorted_slots may be NULL, in one launch and in two: the others are the same."""
+    _say(f"order T={T} E={E} k={k} without {without}")
+    rng = np.random.default_rng(T + k)
+    topk = torch.from_numpy(rng.integers(-1, E + 1, (T, k)).astype(np.int32)).to(DEV)
+    mask = torch.from_numpy((rng.random(T) < 0.2).astype(np.uint8)).to(DEV)
+    want = B.expert_order(topk, E, padding_mask=mask)
+    got = {n: torch.full_like(t, -9) for n, t in want.items()}
+    dims, need = B._order_plan(T, E, k)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+    at = [None if n in without else got[n].data_ptr() for n in ("expert_counts", "expert_offsets", "sorted_slots",
+                                                                "positions")]
+    B._call(torch.device(DEV), "inkling_expert_order", dims, topk.data_ptr(), mask.data_ptr(), *at, ws.data_ptr(), need)
+    for n in want:
+        assert bool((got[n] == -9).all()) if n in without else torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("k", [1, 3, 8, 9, 17])
+@pytest.mark.parametrize("H", [5, 64, 500, 1237, 2056])      # 16 lanes, a wave and a workgroup a token
+@pytest.mark.parametrize("token_dtype,rows_dtype", [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)])
+def test_combine_backward_of_the_weights_alone(k, H, token_dtype, rows_dtype):
+    """drows may be NULL: dweights are the same, bit by bit."""
+    _say(f"combine_backward without drows k={k} H={H} {token_dtype} {rows_dtype}")
+    T, E = 37, 20
+    g = torch.Generator().manual_seed(k * H)
+    topk = torch.randint(-1, E, (T, k), generator=g).to(torch.int32).to(DEV)
+    pos = B.expert_order(topk, E)["positions"]
+    dout = torch.randn((T, H), generator=g).to(token_dtype).to(DEV)
+    rows = torch.randn((T * k, H), generator=g).to(rows_dtype).to(DEV)
+    w = torch.rand((T, k), generator=g).to(DEV)
+    want = B.combine_backward(dout, pos, rows=rows, weights=w)["dweights"]
+    got = torch.full((T, k), MARK, device=DEV)
+    B._call(torch.device(DEV), "inkling_combine_backward", B._dispatch_plan(T, T * k, k, H, token_dtype, rows_dtype),
+            dout.data_ptr(), pos.data_ptr(), w.data_ptr(), rows.data_ptr(), None, got.data_ptr())
+    assert torch.equal(got, want) and bool((want != 0).any())

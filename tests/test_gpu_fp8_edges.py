@@ -71,3 +71,25 @@ def test_every_value_and_every_midpoint(dtype, power):
     q, s = B.fp8_quantize_weight(t.to(DEV).reshape(n // 16, 16, 128))
     got = q.view(torch.uint8).cpu().numpy().reshape(n, 128)
     assert np.array_equal(got[keep], want[keep]) and bool((s == 2.0 ** power).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_quantize_past_32_bits(dtype):
+    """Rows and weights of more than 2^32 values: as their parts."""
+    R, C, step = 270016, 16384, 16876
+    _say(f"quantize {R} x {C} {dtype}")
+    assert R * C > 2 ** 32 + 2 ** 20 and R % step == 0
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.empty((R, C), dtype=dtype, device=DEV)
+    for a in range(0, R, step):
+        x[a:a + step] = torch.randn((step, C), generator=g, device=DEV)
+    v, s = B.fp8_quantize_rows(x)
+    for a in range(0, R, step):
+        pv, ps = B.fp8_quantize_rows(x[a:a + step])
+        assert torch.equal(v[a:a + step].view(torch.uint8), pv.view(torch.uint8)) and torch.equal(s[a:a + step], ps), a
+    del v, s
+    E, N = 4, R // 4            # 67504 = 527.4 blocks of 128: the last one of each expert is short
+    v, s = B.fp8_quantize_weight(x.view(E, N, C))
+    for e in range(E):
+        pv, ps = B.fp8_quantize_weight(x.view(E, N, C)[e:e + 1])
+        assert torch.equal(v[e].view(torch.uint8), pv[0].view(torch.uint8)) and torch.equal(s[e], ps[0]), e

@@ -93,3 +93,76 @@ def test_quantize_past_32_bits(dtype):
     for e in range(E):
         pv, ps = B.fp8_quantize_weight(x.view(E, N, C)[e:e + 1])
         assert torch.equal(v[e].view(torch.uint8), pv[0].view(torch.uint8)) and torch.equal(s[e], ps[0]), e
+
+
+# ---- sums -----------------------------------------------------------------------------------
+
+
+def _e4m3(shape, seed, scale):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return (torch.randn(shape, generator=g, device=DEV) * scale).clamp(-448, 448).to(E4M3)
+
+
+def _lost(x, w):
+    """What the 8-bit matrix units may lose of the products x w of each group of 8 (last dimension): every product
+    that is no multiple of the last kept bit, 13 below the group's leading one, up to that bit.  (Leading bits are
+    those of the numbers as e4m3 holds them, so that subnormal ones count as 2^-6.)"""
+    p = x * w
+    exponent = lambda v: torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6)))  # noqa: E731
+    lead = torch.maximum(exponent(x) + exponent(w), torch.floor(torch.log2(p.abs().clamp(min=2.0 ** -30))))
+    unit = torch.exp2(lead.amax(-1, keepdim=True) - 13)
+    return torch.where(p / unit == torch.round(p / unit), 0.0, unit)
+
+
+@pytest.mark.parametrize("op,R", [("linear", 1), ("linear", 40), ("linear", 300), ("linear", 3000), ("linear", 9000),
+                                  ("input_grad", 1), ("input_grad", 100), ("input_grad", 3000)])
+def test_sums_of_the_8_bit_units(op, R):
+    """Results in bf16 show a sum's own error where most of it is taken away again: the last block of 128 holds
+    three digits of minus the sum of the others, each in a group of its own (so nothing of them is cut).  What is
+    left is at most 2^-12 of the sum, and its rounding to bf16 2^-21.
+
+    Error: what the groups of 8 lose; then 16 groups of a block, and the blocks (nb, and 8 for waves that share out
+    a row), added in fp32, cut or rounded, at most 2 u of the sum of the sizes each; the digits' three sums likewise."""
+    L, C = 2048, 1024
+    _say(f"8-bit sums {op} R={R}")
+    x, w = _e4m3((L,), 1, 60.0), _e4m3((C, L), 2, 60.0)
+    xd, wd = x.double(), w.double()
+    S = wd @ xd
+    # minus the sum, in units of a power of two with |S| <= 256 of them, in three e4m3 digits
+    unit = 2.0 ** float(np.ceil(np.log2(float(S.abs().max()) / 256.0)))
+    rest, digits = -S / unit, []
+    for i in range(3):
+        d = (rest * 16.0 ** i).to(E4M3)
+        digits.append(d)
+        rest = rest - d.double() / 16.0 ** i
+    xl, wl = torch.zeros(128, device=DEV), torch.zeros((C, 128), device=DEV)
+    for i, d in enumerate(digits):
+        xl[8 * i], wl[:, 8 * i] = 16.0 ** -i, d.float()
+    x_all = torch.cat([x.view(torch.uint8), xl.to(E4M3).view(torch.uint8)])
+    assert torch.equal(xl.to(E4M3).float(), xl)
+    w_all = torch.cat([w.view(torch.uint8), wl.to(E4M3).view(torch.uint8)], 1)
+    nb = L // 128 + 1
+    xs = torch.ones((R, nb), device=DEV)
+    ws = torch.ones((1, C // 128, nb), device=DEV)
+    ws[:, :, -1] = unit
+    rows = x_all.expand(R, -1).contiguous().view(E4M3)
+    if op == "linear":
+        out = B.fp8_grouped_linear(rows, xs, w_all.view(E4M3)[None], ws, None)
+    else:
+        out = B.fp8_grouped_input_grad(rows, xs, w_all.t().contiguous().view(E4M3)[None],
+                                       ws.transpose(1, 2).contiguous(), None)
+    assert out.dtype == BF16 and out.shape == (R, C) and bool((out == out[0]).all())
+    left = -unit * rest            # what the exact sum of all blocks is
+    assert float(left.abs().max()) <= 2.0 ** -12 * 256 * unit
+    err = out[0].double() - left
+    size = wd.abs() @ xd.abs() + S.abs() * 1.2
+    lost = _lost(xd.view(-1, 8), wd.view(C, -1, 8))
+    cut, cut2 = lost.sum((1, 2)), lost.square().sum((1, 2))
+    sums = 2 * (16 + nb + 8) * U * size
+    bound = cut + sums
+    bound = bound + 2.0 ** -8 * (left.abs() + bound)
+    rms = lambda t: float(t.square().mean().sqrt())  # noqa: E731
+    _say(f"  error {rms(err) / rms(S):.2e} of the sums' size (rms), at most {float((err.abs() / bound).max()):.2f} of its bound")
+    assert bool((err.abs() <= bound).all())
+    # products of random signs lose in both directions: cutting that leaned one way would add up
+    assert rms(err) <= float(cut2.mean().sqrt()) + rms(sums) + 2.0 ** -8 * rms(left)

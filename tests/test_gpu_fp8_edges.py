@@ -166,3 +166,62 @@ def test_sums_of_the_8_bit_units(op, R):
     assert bool((err.abs() <= bound).all())
     # products of random signs lose in both directions: cutting that leaned one way would add up
     assert rms(err) <= float(cut2.mean().sqrt()) + rms(sums) + 2.0 ** -8 * rms(left)
+
+
+@pytest.mark.parametrize("R", [3, 900])
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("large", [False, True])
+def test_factors_at_the_ends_of_the_range(R, out_dtype, large):
+    """x_scales * weight_scales next to 2^-126 and 2^128, of scales that are no powers of two.  As anywhere: a
+    rounding of the factor, of its product with a block's sum and of each sum.  Results below 2^-126 add half of
+    the smallest steps: 2^-150 a sum in fp32, 2^-134 once in bf16."""
+    N, K = 256, 1040
+    nb = 9
+    x, w = _e4m3((R, K), 3, 0.02 if large else 60.0), _e4m3((1, N, K), 4, 0.02 if large else 60.0)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    one = lambda *shape: 1.0 + 0.4 * torch.rand(shape, generator=g, device=DEV)  # noqa: E731
+    # factors from 2^-126 to 2^-125, or from 2^127 to below 2^128
+    xs, ws = one(R, nb) * 2.0 ** (66 if large else -63), one(1, 2, nb) * 2.0 ** (61 if large else -63)
+    f = xs.double()[:, None, :] * ws.double()[0][None]
+    assert float(f.min()) >= 2.0 ** -126 and float(f.max()) < 2.0 ** 127.99
+    out = B.fp8_grouped_linear(x, xs, w, ws, None, out_dtype=out_dtype)
+    blk_x = torch.nn.functional.pad(x.double(), (0, nb * 128 - K)).unflatten(1, (nb, 128))
+    blk_w = torch.nn.functional.pad(w[0].double(), (0, nb * 128 - K)).unflatten(1, (nb, 128))
+    want, size, cut = (torch.zeros((R, N), dtype=torch.float64, device=DEV) for _ in range(3))
+    for b in range(nb):
+        fb = f[:, :, b].repeat_interleave(128, 1)
+        want += fb * (blk_x[:, b] @ blk_w[:, b].t())
+        size += fb * (blk_x[:, b].abs() @ blk_w[:, b].abs().t())
+        if out_dtype == BF16:
+            for k in range(0, 128, 8):
+                cut += fb * _lost(blk_x[:, b, None, k:k + 8], blk_w[None, :, b, k:k + 8]).sum(2)
+    assert bool((want.abs() < 3e38).all())
+    err = (2 * 128 + 3 + nb + 8) * U * size + cut + (2 * nb + 8) * 2.0 ** -150
+    if out_dtype == BF16:
+        err = err + 2.0 ** -8 * (want.abs() + err) + 2.0 ** -134
+    assert bool(((out.double() - want).abs() <= err).all())
+
+
+@pytest.mark.parametrize("R", [3, 900])
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+def test_factors_past_the_range(R, out_dtype):
+    """A factor is the product of two scales in fp32: past 2^128 it is infinite, also where a block's sum is zero,
+    and below 2^-150 it is zero.  Blocks whose factor is in range are what they are beside it."""
+    N, K = 256, 1152
+    x, w = _e4m3((R, K), 6, 60.0), _e4m3((1, N, K), 7, 60.0)
+    x.view(torch.uint8)[1] = 0
+    xs, ws = torch.ones((R, 9), device=DEV), torch.ones((1, 2, 9), device=DEV)
+    clean = B.fp8_grouped_linear(x, xs, w, ws, None, out_dtype=out_dtype)
+    xs[:, 2], ws[0, 1, 2] = 2.0 ** 70, 2.0 ** 70      # columns 128 .. 255: infinite
+    xs[:, 4], ws[0, 0, 4] = 2.0 ** -80, 2.0 ** -80    # columns 0 .. 127: zero
+    ws[0, 0, 2] = 2.0 ** -70
+    xs[2, 2], xs[2, 4] = 1.0, 1.0
+    ws[0, 1, 4] = 2.0 ** 80
+    out = B.fp8_grouped_linear(x, xs, w, ws, None, out_dtype=out_dtype)
+    rows = torch.arange(R, device=DEV) != 2
+    assert not bool(out[rows, 128:].isfinite().any()) and bool(out[1, 128:].isnan().all())
+    assert bool(out[:, :128].isfinite().all())
+    gone = w.clone()
+    gone.view(torch.uint8)[0, :128, 512:640] = 0
+    alone = B.fp8_grouped_linear(x, torch.ones_like(xs), gone, torch.ones_like(ws), None, out_dtype=out_dtype)
+    assert torch.equal(out[rows, :128], alone[rows, :128]) and not torch.equal(out[rows, :128], clean[rows, :128])

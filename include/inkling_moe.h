@@ -524,7 +524,7 @@ typedef struct {
 
 typedef struct {
     int64_t rows;          /* rows of out, dout, dx and row_index */
-    int64_t x_rows;        /* rows of x (input_grad: ignored)     */
+    int64_t x_rows;        /* rows of x (input_grad: within the limits, not used) */
     int32_t n_groups;
     int32_t in_features;
     int32_t out_features;

@@ -290,8 +290,9 @@ long long max_tiles(const Fp8Params& p) {
 
 }  // namespace
 
-// Tiles count in 31 bits; a launch has fewer than 2^32 threads (512 a workgroup of 16
-// streamed columns; 64 columns take 256).
+// Tiles count in 31 bits.  The bound on the groups' columns is the documented one, of 512
+// groups of 2^20 columns only; no launch is near a limit there (the grids are persistent, and
+// the streamed form's tasks fewer than 2^28).
 bool fp8_product_fits(const Fp8Params& p) {
     return (long long)p.E * ((p.N + 63) / 64) < (1LL << 23) && max_tiles(p) <= INT32_MAX - 4096;
 }

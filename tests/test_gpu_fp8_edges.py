@@ -225,3 +225,61 @@ def test_factors_past_the_range(R, out_dtype):
     gone.view(torch.uint8)[0, :128, 512:640] = 0
     alone = B.fp8_grouped_linear(x, torch.ones_like(xs), gone, torch.ones_like(ws), None, out_dtype=out_dtype)
     assert torch.equal(out[rows, :128], alone[rows, :128]) and not torch.equal(out[rows, :128], clean[rows, :128])
+
+
+# ---- rows that nothing has -------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("T", [20, 700])
+def test_rows_behind_the_last_stay_in_every_step(T, monkeypatch):
+    """A step with padded tokens in buffers that hold a mark (NaN where a result must not read): rows from the count
+    on the device keep it in every buffer, and no result sees it."""
+    E, k, H, I = 5, 3, 256, 144
+    g = torch.Generator().manual_seed(T)
+    rand = lambda *s: torch.randn(s, generator=g).to(BF16).to(DEV)  # noqa: E731
+    x, dout, weights = rand(T, H), rand(T, H), torch.rand((T, k), generator=g).to(DEV)
+    topk = torch.randint(-1, E + 1, (T, k), generator=g).to(torch.int32).to(DEV)
+    mask = (torch.rand(T, generator=g) < 0.4).to(torch.uint8).to(DEV)
+    w8, ws = B.fp8_quantize_weight(rand(E, 2 * I, H) * 0.1)
+    d8, ds = B.fp8_quantize_weight(rand(E, H, I) * 0.1)
+
+    def step(fill):
+        made = []
+        empty = torch.empty
+
+        def filled(shape, dtype=None, device=None):
+            t = empty(shape, dtype=dtype, device=device)
+            t.view(torch.uint8).fill_(fill)
+            if t.dim() == 2 and t.shape[0] == T * k:
+                made.append(t)
+            return t
+
+        with monkeypatch.context() as m:
+            m.setattr(B.torch, "empty", filled)
+            m.setattr(B.torch, "empty_like", lambda t: filled(t.shape, t.dtype, t.device))
+            o = B.expert_order(topk, E, padding_mask=mask)
+            offsets, positions = o["expert_offsets"], o["positions"]
+            used = offsets[-1:]
+            rows = B.dispatch_forward(x, positions)
+            x8, xs = B.fp8_quantize_rows(rows, row_count=used)
+            h = B.fp8_grouped_linear(x8, xs, w8, ws, offsets)
+            act, kept = B.swiglu_forward(h, row_count=used)
+            a8, a_s = B.fp8_quantize_rows(act, row_count=used)
+            y = B.fp8_grouped_linear(a8, a_s, d8, ds, offsets)
+            out = B.combine_forward(y, positions, weights)
+            c = B.combine_backward(dout, positions, rows=y, weights=weights)
+            g8, gs = B.fp8_quantize_rows(c["drows"], row_count=used)
+            dact = B.fp8_grouped_input_grad(g8, gs, d8, ds, offsets)
+            s = B.swiglu_backward(dact, kept, row_count=used)
+            e8, es = B.fp8_quantize_rows(s["dh"], row_count=used)
+            drows = B.fp8_grouped_input_grad(e8, es, w8, ws, offsets)
+            dx = B.dispatch_backward(drows, positions)["dx"]
+        return int(used), made, (out, c["dweights"], dx)
+
+    used, made, results = step(0xFF)          # NaN in every type
+    assert 0 < used < T * k and len(made) >= 12
+    for t in made:
+        assert bool((t[used:].view(torch.uint8) == 0xFF).all()), t.dtype
+    assert all(bool(t.isfinite().all()) for t in results)
+    for a, b in zip(results, step(0)[2]):
+        assert torch.equal(a, b)

@@ -20,7 +20,8 @@
 // rows.  Arithmetic in fp32 in the order of the slots, rounded once.  A wave takes 64
 // vectors of one token's row, so that up to eight rows' loads are on their way together.
 // 8192 tokens of 6144 bf16, top-8: spread of 7168 tokens 135 us (6.0 TB/s), gather of
-// 65536 rows 159 (5.7), weights' gradient with the rows written 325 (5.3).
+// 65536 rows 159 (5.7), weights' gradient with the rows written 325 (5.3), with the tokens'
+// 165 (6.1).
 #include <algorithm>
 
 #include "common.h"
@@ -305,7 +306,10 @@ __global__ __launch_bounds__(256) void gather_kernel(const MoveArgs a) {
 // workgroup.  SPREAD: also rows_out[p] = w x (where rows_out is given); otherwise
 // also token_out = sum w rows.  Sums over the lanes in a fixed order.
 // kMaxSlots: 8 or 32 (with 32 running sums a lane the fp32 gradients of 1001 x 1237,
-// top-2, took 27 us for both operators' kernels instead of 10).
+// top-2, took 27 us for both operators' kernels instead of 10).  With 32 and fp32 rows a
+// lane takes 236 to 243 registers and 96 to 128 of the matrix units', so a SIMD holds one wave:
+// 8192 tokens of 6144 fp32, top-16, take 3420 us with the rows written (1.9 TB/s) and 2450
+// with the tokens'; in bf16 645 (5.2) and 320 (5.7).
 template <typename TT, typename TR, int V, int G, int kMaxSlots, bool SPREAD>
 __global__ __launch_bounds__(256) void dweights_kernel(const MoveArgs a) {
     __shared__ float part[4][kMaxSlots];

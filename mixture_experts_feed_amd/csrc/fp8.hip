@@ -7,7 +7,8 @@
 // value, every midpoint of two and the numbers next to each of them, of both signs).  Half a
 // step is 2^-4 of a value from 2^-6 2^e on, and 2^-10 2^e below.  A block with an infinity or a NaN gets a NaN scale and zeros, so that
 // every product with it is NaN.  One read and one write: HBM bounds both kernels (8192
-// rows of 6144 bf16: 28 us, 5.4 TB/s).
+// rows of 6144: bf16 25 to 29 us, 5.2 to 6.0 TB/s, fp32 35; weights 32 x 4096 x 6144: bf16 449
+// us, 5.4 TB/s, fp32 720, 5.6).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

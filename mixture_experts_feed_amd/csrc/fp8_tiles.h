@@ -16,10 +16,12 @@
 // most 512 experts in LDS), so there is no plan, no workspace and nothing to clear.  A
 // XCD takes a contiguous range of tiles, an expert's row tiles innermost, so that the
 // workgroups that run side by side share weights and rows through its L2.
-// 8192 x 8192 x 8192: 515 us (2.13 PFLOP/s); 128 experts of 316 to 754 rows, 6144 x 4096:
-// 1840 to 1880 us, matrix units busy 46% of the cycles.  Beside the 2048 cycles that a
-// stage's products take on a SIMD's matrix unit stand 1024 for adding them by their
-// scales and 1536 of LDS reads; and the card lowers its clock to 1.7 to 1.9 GHz.
+// 8192 x 8192 x 8192: 515 to 545 us (2.0 to 2.1 PFLOP/s); 128 experts of 316 to 754 rows, 6144 x
+// 4096: 1800 to 1900 us, matrix units busy 46% of the cycles.  Beside the 2048 cycles that a
+// stage's products take on a SIMD's matrix unit stand 1024 for adding them by their scales
+// and 1536 of LDS reads; and the card lowers its clock to 1.7 to 1.9 GHz.  Results in fp32
+// (EXACT) take twice the time: 1052 to 1065 us (1.04 PFLOP/s) and 3700 to 3800, where the
+// conversions to bf16 stand beside the products.
 #pragma once
 
 #include "fp8_common.h"
